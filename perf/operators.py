@@ -10,7 +10,7 @@ alone and are the same for both.
 Packed 4-bit weights: W [N, K] holds whole numbers 0..15 and stands for
 (W - zero) * scale.  It is stored as uint8 [ceil(N/16), ceil(K/128), 1024]:
 a kilobyte covers 16 rows by 128 k, 32-bit word (g, n, j) of it (g = 0..3,
-n = 0..15, j = 0..3, in that order) covers row n, k = 32 g + 8 j .. + 7, with
+n = 0..15, j = 0..3, in that order) covers row n, k = 32 j + 8 g .. + 7, with
 k + 2p in its nibble p and k + 2p + 1 in its nibble p + 4 (p = 0..3).  What
 pads N and K is never read as a weight.  scales [ceil(K/group), N] are bf16,
 zeros [ceil(K/group), N] uint8 (absent: 8 everywhere).
@@ -137,7 +137,7 @@ def _codes(W, N, K):
     words = W.view(torch.int32).view(W.shape[0], W.shape[1], 4, 16, 4, 1)
     shifts = torch.tensor(NIBBLE_SHIFTS, dtype=torch.int32, device=W.device)
     codes = (words >> shifts) & 15
-    return codes.permute(0, 3, 1, 2, 4, 5).reshape(W.shape[0] * 16, W.shape[1] * 128)[:N, :K]
+    return codes.permute(0, 3, 1, 4, 2, 5).reshape(W.shape[0] * 16, W.shape[1] * 128)[:N, :K]
 
 
 def _epilogue(y, bias, kind):
@@ -254,7 +254,7 @@ def exact(case, seed):
         b = d["W"].reshape(-1, d["W"].shape[1], 4, 16, 4, 4)
         nib = torch.stack((b % 16, b // 16), dim=-1).flatten(-2)
         w = torch.empty((b.shape[0], 16, b.shape[1], 4, 4, 8), dtype=torch.float64, device="cuda")
-        nib = nib.permute(0, 3, 1, 2, 4, 5)
+        nib = nib.permute(0, 3, 1, 4, 2, 5)
         w[..., 0::2] = nib[..., :4]
         w[..., 1::2] = nib[..., 4:]
         w = w.reshape(b.shape[0] * 16, -1)[:N, :K]
