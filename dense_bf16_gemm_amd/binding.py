@@ -25,7 +25,8 @@ EXPORTS = (
     "mm_matmul", "mm_linear", "mm_ffn_swiglu", "mm_ffn_glu", "mm_set_config",
     "mm_describe_config", "mm_debug_schedule", "mm_status_string", "mm_last_error",
     "mm_workspace_size", "mm_matmul_ws", "mm_linear_ws", "mm_matmul_batched", "mm_linear_batched",
-    "mm_linear_preact", "mm_matmul_noalloc",
+    "mm_linear_preact", "mm_matmul_noalloc", "mm_rms_norm", "mm_rms_norm_q8", "mm_rms_norm_backward",
+    "mm_rms_norm_backward_workspace_size", "mm_w4_pack", "mm_linear_w4", "mm_linear_q8",
 )
 
 _lib = None
@@ -70,10 +71,19 @@ def open_library(path: str):
     lib.mm_describe_config.argtypes = [ci, i64, i64, i64, ci, ctypes.c_char_p, i64]
     lib.mm_debug_schedule.argtypes = [ci, i64, i64, i64, ci, i64, ctypes.POINTER(ctypes.c_int32), i64,
                                       ctypes.POINTER(ctypes.c_int64)]
+    cf = ctypes.c_float
+    lib.mm_rms_norm.argtypes = [vp, i64, vp, vp, vp, vp, vp, i64, i64, cf, ci, vp]
+    lib.mm_rms_norm_q8.argtypes = [vp, i64, vp, vp, vp, vp, vp, i64, i64, cf, ci, vp]
+    lib.mm_rms_norm_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, ci, vp, i64, vp]
+    lib.mm_rms_norm_backward_workspace_size.argtypes = [i64, i64, ctypes.POINTER(ctypes.c_int64)]
+    lib.mm_w4_pack.argtypes = [vp, vp, i64, i64, vp]
+    lib.mm_linear_w4.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, ci, vp]
+    lib.mm_linear_q8.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, ci, vp]
     for name in ("mm_matmul", "mm_linear", "mm_ffn_swiglu", "mm_ffn_glu", "mm_set_config",
                  "mm_describe_config", "mm_debug_schedule", "mm_workspace_size", "mm_matmul_ws",
                  "mm_linear_ws", "mm_matmul_batched", "mm_linear_batched", "mm_linear_preact",
-                 "mm_matmul_noalloc"):
+                 "mm_matmul_noalloc", "mm_rms_norm", "mm_rms_norm_q8", "mm_rms_norm_backward",
+                 "mm_rms_norm_backward_workspace_size", "mm_w4_pack", "mm_linear_w4", "mm_linear_q8"):
         getattr(lib, name).restype = ci
     lib.mm_status_string.argtypes = [ci]
     lib.mm_status_string.restype = ctypes.c_char_p
@@ -100,6 +110,14 @@ def workspace_size(form: str, M: int, N: int, K: int, layout: str = "nt") -> int
     n = ctypes.c_int64(0)
     check(load().mm_workspace_size(1 if form == "ffn" else 0, M, N, K, LAYOUTS[layout],
                                    ctypes.byref(n)), "mm_workspace_size")
+    return n.value
+
+
+def rms_norm_backward_workspace_size(rows: int, hidden: int) -> int:
+    """Bytes of workspace mm_rms_norm_backward needs on the current device."""
+    n = ctypes.c_int64(0)
+    check(load().mm_rms_norm_backward_workspace_size(rows, hidden, ctypes.byref(n)),
+          "mm_rms_norm_backward_workspace_size")
     return n.value
 
 

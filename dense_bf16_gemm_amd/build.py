@@ -3,7 +3,7 @@
     python -m dense_bf16_gemm_amd.build
 
 Compiler resource remarks (registers, spills, scratch, LDS per kernel) are
-kept in ``_build/resource_usage.txt`` next to this file.
+kept per source in ``_build/resource_usage*.txt`` next to this file.
 
 A second library, ``libmm_fullsync.so``, is built from the same sources with
 MM_DEBUG_FULL_SYNC: the slab kernel then drains every copy and waits at a
@@ -22,8 +22,9 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmm.so")
 LIB_FULLSYNC = os.path.join(HERE, "libmm_fullsync.so")
 BUILD_DIR = os.path.join(HERE, "_build")
-REMARKS = os.path.join(BUILD_DIR, "resource_usage.txt")
-SOURCES = ["mm_api.hip"]
+SOURCES = ["mm_api.hip", "mm_decoder.hip"]
+REMARKS = os.path.join(BUILD_DIR, "resource_usage.txt")  # mm_api.hip
+REMARKS_DECODER = os.path.join(BUILD_DIR, "resource_usage_decoder.txt")
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
@@ -31,7 +32,6 @@ HIPCC_FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     # no packed-fp32 instructions anywhere in the device code
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall",
@@ -45,38 +45,51 @@ def hipcc() -> str:
     return cand if os.path.exists(cand) else "hipcc"
 
 
-def _command(out: str, defines=()) -> list:
+def _compile(source: str, obj: str, defines=()) -> list:
     return [hipcc(), *HIPCC_FLAGS, *[f"-D{d}" for d in defines], "-I", os.path.join(ROOT, "include"),
-            "-o", out, *[os.path.join(CSRC, s) for s in SOURCES]]
+            "-c", "-o", obj, os.path.join(CSRC, source)]
+
+
+def _link(out: str, objs) -> list:
+    return [hipcc(), f"--offload-arch={ARCH}", "-shared", "-o", out, *objs]
 
 
 def build(verbose: bool = False) -> str:
-    """Builds libmm.so and the race-check libmm_fullsync.so (two hipcc runs
-    side by side); returns the path of libmm.so."""
+    """Builds libmm.so and the race-check libmm_fullsync.so (the hipcc runs of
+    every source side by side, then the two links); returns the path of
+    libmm.so.  Objects are linked in the order of SOURCES."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     jobs = []
     for lib, defines in ((LIB, ()), (LIB_FULLSYNC, ("MM_DEBUG_FULL_SYNC",))):
-        tmp = lib + ".tmp%d" % os.getpid()
-        cmd = _command(tmp, defines)
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        # compiler output to a file (a pipe could fill while the other job runs)
-        log = REMARKS if lib == LIB else os.path.join(BUILD_DIR, "fullsync_build.txt")
-        with open(log, "w") as f:
-            proc = subprocess.Popen(cmd, stdout=subprocess.DEVNULL, stderr=f)
-        jobs.append((lib, tmp, log, proc))
+        for source in SOURCES:
+            stem = os.path.splitext(source)[0] + ("" if lib == LIB else "_fullsync")
+            obj = os.path.join(BUILD_DIR, stem + ".o")
+            cmd = _compile(source, obj, defines)
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            # compiler output to a file (a pipe could fill while the other jobs run)
+            if lib == LIB:
+                log = REMARKS if source == "mm_api.hip" else REMARKS_DECODER
+            else:
+                log = os.path.join(BUILD_DIR, stem + "_build.txt")
+            with open(log, "w") as f:
+                proc = subprocess.Popen(cmd, stdout=subprocess.DEVNULL, stderr=f)
+            jobs.append((lib, source, obj, log, proc))
     failed = []
-    for lib, tmp, log, proc in jobs:
-        proc.wait()
-        with open(log) as f:
-            err = f.read()
-        if proc.returncode != 0:
-            errs = [ln for ln in err.splitlines() if "error" in ln]
-            failed.append(f"hipcc failed for {os.path.basename(lib)}:\n" + "\n".join(errs[:40]))
-        else:
-            os.replace(tmp, lib)
+    for lib, source, obj, log, proc in jobs:
+        if proc.wait() != 0:
+            with open(log) as f:
+                errs = [ln for ln in f.read().splitlines() if "error" in ln]
+            failed.append(f"hipcc failed for {source} ({os.path.basename(lib)}):\n" + "\n".join(errs[:40]))
     if failed:
         raise RuntimeError("\n".join(failed))
+    for lib in (LIB, LIB_FULLSYNC):
+        tmp = lib + ".tmp%d" % os.getpid()
+        cmd = _link(tmp, [obj for (of, _, obj, _, _) in jobs if of == lib])
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, lib)
     return LIB
 
 

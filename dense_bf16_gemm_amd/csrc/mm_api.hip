@@ -19,7 +19,7 @@
 #include <mutex>
 #include <string>
 
-#include "../../include/mm.h"
+#include "mm_host.hpp"
 #include "gemm_kernel.hpp"
 #include "gemm_nt_pipe.hpp"
 #include "gemm_pingpong.hpp"
@@ -39,7 +39,7 @@
 constexpr int64_t kScratchBytes = int64_t(64) << 20;
 static __device__ __align__(256) float scratch[kScratchBytes / 4];
 
-namespace {
+namespace mmh {
 
 thread_local std::string g_last_error;
 
@@ -47,6 +47,38 @@ mm_status fail(mm_status s, const std::string& msg) {
   g_last_error = msg;
   return s;
 }
+
+bool overlaps(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
+  if (!a || !b || abytes <= 0 || bbytes <= 0) return false;
+  const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
+  return a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
+}
+
+// device attributes, cached per device
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_cu_count[kMaxDevices];
+
+mm_status device_cus(int* cus) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return fail(MM_ERR_HIP, std::string("hipGetDevice: ") + hipGetErrorString(e));
+  if (dev < 0 || dev >= kMaxDevices) return fail(MM_ERR_UNSUPPORTED, "device index out of range");
+  int n = g_cu_count[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    e = hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev);
+    if (e != hipSuccess || n <= 0)
+      return fail(MM_ERR_HIP, std::string("hipDeviceGetAttribute: ") + hipGetErrorString(e));
+    g_cu_count[dev].store(n, std::memory_order_relaxed);
+  }
+  *cus = n;
+  return MM_OK;
+}
+
+}  // namespace mmh
+
+using namespace mmh;
+
+namespace {
 
 // ----------------------------------------------------------------------------
 // Kernel registry: every instantiated (tile, wave grid, layout, form).
@@ -300,8 +332,6 @@ void read_env_once() {
   });
 }
 
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 // The heuristic: the largest tile that still gives about a wave of work.
 // Band height 4: a wave of 256 workgroups puts 32 consecutive tiles of the
 // band order on each XCD, a 4 x 8 block (12 panels, as few as 8 x 4 reads);
@@ -376,28 +406,6 @@ bool k_alt_enabled(const Config& c, int64_t K) {
   return K * (int64_t)(c.bm + c.bn) * 2 > (int64_t)(2 << 20);
 }
 
-// ----------------------------------------------------------------------------
-// Device attributes (cached per device).
-// ----------------------------------------------------------------------------
-constexpr int kMaxDevices = 64;
-std::atomic<int> g_cu_count[kMaxDevices];
-
-mm_status device_cus(int* cus) {
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return fail(MM_ERR_HIP, std::string("hipGetDevice: ") + hipGetErrorString(e));
-  if (dev < 0 || dev >= kMaxDevices) return fail(MM_ERR_UNSUPPORTED, "device index out of range");
-  int n = g_cu_count[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    e = hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev);
-    if (e != hipSuccess || n <= 0)
-      return fail(MM_ERR_HIP, std::string("hipDeviceGetAttribute: ") + hipGetErrorString(e));
-    g_cu_count[dev].store(n, std::memory_order_relaxed);
-  }
-  *cus = n;
-  return MM_OK;
-}
-
 // Device address of the static scratch on the current device, taken once per
 // device with that device current (each GPU holds its own copy of the array
 // at its own address).
@@ -456,14 +464,6 @@ struct Request {
   void* out_pre = nullptr;  // second output: the pre-activation (GELU epilogues)
   bool static_ws = false;   // ws is the library's static scratch (mm_matmul_noalloc)
 };
-
-bool overlaps(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
-  if (!a || !b || abytes <= 0 || bbytes <= 0) return false;
-  const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-  return a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
-}
-
-bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
 mm_status validate(const Request& r) {
   if (r.M < 0 || r.N < 0 || r.K < 0) return fail(MM_ERR_INVALID_VALUE, "negative size");

@@ -1,0 +1,350 @@
+// mm_decoder.hip -- C ABI of the decoder-layer operators (declared in
+// include/mm.h): the residual addition with its RMS norm and gradient, and
+// the products with 4-bit and 8-bit weights.  Argument checks, the choice of
+// a kernel's shape, launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "mm_host.hpp"
+#include "rms_norm.hpp"
+#include "gemm_w4.hpp"
+#include "gemm_q8.hpp"
+
+using namespace mmh;
+
+namespace {
+
+constexpr int64_t kLimit = int64_t(1) << 31;
+
+mm_status launch(const void* kernel, dim3 grid, int threads, void** args, void* stream, const char* what) {
+  const hipError_t e = hipLaunchKernel(kernel, grid, dim3(threads), args, 0, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess)
+    return fail(MM_ERR_HIP, std::string("hipLaunchKernel (") + what + "): " + hipGetErrorString(e));
+  return MM_OK;
+}
+
+template <typename F>
+const void* fn(F* kernel) {
+  return reinterpret_cast<const void*>(kernel);
+}
+
+// ----------------------------------------------------------------------------
+// RMS norm
+// ----------------------------------------------------------------------------
+mm_status check_norm_sizes(int64_t rows, int64_t hidden, mm_out_dtype dtype) {
+  if (rows < 0 || hidden < 0) return fail(MM_ERR_INVALID_VALUE, "negative size");
+  if (dtype != MM_OUT_BF16 && dtype != MM_OUT_F32) return fail(MM_ERR_INVALID_VALUE, "bad stream type");
+  if (rows >= kLimit) return fail(MM_ERR_UNSUPPORTED, "rows must be below 2^31");
+  if (hidden > mmk::kNormMaxHidden) return fail(MM_ERR_UNSUPPORTED, "hidden must be at most 32768");
+  if (hidden % 8 != 0) return fail(MM_ERR_MISALIGNED, "hidden must be a multiple of 8 elements");
+  return MM_OK;
+}
+
+// Threads per row and vectors of 8 per thread (1, 2 or 4).
+void norm_shape(int64_t hidden, int64_t threads_wanted, int* threads, int* vpt) {
+  const int64_t vectors = hidden / 8;
+  int v = 1;
+  while (v < 4 && threads_wanted * v < vectors) v *= 2;
+  *vpt = v;
+  *threads = (int)(cdiv(cdiv(vectors, v), 64) * 64);
+}
+
+template <bool F32, bool Q8>
+const void* norm_kernel(int vpt) {
+  switch (vpt) {
+    case 1: return fn(&mmk::rms_norm<F32, Q8, 1>);
+    case 2: return fn(&mmk::rms_norm<F32, Q8, 2>);
+  }
+  return fn(&mmk::rms_norm<F32, Q8, 4>);
+}
+
+template <bool F32>
+const void* norm_grad_kernel(int vpt) {
+  switch (vpt) {
+    case 1: return fn(&mmk::rms_norm_grad<F32, 1>);
+    case 2: return fn(&mmk::rms_norm_grad<F32, 2>);
+  }
+  return fn(&mmk::rms_norm_grad<F32, 4>);
+}
+
+mm_status norm(const void* x, int64_t ld_x, const void* residual, const void* weight, void* h, void* y, float* stat,
+               int64_t rows, int64_t hidden, float eps, mm_out_dtype dtype, bool q8, void* stream) {
+  mm_status s = check_norm_sizes(rows, hidden, dtype);
+  if (s != MM_OK) return s;
+  if (!(eps >= 0.0f)) return fail(MM_ERR_INVALID_VALUE, "eps must not be negative");
+  if (rows == 0 || hidden == 0) return MM_OK;
+  if (!x || !weight || !y || !stat || (residual && !h)) return fail(MM_ERR_INVALID_VALUE, "null pointer");
+  if (ld_x < hidden || ld_x >= kLimit) return fail(MM_ERR_INVALID_VALUE, "rows of x must not overlap (ld_x < hidden)");
+  if (ld_x % 8 != 0) return fail(MM_ERR_MISALIGNED, "ld_x must be a multiple of 8 elements");
+  if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(y, 16) || !aligned(stat, 4) ||
+      (residual && (!aligned(residual, 16) || !aligned(h, 16))))
+    return fail(MM_ERR_MISALIGNED, "pointers must be 16-byte aligned");
+  const int64_t e = dtype == MM_OUT_F32 ? 4 : 2;
+  const int64_t xb = ((rows - 1) * ld_x + hidden) * e, hb = rows * hidden * e;
+  const int64_t yb = rows * hidden * (q8 ? 1 : 2), sb = rows * 4, wb = hidden * 2;
+  const struct { const void* p; int64_t n; } in[] = {{x, xb}, {residual, hb}, {weight, wb}};
+  const struct { const void* p; int64_t n; } out[] = {{residual ? h : nullptr, hb}, {y, yb}, {stat, sb}};
+  for (int o = 0; o < 3; ++o) {
+    for (int i = 0; i < 3; ++i) {
+      // h may be residual itself, or x (a contiguous one): each element is
+      // read before it is written, by one thread
+      if (o == 0 && ((i == 1 && h == residual) || (i == 0 && h == x && ld_x == hidden))) continue;
+      if (overlaps(out[o].p, out[o].n, in[i].p, in[i].n))
+        return fail(MM_ERR_INVALID_VALUE, "an output overlaps an input");
+    }
+    for (int q = 0; q < o; ++q)
+      if (overlaps(out[o].p, out[o].n, out[q].p, out[q].n)) return fail(MM_ERR_INVALID_VALUE, "outputs overlap");
+  }
+  mmk::RmsNormParams p;
+  p.x = x;
+  p.residual = residual;
+  p.weight = static_cast<const uint16_t*>(weight);
+  p.h = h;
+  p.y = y;
+  p.stat = stat;
+  p.rows = rows;
+  p.ld_x = ld_x;
+  p.hidden = (int)hidden;
+  p.eps = eps;
+  int threads, vpt;
+  norm_shape(hidden, rows <= 256 ? 1024 : 256, &threads, &vpt);
+  void* args[] = {&p};
+  const void* k = dtype == MM_OUT_F32 ? (q8 ? norm_kernel<true, true>(vpt) : norm_kernel<true, false>(vpt))
+                                      : (q8 ? norm_kernel<false, true>(vpt) : norm_kernel<false, false>(vpt));
+  return launch(k, dim3((unsigned)rows), threads, args, stream, "rms_norm");
+}
+
+mm_status norm_grad_parts(int64_t rows, int64_t* parts) {
+  int cus = 0;
+  const mm_status s = device_cus(&cus);
+  *parts = std::min<int64_t>(rows, 4 * (int64_t)cus);
+  return s;
+}
+
+// ----------------------------------------------------------------------------
+// Products with 4-bit and 8-bit weights
+// ----------------------------------------------------------------------------
+bool map_epilogue(mm_epilogue e, int* epi) {
+  switch (e) {
+    case MM_EPI_NONE: *epi = mmk::EPI_NONE; return true;
+    case MM_EPI_BIAS: *epi = mmk::EPI_BIAS; return true;
+    case MM_EPI_GELU_TANH: *epi = mmk::EPI_GELU; return true;
+    case MM_EPI_BIAS_GELU_TANH: *epi = mmk::EPI_BIAS_GELU; return true;
+  }
+  return false;
+}
+
+mm_status check_product(int64_t M, int64_t N, int64_t K, const void* bias, const void* out, mm_epilogue epi_in,
+                        int* epi) {
+  if (M < 0 || N < 0 || K < 0) return fail(MM_ERR_INVALID_VALUE, "negative size");
+  if (M >= kLimit || N >= kLimit || K >= kLimit) return fail(MM_ERR_UNSUPPORTED, "M, N and K must be below 2^31");
+  if (!map_epilogue(epi_in, epi)) return fail(MM_ERR_INVALID_VALUE, "bad epilogue");
+  if (M == 0 || N == 0) return MM_OK;
+  if (!out) return fail(MM_ERR_INVALID_VALUE, "null output pointer");
+  if (!aligned(out, 2)) return fail(MM_ERR_MISALIGNED, "out must be aligned to its element size");
+  const bool need_bias = *epi == mmk::EPI_BIAS || *epi == mmk::EPI_BIAS_GELU;
+  if (need_bias && !bias) return fail(MM_ERR_INVALID_VALUE, "epilogue needs a bias");
+  if (need_bias && !aligned(bias, 2)) return fail(MM_ERR_MISALIGNED, "bias must be 2-byte aligned");
+  const int64_t room = int64_t(1) << 60;
+  if (M * K > room || N * K > room || M * N > room)
+    return fail(MM_ERR_UNSUPPORTED, "an operand or the output spans 2^60 elements or more");
+  if (need_bias && overlaps(out, M * N * 2, bias, N * 2))
+    return fail(MM_ERR_INVALID_VALUE, "out overlaps an input");
+  return MM_OK;
+}
+
+template <int MB, int NB>
+const void* w4_kernel(int group) {
+  switch (group) {
+    case 32: return fn(&mmk::gemm_w4<MB, NB, 32>);
+    case 64: return fn(&mmk::gemm_w4<MB, NB, 64>);
+  }
+  return fn(&mmk::gemm_w4<MB, NB, 128>);
+}
+
+}  // namespace
+
+extern "C" {
+
+mm_status mm_rms_norm(const void* x, int64_t ld_x, const void* residual, const void* weight, void* h, void* y,
+                      float* rstd, int64_t rows, int64_t hidden, float eps, mm_out_dtype stream_dtype, void* stream) {
+  return norm(x, ld_x, residual, weight, h, y, rstd, rows, hidden, eps, stream_dtype, false, stream);
+}
+
+mm_status mm_rms_norm_q8(const void* x, int64_t ld_x, const void* residual, const void* weight, void* h, void* q,
+                         float* scale, int64_t rows, int64_t hidden, float eps, mm_out_dtype stream_dtype,
+                         void* stream) {
+  return norm(x, ld_x, residual, weight, h, q, scale, rows, hidden, eps, stream_dtype, true, stream);
+}
+
+mm_status mm_rms_norm_backward_workspace_size(int64_t rows, int64_t hidden, int64_t* bytes) {
+  if (!bytes) return fail(MM_ERR_INVALID_VALUE, "null bytes pointer");
+  *bytes = 0;
+  mm_status s = check_norm_sizes(rows, hidden, MM_OUT_BF16);
+  if (s != MM_OK || rows == 0 || hidden == 0) return s;
+  int64_t parts = 0;
+  if ((s = norm_grad_parts(rows, &parts)) != MM_OK) return s;
+  *bytes = parts * hidden * 4;
+  return MM_OK;
+}
+
+mm_status mm_rms_norm_backward(const void* dy, const void* h, const void* weight, const float* rstd, const void* dres,
+                               void* dh, float* dweight, int64_t rows, int64_t hidden, mm_out_dtype stream_dtype,
+                               void* workspace, int64_t workspace_bytes, void* stream) {
+  mm_status s = check_norm_sizes(rows, hidden, stream_dtype);
+  if (s != MM_OK) return s;
+  if (hidden == 0) return MM_OK;
+  if (!dweight || (rows > 0 && (!dy || !h || !weight || !rstd || !dh || !workspace)))
+    return fail(MM_ERR_INVALID_VALUE, "null pointer");
+  if (!aligned(dweight, 16) || (rows > 0 && (!aligned(dy, 16) || !aligned(h, 16) || !aligned(weight, 16) ||
+                                             !aligned(rstd, 4) || !aligned(dres, 16) || !aligned(dh, 16) ||
+                                             !aligned(workspace, 16))))
+    return fail(MM_ERR_MISALIGNED, "pointers must be 16-byte aligned");
+  const int64_t e = stream_dtype == MM_OUT_F32 ? 4 : 2, n = rows * hidden;
+  if (workspace_bytes < 0) return fail(MM_ERR_INVALID_VALUE, "negative workspace size");
+  if (rows > 0) {
+    const struct { const void* p; int64_t n; } in[] = {{dy, n * 2}, {h, n * e}, {dres, n * e}, {weight, hidden * 2},
+                                                       {rstd, rows * 4}};
+    const struct { const void* p; int64_t n; } out[] = {{dh, n * e}, {dweight, hidden * 4},
+                                                        {workspace, workspace_bytes}};
+    for (int o = 0; o < 3; ++o) {
+      for (int i = 0; i < 5; ++i) {
+        if (o == 0 && i == 2 && dh == dres) continue;  // in place: read before written, by one thread
+        if (overlaps(out[o].p, out[o].n, in[i].p, in[i].n))
+          return fail(MM_ERR_INVALID_VALUE, "an output or the workspace overlaps an input");
+      }
+      for (int q = 0; q < o; ++q)
+        if (overlaps(out[o].p, out[o].n, out[q].p, out[q].n))
+          return fail(MM_ERR_INVALID_VALUE, "outputs or the workspace overlap");
+    }
+  }
+  int64_t parts = 0;
+  if (rows > 0) {
+    if ((s = norm_grad_parts(rows, &parts)) != MM_OK) return s;
+    if (workspace_bytes < parts * hidden * 4)
+      return fail(MM_ERR_INVALID_VALUE, "workspace smaller than mm_rms_norm_backward_workspace_size reports");
+    mmk::RmsNormGradParams p;
+    p.dy = static_cast<const uint16_t*>(dy);
+    p.h = h;
+    p.dres = dres;
+    p.weight = static_cast<const uint16_t*>(weight);
+    p.rstd = rstd;
+    p.dh = dh;
+    p.part = static_cast<float*>(workspace);
+    p.rows = rows;
+    p.hidden = (int)hidden;
+    int threads, vpt;
+    norm_shape(hidden, 256, &threads, &vpt);
+    void* args[] = {&p};
+    s = launch(stream_dtype == MM_OUT_F32 ? norm_grad_kernel<true>(vpt) : norm_grad_kernel<false>(vpt),
+               dim3((unsigned)parts), threads, args, stream, "rms_norm gradient");
+    if (s != MM_OK) return s;
+  }
+  const float* part = static_cast<const float*>(workspace);
+  int nparts = (int)parts, hid = (int)hidden;
+  void* args[] = {&part, &dweight, &nparts, &hid};
+  return launch(fn(&mmk::rms_norm_dweight), dim3((unsigned)cdiv(hidden, 32)), 256, args, stream,
+                "rms_norm weight gradient");
+}
+
+mm_status mm_w4_pack(const void* codes, void* packed, int64_t N, int64_t K, void* stream) {
+  if (N < 0 || K < 0) return fail(MM_ERR_INVALID_VALUE, "negative size");
+  if (N >= kLimit || K >= kLimit) return fail(MM_ERR_UNSUPPORTED, "N and K must be below 2^31");
+  if (N == 0 || K == 0) return MM_OK;
+  if (!codes || !packed) return fail(MM_ERR_INVALID_VALUE, "null pointer");
+  if (!aligned(packed, 16)) return fail(MM_ERR_MISALIGNED, "packed must be 16-byte aligned");
+  if (cdiv(N, 16) * cdiv(K, 128) >= kLimit) return fail(MM_ERR_UNSUPPORTED, "more than 2^31 packed kilobytes");
+  int64_t words = cdiv(N, 16) * cdiv(K, 128) * 256;
+  if (overlaps(packed, words * 4, codes, N * K)) return fail(MM_ERR_INVALID_VALUE, "packed overlaps codes");
+  const uint8_t* c = static_cast<const uint8_t*>(codes);
+  uint32_t* w = static_cast<uint32_t*>(packed);
+  int n = (int)N, k = (int)K;
+  void* args[] = {&c, &w, &n, &k, &words};
+  return launch(fn(&mmk::w4_pack), dim3((unsigned)(words / 256)), 256, args, stream, "w4_pack");
+}
+
+mm_status mm_linear_w4(const void* x, const void* W, const void* scales, const void* zeros, const void* bias,
+                       void* out, int64_t M, int64_t N, int64_t K, int64_t group, mm_epilogue epilogue, void* stream) {
+  int epi = 0;
+  mm_status s = check_product(M, N, K, bias, out, epilogue, &epi);
+  if (s != MM_OK) return s;
+  if (group != 32 && group != 64 && group != 128)
+    return fail(MM_ERR_UNSUPPORTED, "group must be 32, 64 or 128");
+  if (M == 0 || N == 0) return MM_OK;
+  if (K > 0) {
+    if (!x || !W || !scales) return fail(MM_ERR_INVALID_VALUE, "null operand pointer");
+    if (!aligned(x, 16) || !aligned(W, 16)) return fail(MM_ERR_MISALIGNED, "x and W must be 16-byte aligned");
+    if (!aligned(scales, 2)) return fail(MM_ERR_MISALIGNED, "scales must be 2-byte aligned");
+    if (K % 8 != 0) return fail(MM_ERR_MISALIGNED, "K must be a multiple of 8 elements");
+    const int64_t ob = M * N * 2, groups = cdiv(K, group);
+    if (overlaps(out, ob, x, M * K * 2) || overlaps(out, ob, W, cdiv(N, 16) * cdiv(K, 128) * 1024) ||
+        overlaps(out, ob, scales, groups * N * 2) || overlaps(out, ob, zeros, groups * N))
+      return fail(MM_ERR_INVALID_VALUE, "out overlaps an input");
+  }
+  mmk::W4Params p;
+  p.x = static_cast<const uint16_t*>(x);
+  p.W = static_cast<const mmk::u32x4*>(W);
+  p.scales = static_cast<const uint16_t*>(scales);
+  p.zeros = static_cast<const uint8_t*>(zeros);
+  p.bias = static_cast<const uint16_t*>(bias);
+  p.out = static_cast<uint16_t*>(out);
+  p.M = (int)M;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.group = (int)group;
+  p.epi = epi;
+  const int mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+  const int nb = mb == 4 ? 2 : 4;
+  const void* k = mb == 1 ? w4_kernel<1, 4>((int)group) : mb == 2 ? w4_kernel<2, 4>((int)group) : w4_kernel<4, 2>((int)group);
+  const int64_t gy = cdiv(M, 16 * mb);
+  if (gy > 65535) return fail(MM_ERR_UNSUPPORTED, "M too large");
+  void* args[] = {&p};
+  return launch(k, dim3((unsigned)cdiv(N, 16 * nb), (unsigned)gy), mmk::kW4Waves * 64, args, stream, "linear_w4");
+}
+
+mm_status mm_linear_q8(const void* x, const float* x_scale, const void* W, const float* w_scale, const void* bias,
+                       void* out, int64_t M, int64_t N, int64_t K, mm_epilogue epilogue, void* stream) {
+  int epi = 0;
+  mm_status s = check_product(M, N, K, bias, out, epilogue, &epi);
+  if (s != MM_OK) return s;
+  if (M == 0 || N == 0) return MM_OK;
+  if (!x_scale || !w_scale) return fail(MM_ERR_INVALID_VALUE, "null scale pointer");
+  if (!aligned(x_scale, 4) || !aligned(w_scale, 4)) return fail(MM_ERR_MISALIGNED, "scales must be 4-byte aligned");
+  const int64_t ob = M * N * 2;
+  if (overlaps(out, ob, x_scale, M * 4) || overlaps(out, ob, w_scale, N * 4))
+    return fail(MM_ERR_INVALID_VALUE, "out overlaps an input");
+  if (K > 0) {
+    if (!x || !W) return fail(MM_ERR_INVALID_VALUE, "null operand pointer");
+    if (!aligned(x, 16) || !aligned(W, 16)) return fail(MM_ERR_MISALIGNED, "x and W must be 16-byte aligned");
+    if (K % 16 != 0) return fail(MM_ERR_MISALIGNED, "K must be a multiple of 16 elements");
+    if (K > (int64_t(1) << 22)) return fail(MM_ERR_UNSUPPORTED, "K must be at most 2^22");
+    if (overlaps(out, ob, x, M * K) || overlaps(out, ob, W, N * K))
+      return fail(MM_ERR_INVALID_VALUE, "out overlaps an input");
+  }
+  mmk::Q8Params p;
+  p.x = static_cast<const uint8_t*>(x);
+  p.xs = x_scale;
+  p.W = static_cast<const uint8_t*>(W);
+  p.ws = w_scale;
+  p.bias = static_cast<const uint16_t*>(bias);
+  p.out = static_cast<uint16_t*>(out);
+  p.M = (int)M;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.epi = epi;
+  void* args[] = {&p};
+  if (M <= 64) {
+    const int mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+    const int nb = mb == 4 ? 2 : 4;
+    const void* k = mb == 1 ? fn(&mmk::gemm_q8_rows<1, 4>) : mb == 2 ? fn(&mmk::gemm_q8_rows<2, 4>) : fn(&mmk::gemm_q8_rows<4, 2>);
+    return launch(k, dim3((unsigned)cdiv(N, 16 * nb)), mmk::kW4Waves * 64, args, stream, "linear_q8 rows");
+  }
+  const int64_t tm = cdiv(M, 128), tn = cdiv(N, 128);
+  if (tm * tn >= kLimit) return fail(MM_ERR_UNSUPPORTED, "more than 2^31 output tiles");
+  p.tiles_m = (int)tm;
+  p.tiles_n = (int)tn;
+  return launch(fn(&mmk::gemm_q8_tile), dim3((unsigned)(tm * tn)), 256, args, stream, "linear_q8 tiles");
+}
+
+}  // extern "C"

@@ -1,0 +1,59 @@
+// mm_device.hpp -- what the kernels share: vector types, epilogue codes, the
+// persistent tile order and the activation.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mmk {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Epilogue codes (kernel-internal; the C ABI maps onto them).
+enum : int {
+  EPI_NONE = 0,
+  EPI_BIAS = 1,
+  EPI_GELU = 2,
+  EPI_BIAS_GELU = 3,
+  EPI_SWIGLU = 4,
+  EPI_GLU_ID = 5
+};
+
+constexpr int kNumXcd = 8;       // MI355X: 8 accelerator dies, round-robin dispatch
+
+// Schedule helpers, shared with the host so that it can describe the order.
+__host__ __device__ inline int remap_workgroup(int b, int G, int on) {
+  if (!on || G < kNumXcd) return b;
+  const int per = G / kNumXcd, rem = G % kNumXcd;
+  const int xcd = b % kNumXcd, local = b / kNumXcd;
+  return xcd < rem ? xcd * (per + 1) + local : rem * (per + 1) + (xcd - rem) * per + local;
+}
+
+__host__ __device__ inline void tile_coords(int t, int tiles_m, int tiles_n, int group_m, int* tm,
+                                            int* tn) {
+  const int band = group_m * tiles_n;
+  const int g = t / band;
+  const int first_m = g * group_m;
+  const int rows = (tiles_m - first_m) < group_m ? (tiles_m - first_m) : group_m;
+  const int r = t - g * band;
+  *tm = first_m + r % rows;
+  *tn = r / rows;
+}
+
+__device__ __forceinline__ float gelu_tanh(float t) {
+  // 0.5 t (1 + tanh z) == t / (1 + exp(-2 z)),  z = sqrt(2/pi) (t + 0.044715 t^3)
+  const float z = 0.7978845608028654f * (t + 0.044715f * t * t * t);
+  return t * __builtin_amdgcn_rcpf(1.0f + __expf(-2.0f * z));
+}
+
+// Two floats to a packed pair of bf16 (round to nearest even), low half
+// first: one v_cvt_pk_bf16_f32 through a two-element vector conversion.
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{lo, hi}, bf16x2_t));
+}
+
+}  // namespace mmk

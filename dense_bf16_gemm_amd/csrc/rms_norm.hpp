@@ -1,0 +1,295 @@
+// Residual addition and root-mean-square norm of a decoder layer's stream,
+// with a bf16 or an 8-bit output, and its gradient.
+//
+//   h = T(x + residual)            T: the stream's type (bf16 or fp32)
+//   r = 1 / sqrt(mean(h^2) + eps)  fp32, from h as stored
+//   y = h r w                      w: bf16 weight
+//   bf16 output: y, rounded once.  8-bit output: s = max(max|y| / 448, 2^-126),
+//   q = e4m3(y / s): a row's largest value lands on e4m3's largest.
+//
+// One pass over memory: a row lives in its workgroup's registers between the
+// sum of squares, the maximum and the output.  Bound by HBM: 7 bytes per
+// element (bf16 stream, residual, 8-bit output).
+#pragma once
+
+#include "mm_device.hpp"
+
+namespace mmk {
+
+constexpr int kNormMaxHidden = 32768;  // 1024 threads x 4 vectors of 8
+
+struct RmsNormParams {
+  const void* x;           // [rows][ld_x]
+  const void* residual;    // [rows][hidden] or null
+  const uint16_t* weight;  // [hidden] bf16
+  void* h;                 // [rows][hidden], written when residual is given
+  void* y;                 // [rows][hidden] bf16 or e4m3
+  float* stat;             // [rows]: r (bf16 output) or s (8-bit output)
+  int64_t rows, ld_x;
+  int hidden;
+  float eps;
+};
+
+struct RmsNormGradParams {
+  const uint16_t* dy;      // [rows][hidden] bf16
+  const void* h;           // [rows][hidden]
+  const void* dres;        // [rows][hidden] or null: the gradient that reached h past the norm
+  const uint16_t* weight;
+  const float* rstd;       // [rows]
+  void* dh;                // [rows][hidden]
+  float* part;             // [gridDim.x][hidden] sums over each workgroup's rows
+  int64_t rows;
+  int hidden;
+};
+
+// Eight consecutive values as stored: 16 bytes of bf16 or 32 of fp32.
+template <bool F32>
+struct Raw8 {
+  u32x4 w[F32 ? 2 : 1];
+  // (16-byte aligned rows)
+  __device__ __forceinline__ void load(const void* base, int64_t i) {
+    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(base) + i * (F32 ? 4 : 2));
+    w[0] = p[0];
+    if constexpr (F32) w[1] = p[1];
+  }
+  __device__ __forceinline__ void clear() {
+    w[0] = u32x4{0u, 0u, 0u, 0u};
+    if constexpr (F32) w[1] = w[0];
+  }
+  __device__ __forceinline__ float operator[](int j) const {
+    // (through a scalar: a bit cast of a vector's element takes element 0)
+    uint32_t b;
+    if constexpr (F32)
+      b = w[j >> 2][j & 3];
+    else
+      b = j & 1 ? w[0][j >> 1] & 0xffff0000u : w[0][j >> 1] << 16;
+    return __builtin_bit_cast(float, b);
+  }
+};
+
+template <bool F32>
+__device__ __forceinline__ void load8(const void* base, int64_t i, float (&v)[8]) {
+  Raw8<F32> r;
+  r.load(base, i);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = r[j];
+}
+
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
+  return u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+}
+
+template <bool F32>
+__device__ __forceinline__ void store8(void* base, int64_t i, const float (&v)[8]) {
+  if constexpr (F32) {
+    f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(base) + i);
+    p[0] = f32x4{v[0], v[1], v[2], v[3]};
+    p[1] = f32x4{v[4], v[5], v[6], v[7]};
+  } else {
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + i) = pack8(v);
+  }
+}
+
+// Sum and maximum over a workgroup, the same in every thread.  The waves'
+// parts meet in LDS and are added in wave order, so results do not depend on
+// timing.  `slot` holds one value per wave and is not reused within a row.
+__device__ __forceinline__ float block_sum(float v, float* slot) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  const int waves = blockDim.x >> 6;
+  if (waves == 1) return v;
+  if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = 0.f;
+  for (int w = 0; w < waves; ++w) v += slot[w];
+  return v;
+}
+// (of the bit patterns of non-negative floats: they order as unsigned
+// numbers, and a NaN lies above infinity, so it is kept)
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* slot) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
+  const int waves = blockDim.x >> 6;
+  if (waves == 1) return v;
+  if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = 0u;
+  for (int w = 0; w < waves; ++w) v = max(v, slot[w]);
+  return v;
+}
+
+// One row per workgroup; thread t holds vectors t, t + T, ... (VPT of them)
+// of 8 values.
+template <bool F32, bool Q8, int VPT>
+__global__ void __launch_bounds__(1024) rms_norm(RmsNormParams p) {
+  __shared__ float slot_sum[16];
+  __shared__ uint32_t slot_max[16];
+  const int64_t row = blockIdx.x;
+  const int T = blockDim.x;
+  const int vectors = p.hidden >> 3;
+  float v[VPT][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = threadIdx.x + i * T;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    if (c < vectors) {
+      load8<F32>(p.x, row * p.ld_x + 8 * c, v[i]);
+      if (p.residual) {
+        float r[8];
+        load8<F32>(p.residual, row * p.hidden + 8 * c, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[i][j] += r[j];
+          // the norm is of h as the stream stores it
+          if constexpr (!F32) v[i][j] = static_cast<float>(static_cast<__bf16>(v[i][j]));
+        }
+        store8<F32>(p.h, row * p.hidden + 8 * c, v[i]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(v[i][j], v[i][j], ss);
+  }
+  ss = block_sum(ss, slot_sum);
+  const float rstd = 1.0f / sqrtf(ss / (float)p.hidden + p.eps);
+  uint32_t top = 0u;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = threadIdx.x + i * T;
+    if (c >= vectors) continue;
+    float w[8];
+    load8<false>(p.weight, 8 * c, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[i][j] = v[i][j] * rstd * w[j];
+      if constexpr (Q8) top = max(top, __builtin_bit_cast(uint32_t, v[i][j]) & 0x7fffffffu);
+    }
+    if constexpr (!Q8) *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.y) + row * p.hidden + 8 * c) = pack8(v[i]);
+  }
+  if constexpr (Q8) {
+    top = block_max(top, slot_max);
+    float s = __builtin_bit_cast(float, top) / 448.0f;
+    s = s < 0x1p-126f ? 0x1p-126f : s;  // (a NaN stays)
+    const float inv = 1.0f / s;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = threadIdx.x + i * T;
+      if (c >= vectors) continue;
+      int lo = 0, hi = 0;
+      lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[i][0] * inv, v[i][1] * inv, lo, false);
+      lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[i][2] * inv, v[i][3] * inv, lo, true);
+      hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[i][4] * inv, v[i][5] * inv, hi, false);
+      hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[i][6] * inv, v[i][7] * inv, hi, true);
+      reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + row * p.hidden)[c] = uint2{(uint32_t)lo, (uint32_t)hi};
+    }
+    if (threadIdx.x == 0) p.stat[row] = s;
+  } else {
+    if (threadIdx.x == 0) p.stat[row] = rstd;
+  }
+}
+
+// The gradient.  With n = h r and g = dy w:
+//   dh = r (g - n mean(g n)) + dres,   dw = sum over rows of dy n.
+// A workgroup takes rows b, b + G, ...; each thread keeps the same columns
+// for every row, so its part of dw stays in registers (fp32) and is written
+// once; rms_norm_dweight adds the workgroups' parts in order.
+//
+// A row's vectors are held as stored and widened where they are used, which
+// keeps four vectors per thread within the 128 registers of 1024 threads.
+template <bool F32, int VPT>
+__global__ void __launch_bounds__(1024) rms_norm_grad(RmsNormGradParams p) {
+  __shared__ float slot[2][16];
+  const int T = blockDim.x;
+  const int vectors = p.hidden >> 3;
+  const float inv_n = 1.0f / (float)p.hidden;
+  Raw8<false> w[VPT];
+  float dw[VPT][8];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = threadIdx.x + i * T;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+    w[i].clear();
+    if (c < vectors) w[i].load(p.weight, 8 * c);
+  }
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const float r = p.rstd[row];
+    Raw8<F32> h[VPT];
+    Raw8<false> dy[VPT];
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) asm volatile("" : "+v"(w[i].w[0]));  // (widened here, not once before the loop)
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = threadIdx.x + i * T;
+      h[i].clear();
+      dy[i].clear();
+      if (c < vectors) {
+        h[i].load(p.h, row * p.hidden + 8 * c);
+        dy[i].load(p.dy, row * p.hidden + 8 * c);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float t = dy[i][j] * (h[i][j] * r);
+        dw[i][j] += t;
+        dot = __builtin_fmaf(t, w[i][j], dot);
+      }
+    }
+    // two slot rows in turn: a wave may start the next row's sum while
+    // another still reads this one's
+    const float mean = block_sum(dot, slot[turn]) * inv_n;
+    turn ^= 1;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = threadIdx.x + i * T;
+      if (c >= vectors) continue;
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = r * (dy[i][j] * w[i][j] - h[i][j] * r * mean);
+      if (p.dres) {
+        float d[8];
+        load8<F32>(p.dres, row * p.hidden + 8 * c, d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] += d[j];
+      }
+      store8<F32>(p.dh, row * p.hidden + 8 * c, o);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = threadIdx.x + i * T;
+    if (c < vectors) store8<true>(p.part, (int64_t)blockIdx.x * p.hidden + 8 * c, dw[i]);
+  }
+}
+
+// dw[c] = sum over b of part[b][c]: 32 columns per workgroup (8 lanes of four)
+// by 32 interleaved runs of b, joined in LDS in a fixed order.
+__global__ void __launch_bounds__(256) rms_norm_dweight(const float* part, float* dw, int parts, int hidden) {
+  __shared__ f32x4 slot[32][8];
+  const int lane = threadIdx.x & 7, run = threadIdx.x >> 3;
+  const int c = blockIdx.x * 32 + 4 * lane;
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  if (c < hidden) {
+    for (int b = run; b < parts; b += 32) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(part + (int64_t)b * hidden + c);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[j] += v[j];
+    }
+  }
+  slot[run][lane] = s;
+  __syncthreads();
+  if (run == 0 && c < hidden) {
+    for (int b = 1; b < 32; ++b) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[j] += slot[b][lane][j];
+    }
+    *reinterpret_cast<f32x4*>(dw + c) = s;
+  }
+}
+
+}  // namespace mmk

@@ -222,6 +222,83 @@ mm_status mm_ffn_swiglu(const void* x, const void* W_gate, const void* W_up, voi
 mm_status mm_ffn_glu(const void* x, const void* W_gate, const void* W_up, void* out, int64_t M,
                      int64_t N, int64_t K, mm_glu_act act, void* stream);
 
+/* ---- Decoder-layer operators beside the products -------------------------
+ *
+ * Conventions as above (device memory, `stream`, host-side checks before any
+ * launch, M == 0, N == 0 or rows == 0 a no-op unless stated).  Where an
+ * output may share memory with an input it is said so.
+ *
+ * Residual addition and root-mean-square norm of `rows` rows:
+ *   h = T(x + residual)                 (h = x without a residual)
+ *   rstd = 1 / sqrt(mean(h^2) + eps)    fp32, from h as stored
+ *   y = h * rstd * weight
+ *   x         [rows][ld_x] of the stream's type T (MM_OUT_BF16 or MM_OUT_F32),
+ *             the first `hidden` of each row; ld_x >= hidden, a multiple of 8
+ *   residual  [rows][hidden] of type T, or NULL
+ *   weight    [hidden] bf16
+ *   h         [rows][hidden] of type T: written when residual is given (else
+ *             ignored); may be `residual` itself, or a contiguous x
+ *   y         [rows][hidden] bf16 (RNE)
+ *   rstd      [rows] fp32 (the backward pass reads it)
+ * hidden: a multiple of 8, at most 32768; 16-byte aligned pointers.  A row
+ * with a NaN is NaN; one with an infinity has rstd = 0. */
+mm_status mm_rms_norm(const void* x, int64_t ld_x, const void* residual, const void* weight, void* h,
+                      void* y, float* rstd, int64_t rows, int64_t hidden, float eps,
+                      mm_out_dtype stream_dtype, void* stream);
+
+/* The same with an 8-bit output (the activations of mm_linear_q8):
+ *   scale[row] = max(max|y| / 448, 2^-126),  q = e4m3(y / scale)
+ * with y the fp32 value before any rounding; q stands for q * scale. */
+mm_status mm_rms_norm_q8(const void* x, int64_t ld_x, const void* residual, const void* weight, void* h,
+                         void* q, float* scale, int64_t rows, int64_t hidden, float eps,
+                         mm_out_dtype stream_dtype, void* stream);
+
+/* Gradient of mm_rms_norm.  With n = h rstd and g = dy weight:
+ *   dh = rstd (g - n mean(g n)) + dres     the gradient of x and of residual
+ *   dweight = sum over rows of dy n        fp32
+ *   dy    [rows][hidden] bf16;  h, rstd as mm_rms_norm left them
+ *   dres  [rows][hidden] of type T or NULL: the gradient that reached h past
+ *         the norm;  dh of type T may be dres itself
+ * Two kernels: the rows, each workgroup keeping its part of dweight, and the
+ * sum of the parts in a fixed order (results are reproducible).  rows == 0
+ * writes zeros to dweight.  The workspace (size from the function below, a
+ * device query; 16-byte aligned, any contents) holds the parts; two calls in
+ * flight at once must not share it. */
+mm_status mm_rms_norm_backward_workspace_size(int64_t rows, int64_t hidden, int64_t* bytes);
+mm_status mm_rms_norm_backward(const void* dy, const void* h, const void* weight, const float* rstd,
+                               const void* dres, void* dh, float* dweight, int64_t rows, int64_t hidden,
+                               mm_out_dtype stream_dtype, void* workspace, int64_t workspace_bytes,
+                               void* stream);
+
+/* LinearOp form with 4-bit weights in groups along K (a served model's decode
+ * step: the weight is read once, half a byte per value):
+ *   out[M][N] = epi(x . Wd^T + bias),  Wd[n][k] = (q[n][k] - z) s,
+ * with z = zeros[k / group][n] (8 when zeros is NULL), s = scales[k / group][n].
+ *   x       [M][K] bf16
+ *   W       the codes q (0..15) packed as mm_w4_pack lays them out
+ *   scales  [ceil(K / group)][N] bf16;  zeros the same shape, one byte each
+ *   group   32, 64 or 128;  K a multiple of 8 (the last group may be short)
+ * Other arguments, the epilogue and errors as for mm_linear.
+ *
+ * Packed layout: [ceil(N/16)][ceil(K/128)] kilobytes.  In a kilobyte, 32-bit
+ * word (g, n, j) (g = 0..3, n = 0..15, j = 0..3, j fastest) covers row n,
+ * k = 32 j + 8 g .. + 7: k + 2p in its nibble p, k + 2p + 1 in its nibble
+ * p + 4.  What pads N and K may hold anything.  mm_w4_pack lays out codes
+ * [N][K] (one byte each; the low four bits are taken) and pads with 0. */
+mm_status mm_w4_pack(const void* codes, void* packed, int64_t N, int64_t K, void* stream);
+mm_status mm_linear_w4(const void* x, const void* W, const void* scales, const void* zeros,
+                       const void* bias, void* out, int64_t M, int64_t N, int64_t K, int64_t group,
+                       mm_epilogue epi, void* stream);
+
+/* LinearOp form with e4m3 operands and row scales:
+ *   out[M][N] = epi(x_scale[m] w_scale[n] (x . W^T) + bias), bf16 (RNE)
+ *   x [M][K], W [N][K] e4m3 (OCP), K contiguous and a multiple of 16, at most
+ *   2^22;  x_scale [M], w_scale [N] fp32.
+ * fp32 sums; the scales multiply the sum, then the epilogue, then one rounding. */
+mm_status mm_linear_q8(const void* x, const float* x_scale, const void* W, const float* w_scale,
+                       const void* bias, void* out, int64_t M, int64_t N, int64_t K, mm_epilogue epi,
+                       void* stream);
+
 /* Tile configuration override, parsed from a string such as
  *   "BM=256,BN=256,WM=2,WN=2,G=8,XCD=1,KALT=1,GRID=0"
  * (BM/BN: output tile; WM/WN: wave grid; G: grouped-swizzle band height in
