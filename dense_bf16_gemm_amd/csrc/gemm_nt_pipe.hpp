@@ -36,10 +36,6 @@ constexpr int kPipeStages = 5;
 // comb of the permuted weight fragments.
 __host__ __device__ __forceinline__ int pipe_swz(int row) { return (row >> 2) & 2; }
 
-// s_waitcnt immediate for gfx9: vmcnt in bits 3:0 and 15:14, expcnt 6:4
-// (left at its maximum), lgkmcnt 11:8 (0).
-constexpr int waitcnt_vm_lgkm0(int vm) { return (vm & 15) | ((vm >> 4) << 14) | (7 << 4); }
-
 template <int BM, int BN, int WGM, int WGN, bool FFN>
 __global__ void __launch_bounds__(WGM * WGN * 64)
 gemm_nt_pipe(GemmParams p) {

@@ -35,6 +35,8 @@ struct W4Params {
   int epi;
 };
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
 constexpr int kW4Waves = 8;
 
 __device__ __forceinline__ float bf16_float(uint16_t v) { return __builtin_bit_cast(float, (uint32_t)v << 16); }
@@ -45,6 +47,20 @@ __device__ __forceinline__ uint16_t decoder_epilogue(float v, const uint16_t* bi
   if (epi == EPI_GELU || epi == EPI_BIAS_GELU) v = gelu_tanh(v);
   return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
+
+// The constants of (a & mask) | bits as values the compiler does not know: it
+// then makes one v_and_or_b32 of it, which takes no literals on this GPU, where
+// of known constants it makes two instructions.
+__device__ __forceinline__ void keep_in_registers(uint32_t& mask, uint32_t& bits) {
+  asm volatile("" : "+s"(mask), "+v"(bits));
+}
+// no memory operation moves across
+__device__ __forceinline__ void order() { asm volatile("" ::: "memory"); }
+// a value is computed before this point and its uses after it
+__device__ __forceinline__ void settle(f32x4& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void settle(u32x4& v) { asm volatile("" : "+v"(v)); }
+// the value of a load is there before anything after this point runs
+__device__ __forceinline__ void arrived(u32x4 v) { asm volatile("" ::"v"(v) : "memory"); }
 
 // Output (m, n) from the definition, term by term.  The kernel's offset form
 // turns an infinite activation (or a sum that overflows) into a NaN of its
@@ -65,96 +81,257 @@ __device__ __forceinline__ float w4_dot(const W4Params& p, int m, int n) {
   return v;
 }
 
-// MB blocks of 16 activation rows by NB blocks of 16 columns per workgroup;
-// its waves take every eighth 128-k step and meet in LDS, added in wave order.
-template <int MB, int NB, int G>
-__global__ void __launch_bounds__(kW4Waves * 64) gemm_w4(W4Params p) {
-  __shared__ f32x4 red[kW4Waves][MB * NB][64];
+// XR activation rows (4: the first four of a block of 16, whose others are
+// never used) by NB blocks of 16 columns per workgroup.  Its WV waves take
+// every WV-th 128-k step, each step's loads issued one step ahead, and their
+// sums meet in LDS, added in wave order.  No barrier until then: what a wave
+// stages in LDS is its own.
+//
+// Activations: each wave copies its step's tile, XR rows of 256 bytes, from
+// L2 to LDS (whole lines: fragments loaded straight into registers touch 16
+// half lines each, and the products of 16 rows, bound by those, ran at 33 us
+// where whole lines made it 30).  16-byte chunk c of row r sits at position
+// c ^ (r & 15), so the fragment reads of 16 rows at one chunk hit 16 banks.
+//
+// Scales: lane (group, four columns) loads the step's, widens them with the
+// offset -(16 + z), and leaves the pairs in LDS, from where the lanes of each
+// column read theirs (a load per column block and group would cost more of
+// the address unit than the weight does).
+template <int XR, int NB, int G, int WV>
+__global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
+  constexpr int MB = XR < 16 ? 1 : XR / 16;
+  constexpr int AB = MB * NB;
+  constexpr int GP = 128 / G;             // groups per step
+  constexpr int SLOTS = XR < 64 ? 2 : 1;  // tiles of activations in LDS per wave
+  // a chunk: what shares one scale and one pass over the accumulators; JC
+  // MFMAs, whose fragments are read JR at a time
+  constexpr int JC = (SLOTS == 1 && G > 64 ? 64 : G) / 32;
+  constexpr int JR = SLOTS == 1 ? 2 : JC;
+  // The compiler would start all of a step's products at once.  Where that
+  // takes more registers than there are (or than the waves of two workgroups
+  // share), a column block's products wait for those BB blocks before.
+  constexpr bool CALM = MB == 4 || AB * GP > (MB == 2 ? 16 : 4);
+  constexpr int BB = MB < 4 && NB > 1 ? 2 : 1;
+  constexpr int XC = XR / 4;    // copies per step: four rows of 256 bytes each
+  // scale pairs: a column's GP * NB, in an odd number of 16-byte units (reads
+  // of 16 columns then fall in 16 bank groups)
+  constexpr int PB = GP * NB, SU = PB < 2 ? 1 : (PB / 2) | 1;
+  constexpr int kSc = 16 * SU * 16;
+  constexpr int kX = SLOTS * XR * 256, kWave = kX + kSc;  // LDS bytes per wave
+  constexpr int RS = AB > 8 ? WV / 2 : WV;  // waves whose sums are in LDS at once
+  constexpr int kRed = RS * AB * 1024;
+  __shared__ __attribute__((aligned(1024))) char smem[WV * kWave > kRed ? WV * kWave : kRed];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lx = lane & 15, lg = lane >> 4;
   const int kblocks = (p.K + 127) >> 7;
   const int nblocks = (p.N + 15) >> 4;
-  const int m0 = blockIdx.y * (16 * MB);
+  const int groups = (p.K + G - 1) / G;
+  const int m0 = blockIdx.y * XR;
   const int b0 = blockIdx.x * NB;
+  char* xs = smem + wave * kX;
+  char* sc = smem + WV * kX + wave * kSc;
+
+  // rows past M lie past the descriptor's end and arrive as zeros, as do (bit
+  // 31 of the offset) the chunks of the last step past K
+  const uint32_t row_bytes = (uint32_t)p.K * 2u;
+  const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint16_t*>(p.x + (int64_t)m0 * p.K), (short)0, (int)((uint32_t)min(p.M - m0, XR) * row_bytes),
+      0x00020000);
+  uint32_t voff[XC], tail[XC < 4 ? XC : 4];
+#pragma unroll
+  for (int i = 0; i < XC; ++i) {
+    const int r = 4 * i + lg, chunk = lx ^ (r & 15);
+    voff[i] = (uint32_t)r * row_bytes + 16u * (uint32_t)chunk;
+    if (i < 4) tail[i] = (kblocks - 1) * 128 + 8 * chunk < p.K ? 0u : 0x80000000u;
+  }
+  // scales: lane (group sg of the step, columns sn .. sn + 3); lanes past the
+  // step's groups repeat earlier ones.  The last columns' loads start early
+  // enough to end with the row (N >= 4) and are shifted into place.
+  const int sg = lane / (4 * NB) % GP, sq = lane % (4 * NB);
+  const int sn = 16 * b0 + 4 * sq;
+  const int back = max(0, sn + 4 - p.N);
+  const int shift = 8 * min(back, 3);
+  const uint8_t* zp = p.zeros ? p.zeros : reinterpret_cast<const uint8_t*>(p.scales);
+
+  struct Step {
+    u32x4 w[NB];
+    uint64_t s;  // four bf16
+    uint32_t z;
+  };
+  auto copy = [&](int kb, int slot) __attribute__((always_inline)) {
+    const bool last = kb == kblocks - 1;
+#pragma unroll
+    for (int i = 0; i < XC; ++i)
+      copy_to_lds(rx, xs + slot * (XR * 256) + i * 1024, voff[i] | (last ? tail[i & 3] : 0u), (uint32_t)kb * 256u);
+  };
+  auto load = [&](int kb, Step& t) __attribute__((always_inline)) {
+    const int group = min(kb * GP + sg, groups - 1);
+    const int64_t at = (int64_t)group * p.N + (sn - back);
+    __builtin_memcpy(&t.s, p.scales + at, 8);
+    __builtin_memcpy(&t.z, zp + at, 4);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)  // (a block past N reads the last one; its sums are dropped)
+      t.w[b] = __builtin_nontemporal_load(p.W + ((int64_t)min(b0 + b, nblocks - 1) * kblocks + kb) * 64 + lane);
+  };
+
   f32x4 acc[MB][NB];
 #pragma unroll
   for (int a = 0; a < MB; ++a)
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-
   const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
-  for (int kb = wave; kb < kblocks; kb += kW4Waves) {
-    u32x4 w[NB];
+  uint32_t mask = 0x00780078u, sixteen = 0x41804180u;
+  keep_in_registers(mask, sixteen);
+
+  // Step kb, and the loads of the wave's next.  Two slots: the next step's
+  // copies go out first (loads arrive in order, so once a step's weights are
+  // there its activations are).  One slot (64 rows): the next step's weights
+  // go out first, its copies once this step's last fragments are in registers.
+  auto step = [&](int kb, int slot, Step& t, Step& next) __attribute__((always_inline)) {
+    const int kn = min(kb + WV, kblocks - 1);
+    if constexpr (SLOTS == 2) {
+      copy(kn, slot ^ 1);
+      load(kn, next);
 #pragma unroll
-    for (int b = 0; b < NB; ++b)  // (a block past N reads the last one; its sums are dropped)
-      w[b] = p.W[((int64_t)min(b0 + b, nblocks - 1) * kblocks + kb) * 64 + lane];
-    u32x4 x[MB][4];
-#pragma unroll
-    for (int a = 0; a < MB; ++a) {
-      const int m = m0 + 16 * a + lx;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = kb * 128 + 32 * j + 8 * lg;
-        x[a][j] = u32x4{0u, 0u, 0u, 0u};
-        if (m < p.M && k < p.K) x[a][j] = *reinterpret_cast<const u32x4*>(p.x + (int64_t)m * p.K + k);
-      }
+      for (int b = 0; b < NB; ++b) arrived(t.w[b]);
+    } else {
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+      order();
+      load(kn, next);
     }
+    // (a group past K has no activations: scale 0, whatever the last group's is)
+    const uint64_t s = kb * GP + sg < groups ? t.s >> (2 * shift) : 0u;
+    const uint32_t z = p.zeros ? t.z >> shift : 0x08080808u;
 #pragma unroll
-    for (int g = 0; g < 128 / G; ++g) {
-      constexpr int JG = G / 32;  // MFMAs per group
-      const int group = kb * (128 / G) + g;
-      const bool live = group * G < p.K;  // (x is zero in a group past K)
-      f32x4 sx[MB];
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t bits = (uint32_t)(s >> (16 * i)) << 16;
+      // column 4 sq + i of the workgroup's: block sq / 4, lane 4 (sq % 4) + i
+      *reinterpret_cast<f32x2*>(sc + (4 * (sq & 3) + i) * (16 * SU) + (sg * NB + (sq >> 2)) * 8) =
+          f32x2{__builtin_bit_cast(float, bits), -16.0f - (float)((z >> (8 * i)) & 255u)};
+    }
+    order();  // (a wave's LDS operations run in order)
+    const char* xt = xs + (SLOTS == 2 ? slot * (XR * 256) : 0);
+    f32x4 so = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int a = 0; a < MB; ++a) {
-        sx[a] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < 4 / JR; ++r) {
+      u32x4 x[MB][JR];
 #pragma unroll
-        for (int j = 0; j < JG; ++j)
-          sx[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[a][g * JG + j]), ones, sx[a],
-                                                          0, 0, 0);
+      for (int a = 0; a < MB; ++a)
+#pragma unroll
+        for (int j = 0; j < JR; ++j) {
+          const int row = XR < 16 ? lx & (XR - 1) : 16 * a + lx;
+          x[a][j] = *reinterpret_cast<const u32x4*>(xt + row * 256 + (((4 * (r * JR + j) + lg) ^ (row & 15)) << 4));
+        }
+      if (r == 4 / JR - 1) {
+        // every read of the tile has returned before a copy into it is issued
+        // (two slots: at the next step's start)
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(63));
+        order();
+        if constexpr (SLOTS == 1) copy(kn, 0);
       }
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int n = min(16 * (b0 + b) + lx, p.N - 1);
-        const int64_t at = (int64_t)(live ? group : 0) * p.N + n;
-        const float s = bf16_float(p.scales[at]);
-        const float off = -16.0f - (p.zeros ? (float)p.zeros[at] : 8.0f);
-        f32x4 t[MB];
+      for (int c = 0; c < JR / JC; ++c) {
+        const int g = (r * JR + c * JC) * 32 / G;  // the chunk's group in the step
+        f32x4 sx[MB];
 #pragma unroll
-        for (int a = 0; a < MB; ++a) t[a] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int a = 0; a < MB; ++a) {
+          sx[a] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < JG; ++j) {
-          const uint32_t v = w[b][g * JG + j];
-          u32x4 q;
-          q[0] = ((v << 3) & 0x00780078u) | 0x41804180u;
-          q[1] = ((v >> 1) & 0x00780078u) | 0x41804180u;
-          q[2] = ((v >> 5) & 0x00780078u) | 0x41804180u;
-          q[3] = ((v >> 9) & 0x00780078u) | 0x41804180u;
-#pragma unroll
-          for (int a = 0; a < MB; ++a)
-            t[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[a][g * JG + j]),
-                                                           __builtin_bit_cast(bf16x8, q), t[a], 0, 0, 0);
+          for (int j = 0; j < JC; ++j)
+            sx[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[a][c * JC + j]), ones, sx[a],
+                                                            0, 0, 0);
         }
 #pragma unroll
-        for (int a = 0; a < MB; ++a)
+        for (int b = 0; b < NB; ++b) {
+          float scale, off;
+          if constexpr (PB == 1) {
+            const f32x2 u = *reinterpret_cast<const f32x2*>(sc + lx * (16 * SU));
+            scale = u[0];
+            off = u[1];
+          } else {
+            // two pairs per read
+            const int pair = g * NB + b;
+            if (pair % 2 == 0 || GP == 1) so = *reinterpret_cast<const f32x4*>(sc + lx * (16 * SU) + (pair & ~1) * 8);
+            scale = so[2 * (pair & 1)];
+            off = so[2 * (pair & 1) + 1];
+          }
+          if constexpr (CALM) {
+            const int before = (b + NB - BB) % NB;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc[a][b][i] = __builtin_fmaf(s, __builtin_fmaf(off, sx[a][i], t[a][i]), acc[a][b][i]);
+            for (int a = 0; a < MB; ++a) settle(acc[a][before]);
+            settle(t.w[b]);
+          }
+          f32x4 d[MB];
+#pragma unroll
+          for (int a = 0; a < MB; ++a) d[a] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < JC; ++j) {
+            const uint32_t v = t.w[b][r * JR + c * JC + j];
+            const u32x4 q = {((v << 3) & mask) | sixteen, ((v >> 1) & mask) | sixteen, ((v >> 5) & mask) | sixteen,
+                             ((v >> 9) & mask) | sixteen};
+#pragma unroll
+            for (int a = 0; a < MB; ++a)
+              d[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[a][c * JC + j]),
+                                                             __builtin_bit_cast(bf16x8, q), d[a], 0, 0, 0);
+          }
+#pragma unroll
+          for (int a = 0; a < MB; ++a)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              acc[a][b][i] = __builtin_fmaf(scale, __builtin_fmaf(off, sx[a][i], d[a][i]), acc[a][b][i]);
+        }
       }
     }
+    order();
+  };
+
+  if (wave < kblocks) {
+    // (past its last step a wave loads the last one of all again, unused: the
+    // loop then has one shape, and its waits count loads exactly)
+    Step s0, s1;
+    copy(wave, 0);
+    load(wave, s0);
+    for (int kb = wave; kb < kblocks; kb += 2 * WV) {
+      step(kb, 0, s0, s1);
+      if (kb + WV < kblocks) step(kb + WV, 1, s1, s0);
+    }
   }
-#pragma unroll
-  for (int a = 0; a < MB; ++a)
-#pragma unroll
-    for (int b = 0; b < NB; ++b) red[wave][a * NB + b][lane] = acc[a][b];
+
+  // the copies' slots become slots of sums, once every copy has landed
+  __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  for (int e = threadIdx.x; e < MB * NB * 64; e += kW4Waves * 64) {
-    const int ab = e >> 6, l = e & 63;
-    f32x4 v = red[0][ab][l];
+  f32x4* red = reinterpret_cast<f32x4*>(smem);
+  auto put = [&](int place) __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 1; q < kW4Waves; ++q) {
-      const f32x4 u = red[q][ab][l];
+    for (int a = 0; a < MB; ++a)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) red[(place * AB + a * NB + b) * 64 + lane] = acc[a][b];
+  };
+  if constexpr (RS < WV) {  // the later half of the waves hands its sums to the earlier first
+    if (wave >= RS) put(wave - RS);
+    __syncthreads();
+    if (wave < RS) {
+#pragma unroll
+      for (int a = 0; a < MB; ++a)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const f32x4 u = red[(wave * AB + a * NB + b) * 64 + lane];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[a][b][i] += u[i];
+        }
+      put(wave);
+    }
+  } else {
+    put(wave);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < AB * 64; e += WV * 64) {
+    const int ab = e >> 6, l = e & 63;
+    f32x4 v = red[e];
+#pragma unroll
+    for (int q = 1; q < RS; ++q) {
+      const f32x4 u = red[q * AB * 64 + e];
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] += u[i];
     }
@@ -170,6 +347,14 @@ __global__ void __launch_bounds__(kW4Waves * 64) gemm_w4(W4Params p) {
       p.out[(int64_t)m * p.N + n] = decoder_epilogue(o, p.bias, p.epi, n);
     }
   }
+}
+
+// Fewer than four columns: every output term by term, one per thread.
+__global__ void __launch_bounds__(64) gemm_w4_narrow(W4Params p) {
+  const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x;
+  if (i >= (int64_t)p.M * p.N) return;
+  const int m = (int)(i / p.N), n = (int)(i % p.N);
+  p.out[i] = decoder_epilogue(w4_dot(p, m, n), p.bias, p.epi, n);
 }
 
 // Lays out codes [N][K] (one byte each, the low four bits taken) as packed

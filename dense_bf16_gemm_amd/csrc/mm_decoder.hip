@@ -154,13 +154,25 @@ mm_status check_product(int64_t M, int64_t N, int64_t K, const void* bias, const
   return MM_OK;
 }
 
-template <int MB, int NB>
+template <int XR, int NB>
 const void* w4_kernel(int group) {
   switch (group) {
-    case 32: return fn(&mmk::gemm_w4<MB, NB, 32>);
-    case 64: return fn(&mmk::gemm_w4<MB, NB, 64>);
+    case 32: return fn(&mmk::gemm_w4<XR, NB, 32, mmk::kW4Waves>);
+    case 64: return fn(&mmk::gemm_w4<XR, NB, 64, mmk::kW4Waves>);
   }
-  return fn(&mmk::gemm_w4<MB, NB, 128>);
+  return fn(&mmk::gemm_w4<XR, NB, 128, mmk::kW4Waves>);
+}
+template <int XR>
+const void* w4_kernel(int nb, int group) {
+  return nb == 1 ? w4_kernel<XR, 1>(group) : nb == 2 ? w4_kernel<XR, 2>(group) : w4_kernel<XR, 4>(group);
+}
+const void* w4_kernel(int rows, int nb, int group) {
+  switch (rows) {
+    case 4: return w4_kernel<4>(nb, group);
+    case 16: return w4_kernel<16>(nb, group);
+    case 32: return w4_kernel<32>(nb, group);
+  }
+  return w4_kernel<64>(nb, group);
 }
 
 }  // namespace
@@ -277,6 +289,7 @@ mm_status mm_linear_w4(const void* x, const void* W, const void* scales, const v
     if (!aligned(x, 16) || !aligned(W, 16)) return fail(MM_ERR_MISALIGNED, "x and W must be 16-byte aligned");
     if (!aligned(scales, 2)) return fail(MM_ERR_MISALIGNED, "scales must be 2-byte aligned");
     if (K % 8 != 0) return fail(MM_ERR_MISALIGNED, "K must be a multiple of 8 elements");
+    if (K > (int64_t(1) << 22)) return fail(MM_ERR_UNSUPPORTED, "K must be at most 2^22");
     const int64_t ob = M * N * 2, groups = cdiv(K, group);
     if (overlaps(out, ob, x, M * K * 2) || overlaps(out, ob, W, cdiv(N, 16) * cdiv(K, 128) * 1024) ||
         overlaps(out, ob, scales, groups * N * 2) || overlaps(out, ob, zeros, groups * N))
@@ -294,13 +307,22 @@ mm_status mm_linear_w4(const void* x, const void* W, const void* scales, const v
   p.K = (int)K;
   p.group = (int)group;
   p.epi = epi;
-  const int mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-  const int nb = mb == 4 ? 2 : 4;
-  const void* k = mb == 1 ? w4_kernel<1, 4>((int)group) : mb == 2 ? w4_kernel<2, 4>((int)group) : w4_kernel<4, 2>((int)group);
-  const int64_t gy = cdiv(M, 16 * mb);
+  if (N < 4) {
+    void* args[] = {&p};
+    return launch(fn(&mmk::gemm_w4_narrow), dim3((unsigned)cdiv(M * N, 64)), 64, args, stream, "linear_w4 narrow");
+  }
+  const int xr = M <= 4 ? 4 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  const int64_t blocks = cdiv(N, 16);
+  // Column blocks per workgroup: each workgroup reads the activations for
+  // itself, so as many as leave most CUs a workgroup.  Measured (us, 1 / 2 / 4
+  // blocks): 1 x 8192 x 8192 9.8 / 8.7 / 10.9, 16 x 14336 x 4096 15.9 / 11.5 /
+  // 9.6, 64 x 14336 x 4096 40 / 26 / 20, 37 x 3001 x 4104 12.4 / 14.4 / 19.3.
+  const int nb = blocks >= 800 ? 4 : blocks >= 400 ? 2 : 1;
+  const int64_t gy = cdiv(M, xr);
   if (gy > 65535) return fail(MM_ERR_UNSUPPORTED, "M too large");
   void* args[] = {&p};
-  return launch(k, dim3((unsigned)cdiv(N, 16 * nb), (unsigned)gy), mmk::kW4Waves * 64, args, stream, "linear_w4");
+  return launch(w4_kernel(xr, nb, (int)group), dim3((unsigned)cdiv(blocks, nb), (unsigned)gy), mmk::kW4Waves * 64, args,
+                stream, "linear_w4");
 }
 
 mm_status mm_linear_q8(const void* x, const float* x_scale, const void* W, const float* w_scale, const void* bias,

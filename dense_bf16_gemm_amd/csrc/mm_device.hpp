@@ -48,6 +48,17 @@ __device__ __forceinline__ float gelu_tanh(float t) {
   return t * __builtin_amdgcn_rcpf(1.0f + __expf(-2.0f * z));
 }
 
+// s_waitcnt immediate for gfx9: vmcnt in bits 3:0 and 15:14, expcnt 6:4
+// (left at its maximum), lgkmcnt 11:8 (0).
+constexpr int waitcnt_vm_lgkm0(int vm) { return (vm & 15) | ((vm >> 4) << 14) | (7 << 4); }
+
+// One wave-wide copy of 64 x 16 bytes from a buffer to LDS: lane l's chunk, at
+// byte `off` (its own) + `base` (the wave's) of the buffer, lands at dst + 16 l;
+// zeros do where `off` lies past the buffer's end.
+__device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t buf, char* dst, uint32_t off, uint32_t base) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (__attribute__((address_space(3))) void*)dst, 16, off, base, 0, 0);
+}
+
 // Two floats to a packed pair of bf16 (round to nearest even), low half
 // first: one v_cvt_pk_bf16_f32 through a two-element vector conversion.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {

@@ -277,7 +277,8 @@ mm_status mm_rms_norm_backward(const void* dy, const void* h, const void* weight
  *   x       [M][K] bf16
  *   W       the codes q (0..15) packed as mm_w4_pack lays them out
  *   scales  [ceil(K / group)][N] bf16;  zeros the same shape, one byte each
- *   group   32, 64 or 128;  K a multiple of 8 (the last group may be short)
+ *   group   32, 64 or 128;  K a multiple of 8 (the last group may be short), at
+ *           most 2^22
  * Other arguments, the epilogue and errors as for mm_linear.
  *
  * Packed layout: [ceil(N/16)][ceil(K/128)] kilobytes.  In a kilobyte, 32-bit

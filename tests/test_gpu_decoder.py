@@ -224,7 +224,8 @@ def test_pack_w4(dev, N, K):
 
 W4 = [(1, 16, 128), (1, 1, 8), (1, 4096, 2048), (2, 65, 136), (5, 130, 1000), (15, 100, 520), (16, 333, 1024),
       (17, 47, 2056), (32, 129, 640), (33, 64, 384), (37, 3001, 264), (64, 515, 1280), (65, 70, 256),
-      (200, 97, 392)]
+      (200, 97, 392), (1, 16421, 264), (4, 9001, 1160), (16, 16450, 264), (13, 9001, 392), (30, 16421, 136),
+      (32, 9001, 1160), (64, 16450, 136), (50, 9001, 264)]
 
 
 @pytest.mark.parametrize("M,N,K", W4)
