@@ -27,6 +27,7 @@ EXPORTS = (
     "mm_workspace_size", "mm_matmul_ws", "mm_linear_ws", "mm_matmul_batched", "mm_linear_batched",
     "mm_linear_preact", "mm_matmul_noalloc", "mm_rms_norm", "mm_rms_norm_q8", "mm_rms_norm_backward",
     "mm_rms_norm_backward_workspace_size", "mm_w4_pack", "mm_linear_w4", "mm_linear_q8",
+    "mm_linear_q8_workspace_size",
 )
 
 _lib = None
@@ -78,12 +79,14 @@ def open_library(path: str):
     lib.mm_rms_norm_backward_workspace_size.argtypes = [i64, i64, ctypes.POINTER(ctypes.c_int64)]
     lib.mm_w4_pack.argtypes = [vp, vp, i64, i64, vp]
     lib.mm_linear_w4.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, ci, vp]
-    lib.mm_linear_q8.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, ci, vp]
+    lib.mm_linear_q8.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, ci, vp, i64, vp]
+    lib.mm_linear_q8_workspace_size.argtypes = [i64, i64, i64, ctypes.POINTER(ctypes.c_int64)]
     for name in ("mm_matmul", "mm_linear", "mm_ffn_swiglu", "mm_ffn_glu", "mm_set_config",
                  "mm_describe_config", "mm_debug_schedule", "mm_workspace_size", "mm_matmul_ws",
                  "mm_linear_ws", "mm_matmul_batched", "mm_linear_batched", "mm_linear_preact",
                  "mm_matmul_noalloc", "mm_rms_norm", "mm_rms_norm_q8", "mm_rms_norm_backward",
-                 "mm_rms_norm_backward_workspace_size", "mm_w4_pack", "mm_linear_w4", "mm_linear_q8"):
+                 "mm_rms_norm_backward_workspace_size", "mm_w4_pack", "mm_linear_w4", "mm_linear_q8",
+                 "mm_linear_q8_workspace_size"):
         getattr(lib, name).restype = ci
     lib.mm_status_string.argtypes = [ci]
     lib.mm_status_string.restype = ctypes.c_char_p
@@ -118,6 +121,13 @@ def rms_norm_backward_workspace_size(rows: int, hidden: int) -> int:
     n = ctypes.c_int64(0)
     check(load().mm_rms_norm_backward_workspace_size(rows, hidden, ctypes.byref(n)),
           "mm_rms_norm_backward_workspace_size")
+    return n.value
+
+
+def linear_q8_workspace_size(M: int, N: int, K: int) -> int:
+    """Bytes of workspace mm_linear_q8 may use for this shape (0: none)."""
+    n = ctypes.c_int64(0)
+    check(load().mm_linear_q8_workspace_size(M, N, K, ctypes.byref(n)), "mm_linear_q8_workspace_size")
     return n.value
 
 

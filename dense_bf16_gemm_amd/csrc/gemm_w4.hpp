@@ -54,14 +54,6 @@ __device__ __forceinline__ uint16_t decoder_epilogue(float v, const uint16_t* bi
 __device__ __forceinline__ void keep_in_registers(uint32_t& mask, uint32_t& bits) {
   asm volatile("" : "+s"(mask), "+v"(bits));
 }
-// no memory operation moves across
-__device__ __forceinline__ void order() { asm volatile("" ::: "memory"); }
-// a value is computed before this point and its uses after it
-__device__ __forceinline__ void settle(f32x4& v) { asm volatile("" : "+v"(v)); }
-__device__ __forceinline__ void settle(u32x4& v) { asm volatile("" : "+v"(v)); }
-// the value of a load is there before anything after this point runs
-__device__ __forceinline__ void arrived(u32x4 v) { asm volatile("" ::"v"(v) : "memory"); }
-
 // Output (m, n) from the definition, term by term.  The kernel's offset form
 // turns an infinite activation (or a sum that overflows) into a NaN of its
 // own making; those outputs, rare and never in a finite model, are computed

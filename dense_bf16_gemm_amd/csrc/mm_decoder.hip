@@ -175,6 +175,80 @@ const void* w4_kernel(int rows, int nb, int group) {
   return w4_kernel<64>(nb, group);
 }
 
+template <int XR>
+const void* q8_rows_kernel(int nb) {
+  return nb == 1   ? fn(&mmk::gemm_q8_rows<XR, 1, mmk::kW4Waves>)
+         : nb == 2 ? fn(&mmk::gemm_q8_rows<XR, 2, mmk::kW4Waves>)
+                   : fn(&mmk::gemm_q8_rows<XR, 4, mmk::kW4Waves>);
+}
+const void* q8_rows_kernel(int rows, int nb) {
+  switch (rows) {
+    case 4: return q8_rows_kernel<4>(nb);
+    case 16: return q8_rows_kernel<16>(nb);
+    case 32: return q8_rows_kernel<32>(nb);
+  }
+  return q8_rows_kernel<64>(nb);
+}
+
+// ----------------------------------------------------------------------------
+// 8-bit products of more than kQ8Rows rows: the kind of tile, and whether K is
+// cut so that few tiles fill the GPU.
+// ----------------------------------------------------------------------------
+constexpr int64_t kQ8Rows = 64;
+constexpr int64_t kQ8MaxChunks = 8;
+constexpr int64_t kQ8Cus = 256;  // of the target GPU
+
+// A kind's cost is the time (us) of one 128-k super-step of a full GPU of
+// workgroups (measured at K = 8192: 4096 x 4096, 4096 x 2048, 2048 x 4096); a
+// partly filled GPU runs its tiles faster, down to 0.45 of that (128 tiles of
+// each kind: 0.73, 0.70 and 0.63 of it).
+struct Q8Kind {
+  int fm, fn, resident;  // tile of 64 fm x 64 fn, workgroups per CU
+  double step;
+};
+constexpr Q8Kind kQ8Kinds[] = {{4, 4, 1, 1.90}, {4, 2, 1, 1.16}, {2, 2, 2, 1.09}};
+
+struct Q8Plan {
+  int kind = 0;
+  int64_t tiles_m = 0, tiles_n = 0, chunks = 1, chunk_steps = 0;
+};
+
+int64_t q8_ws_bytes(const Q8Plan& p) {
+  if (p.chunks == 1) return 0;
+  const Q8Kind& k = kQ8Kinds[p.kind];
+  return p.tiles_m * p.tiles_n * p.chunks * k.fm * k.fn * 4096 * 4;
+}
+
+Q8Plan q8_plan(int64_t M, int64_t N, int64_t K, int64_t max_chunks) {
+  const int64_t steps = cdiv(K, 128);
+  Q8Plan best;
+  double bc = -1.0;
+  for (int kind = 0; kind < 3; ++kind) {
+    const Q8Kind& k = kQ8Kinds[kind];
+    Q8Plan p;
+    p.kind = kind;
+    p.tiles_m = cdiv(M, 64 * k.fm);
+    p.tiles_n = cdiv(N, 64 * k.fn);
+    for (int64_t c = 1; c <= max_chunks; ++c) {
+      p.chunk_steps = cdiv(steps, c);
+      p.chunks = cdiv(steps, p.chunk_steps);
+      if (p.chunks != c || (c > 1 && p.chunk_steps < 4)) continue;
+      const int64_t units = p.tiles_m * p.tiles_n * c, slots = kQ8Cus * k.resident;
+      const int64_t rem = units % slots;
+      const double passes = (double)(units / slots) + (rem ? 0.45 + 0.55 * (double)rem / (double)slots : 0.0);
+      // per pass, a start and an end worth about four super-steps
+      double cost = passes * k.step * (double)(p.chunk_steps + 4);
+      // the chunks' sums written and read at about 4 TB/s, and a second launch
+      if (c > 1) cost += 2.0 * (double)q8_ws_bytes(p) / 4e6 + 4.0;
+      if (bc < 0.0 || cost < bc) {
+        bc = cost;
+        best = p;
+      }
+    }
+  }
+  return best;
+}
+
 }  // namespace
 
 extern "C" {
@@ -325,8 +399,18 @@ mm_status mm_linear_w4(const void* x, const void* W, const void* scales, const v
                 stream, "linear_w4");
 }
 
+mm_status mm_linear_q8_workspace_size(int64_t M, int64_t N, int64_t K, int64_t* bytes) {
+  if (!bytes) return fail(MM_ERR_INVALID_VALUE, "null bytes pointer");
+  *bytes = 0;
+  if (M < 0 || N < 0 || K < 0) return fail(MM_ERR_INVALID_VALUE, "negative size");
+  if (M >= kLimit || N >= kLimit || K >= kLimit) return fail(MM_ERR_UNSUPPORTED, "M, N and K must be below 2^31");
+  if (M > kQ8Rows && N > 0 && K > 0) *bytes = q8_ws_bytes(q8_plan(M, N, K, kQ8MaxChunks));
+  return MM_OK;
+}
+
 mm_status mm_linear_q8(const void* x, const float* x_scale, const void* W, const float* w_scale, const void* bias,
-                       void* out, int64_t M, int64_t N, int64_t K, mm_epilogue epilogue, void* stream) {
+                       void* out, int64_t M, int64_t N, int64_t K, mm_epilogue epilogue, void* workspace,
+                       int64_t workspace_bytes, void* stream) {
   int epi = 0;
   mm_status s = check_product(M, N, K, bias, out, epilogue, &epi);
   if (s != MM_OK) return s;
@@ -344,6 +428,11 @@ mm_status mm_linear_q8(const void* x, const float* x_scale, const void* W, const
     if (overlaps(out, ob, x, M * K) || overlaps(out, ob, W, N * K))
       return fail(MM_ERR_INVALID_VALUE, "out overlaps an input");
   }
+  if (workspace_bytes < 0) return fail(MM_ERR_INVALID_VALUE, "negative workspace size");
+  if (overlaps(workspace, workspace_bytes, out, ob) || overlaps(workspace, workspace_bytes, x, M * K) ||
+      overlaps(workspace, workspace_bytes, W, N * K) || overlaps(workspace, workspace_bytes, x_scale, M * 4) ||
+      overlaps(workspace, workspace_bytes, w_scale, N * 4) || overlaps(workspace, workspace_bytes, bias, N * 2))
+    return fail(MM_ERR_INVALID_VALUE, "workspace overlaps an operand or the output");
   mmk::Q8Params p;
   p.x = static_cast<const uint8_t*>(x);
   p.xs = x_scale;
@@ -356,17 +445,49 @@ mm_status mm_linear_q8(const void* x, const float* x_scale, const void* W, const
   p.K = (int)K;
   p.epi = epi;
   void* args[] = {&p};
-  if (M <= 64) {
-    const int mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-    const int nb = mb == 4 ? 2 : 4;
-    const void* k = mb == 1 ? fn(&mmk::gemm_q8_rows<1, 4>) : mb == 2 ? fn(&mmk::gemm_q8_rows<2, 4>) : fn(&mmk::gemm_q8_rows<4, 2>);
-    return launch(k, dim3((unsigned)cdiv(N, 16 * nb)), mmk::kW4Waves * 64, args, stream, "linear_q8 rows");
+  if (M <= kQ8Rows || K == 0) {
+    const int xr = M <= 4 ? 4 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
+    const int64_t blocks = cdiv(N, 16);
+    // Column blocks per workgroup.  Many small workgroups stream W best (1 x
+    // 28672 x 8192: 41.9 us with one block, 51.9 / 48.8 with 2 / 4), but each
+    // reads x for itself, and one of few steps is mostly its start and end (us,
+    // 1 / 2 / 4 blocks: 4 x 14336 x 4096 14.6 / 13.9 / 13.3; 16 x 8192 x 8192
+    // 13.9 / 16.2 / 20.0; 16 x 28672 x 8192 56.7 / 53.5 / 52.6; 64 x 8192 x 8192
+    // 23.2 / 18.2 / 25.2; 64 x 28672 x 8192 102 / 81 / 68).
+    const int nb = blocks < 400 || (M <= 4 && K >= 8192) || (M <= 16 && blocks < 800) ? 1 : blocks < 800 ? 2 : 4;
+    const int64_t gy = cdiv(M, xr);
+    if (gy > 65535) return fail(MM_ERR_UNSUPPORTED, "M too large");
+    return launch(q8_rows_kernel(xr, nb), dim3((unsigned)cdiv(blocks, nb), (unsigned)gy), mmk::kW4Waves * 64, args, stream,
+                  "linear_q8 rows");
   }
-  const int64_t tm = cdiv(M, 128), tn = cdiv(N, 128);
-  if (tm * tn >= kLimit) return fail(MM_ERR_UNSUPPORTED, "more than 2^31 output tiles");
-  p.tiles_m = (int)tm;
-  p.tiles_n = (int)tn;
-  return launch(fn(&mmk::gemm_q8_tile), dim3((unsigned)(tm * tn)), 256, args, stream, "linear_q8 tiles");
+  const Q8Plan plan = q8_plan(M, N, K, workspace ? kQ8MaxChunks : 1);
+  if (plan.tiles_m * plan.tiles_n * plan.chunks >= kLimit) return fail(MM_ERR_UNSUPPORTED, "more than 2^31 output tiles");
+  const int64_t need = q8_ws_bytes(plan);
+  if (need > 0) {
+    if (workspace_bytes < need)
+      return fail(MM_ERR_INVALID_VALUE, "workspace smaller than mm_linear_q8_workspace_size reports");
+    if (!aligned(workspace, 16)) return fail(MM_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+  }
+  p.tiles_m = (int)plan.tiles_m;
+  p.tiles_n = (int)plan.tiles_n;
+  p.chunks = (int)plan.chunks;
+  p.chunk_steps = (int)plan.chunk_steps;
+  p.part = static_cast<float*>(workspace);
+  int cus = 0;
+  if ((s = device_cus(&cus)) != MM_OK) return s;
+  const int64_t units = plan.tiles_m * plan.tiles_n * plan.chunks;
+  const int64_t grid = std::min<int64_t>(units, (int64_t)cus * kQ8Kinds[plan.kind].resident);
+  const bool split = plan.chunks > 1;
+  s = launch(plan.kind == 0   ? (split ? fn(&mmk::gemm_q8_tile<4, 4, true>) : fn(&mmk::gemm_q8_tile<4, 4, false>))
+             : plan.kind == 1 ? (split ? fn(&mmk::gemm_q8_tile<4, 2, true>) : fn(&mmk::gemm_q8_tile<4, 2, false>))
+                              : (split ? fn(&mmk::gemm_q8_tile<2, 2, true>) : fn(&mmk::gemm_q8_tile<2, 2, false>)),
+             dim3((unsigned)grid), 256, args, stream, "linear_q8 tiles");
+  if (s != MM_OK || !split) return s;
+  const int64_t blocks = plan.tiles_m * plan.tiles_n * kQ8Kinds[plan.kind].fm * kQ8Kinds[plan.kind].fn;
+  return launch(plan.kind == 0   ? fn(&mmk::gemm_q8_join<4, 4>)
+                : plan.kind == 1 ? fn(&mmk::gemm_q8_join<4, 2>)
+                                 : fn(&mmk::gemm_q8_join<2, 2>),
+                dim3((unsigned)blocks), 256, args, stream, "linear_q8 join");
 }
 
 }  // extern "C"

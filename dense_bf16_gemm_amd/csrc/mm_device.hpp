@@ -59,6 +59,21 @@ __device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t buf, char* ds
   __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (__attribute__((address_space(3))) void*)dst, 16, off, base, 0, 0);
 }
 
+// Marks for the compiler, no instructions.
+// No memory operation moves across:
+__device__ __forceinline__ void order() { asm volatile("" ::: "memory"); }
+// A value is computed before this point and its uses come after it:
+__device__ __forceinline__ void settle(float& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void settle(f32x4& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void settle(u32x4& v) { asm volatile("" : "+v"(v)); }
+// The value of a load is there before anything after this point runs:
+__device__ __forceinline__ void arrived(u32x4 v) { asm volatile("" ::"v"(v) : "memory"); }
+
+// A 16-byte read of LDS.  The restrict parameter tells the compiler that no copy
+// in flight writes what is read (the kernel's waits and barriers see to it);
+// without it, it waits for every copy before reads it cannot tell apart.
+__device__ __forceinline__ u32x4 lds_chunk(const char* __restrict__ p) { return *reinterpret_cast<const u32x4*>(p); }
+
 // Two floats to a packed pair of bf16 (round to nearest even), low half
 // first: one v_cvt_pk_bf16_f32 through a two-element vector conversion.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {

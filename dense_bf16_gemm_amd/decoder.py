@@ -209,8 +209,14 @@ def linear_q8(x: torch.Tensor, x_scale: torch.Tensor, W: torch.Tensor, w_scale: 
     _check(x_scale, "x_scale", _F32, (M,), dev)
     _check(w_scale, "w_scale", _F32, (N,), dev)
     epi, bias, out = _product(x, bias, epilogue, N, out, dev)
+    ws, nbytes = None, 0
+    if M > 64:
+        nbytes = binding.linear_q8_workspace_size(M, N, K)
+        if nbytes:
+            ws = torch.empty(nbytes, dtype=_U8, device=dev)
     st = binding.load().mm_linear_q8(x.data_ptr(), x_scale.data_ptr(), W.data_ptr(), w_scale.data_ptr(), bias,
-                                     out.data_ptr(), M, N, K, epi, _stream(dev))
+                                     out.data_ptr(), M, N, K, epi, None if ws is None else ws.data_ptr(), nbytes,
+                                     _stream(dev))
     if st:
         binding.check(st, "mm_linear_q8")
     return out

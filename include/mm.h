@@ -295,10 +295,16 @@ mm_status mm_linear_w4(const void* x, const void* W, const void* scales, const v
  *   out[M][N] = epi(x_scale[m] w_scale[n] (x . W^T) + bias), bf16 (RNE)
  *   x [M][K], W [N][K] e4m3 (OCP), K contiguous and a multiple of 16, at most
  *   2^22;  x_scale [M], w_scale [N] fp32.
- * fp32 sums; the scales multiply the sum, then the epilogue, then one rounding. */
+ * fp32 sums; the scales multiply the sum, then the epilogue, then one rounding.
+ * With a workspace (NULL: without), of the size the function below reports
+ * (host arithmetic only; 0: the shape runs without one), a product of few
+ * output tiles has its K cut into chunks, whose fp32 sums a second kernel adds
+ * in k order.  The workspace is 16-byte aligned, holds anything before, and
+ * two calls in flight at once must not share it. */
 mm_status mm_linear_q8(const void* x, const float* x_scale, const void* W, const float* w_scale,
                        const void* bias, void* out, int64_t M, int64_t N, int64_t K, mm_epilogue epi,
-                       void* stream);
+                       void* workspace, int64_t workspace_bytes, void* stream);
+mm_status mm_linear_q8_workspace_size(int64_t M, int64_t N, int64_t K, int64_t* bytes);
 
 /* Tile configuration override, parsed from a string such as
  *   "BM=256,BN=256,WM=2,WN=2,G=8,XCD=1,KALT=1,GRID=0"

@@ -133,17 +133,28 @@ def test_w4_refusals(lib):
 
 
 def test_q8_refusals(lib):
-    def q8(x=P[0], xs=P[1], W=P[2], ws=P[3], b=P[4], out=P[5], M=4, N=64, K=128, epi=3):
-        return lib.mm_linear_q8(x, xs, W, ws, b, out, M, N, K, epi, None)
+    def q8(x=P[0], xs=P[1], W=P[2], ws=P[3], b=P[4], out=P[5], M=4, N=64, K=128, epi=3, work=NULL, nbytes=0):
+        return lib.mm_linear_q8(x, xs, W, ws, b, out, M, N, K, epi, work, nbytes, None)
 
     for bad in (dict(x=NULL), dict(xs=NULL), dict(W=NULL), dict(ws=NULL), dict(b=NULL), dict(out=NULL), dict(N=-1),
-                dict(epi=4), dict(out=P[0]), dict(out=P[1]), dict(out=P[2] + 64), dict(out=P[3]), dict(out=P[4])):
+                dict(epi=4), dict(out=P[0]), dict(out=P[1]), dict(out=P[2] + 64), dict(out=P[3]), dict(out=P[4]), dict(nbytes=-1),
+                dict(work=P[5], nbytes=4096), dict(work=P[0], nbytes=4096), dict(work=P[3], nbytes=4096),
+                dict(work=P[6], nbytes=16, M=128, N=512, K=8192)):
         assert q8(**bad) == INVALID, bad
     for bad in (dict(K=(1 << 22) + 16), dict(N=1 << 31)):
         assert q8(**bad) == UNSUPPORTED, bad
     for bad in (dict(K=120), dict(x=P[0] + 8), dict(W=P[2] + 4), dict(xs=P[1] + 2), dict(out=P[5] + 1)):
         assert q8(**bad) == MISALIGNED, bad
+    assert q8(work=P[6] + 4, nbytes=1 << 40, M=128, N=512, K=8192) == MISALIGNED
     assert q8(M=0, x=NULL) == binding.MM_OK and q8(N=0) == binding.MM_OK
+    n = ctypes.c_int64(5)
+    assert lib.mm_linear_q8_workspace_size(4, 64, 128, ctypes.byref(n)) == binding.MM_OK and n.value == 0
+    assert lib.mm_linear_q8_workspace_size(8192, 8192, 8192, ctypes.byref(n)) == binding.MM_OK and n.value == 0
+    # 4 tiles of 128 x 128 in 8 chunks
+    assert lib.mm_linear_q8_workspace_size(128, 512, 8192, ctypes.byref(n)) == binding.MM_OK
+    assert n.value == 4 * 8 * 128 * 128 * 4
+    assert lib.mm_linear_q8_workspace_size(-1, 64, 128, ctypes.byref(n)) == INVALID
+    assert lib.mm_linear_q8_workspace_size(4, 64, 128, None) == INVALID
 
 
 def test_python_checks_types_and_devices():

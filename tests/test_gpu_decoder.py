@@ -10,6 +10,7 @@ import torch
 
 import dense_bf16_gemm_amd as mm
 import decoder_ref as ref
+from dense_bf16_gemm_amd import binding
 
 pytestmark = pytest.mark.gpu
 
@@ -330,7 +331,11 @@ def q8_inputs(M, N, K, seed, exact=False):
 
 Q8 = [(1, 1, 16), (1, 64, 128), (1, 3001, 2048), (2, 65, 144), (7, 130, 1008), (16, 333, 1024), (17, 47, 2064),
       (32, 129, 640), (33, 64, 384), (64, 515, 1280), (65, 128, 256), (100, 200, 16), (128, 128, 128),
-      (129, 131, 400), (255, 257, 1040), (256, 256, 1024), (300, 700, 272), (513, 300, 528), (700, 1030, 640)]
+      (129, 131, 400), (255, 257, 1040), (256, 256, 1024), (300, 700, 272), (513, 300, 528), (700, 1030, 640),
+      # K cut into chunks (the last one shorter, and ragged)
+      (70, 1001, 4096), (130, 300, 4112), (256, 512, 1296), (1000, 520, 2064),
+      # each kind of tile, several tiles per workgroup, ragged edges
+      (2050, 2056, 144), (3000, 4100, 272), (1030, 9001, 400)]
 
 
 @pytest.mark.parametrize("M,N,K", Q8)
@@ -342,6 +347,18 @@ def test_linear_q8_exact(dev, M, N, K):
     intact()
     want = ((x.double() @ W.double().t()) * xs.double()[:, None] * ws.double()).float().bfloat16()
     assert torch.equal(got.cpu(), want)
+
+
+def test_linear_q8_without_a_workspace(dev):
+    """The same product uncut: equal to fp32 rounding, here exactly (whole numbers)."""
+    M, N, K = 130, 300, 4112
+    x, xs, W, ws, _ = q8_inputs(M, N, K, 6, exact=True)
+    assert binding.linear_q8_workspace_size(M, N, K) > 0
+    args = on(dev, x, xs, W, ws)
+    out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    binding.check(binding.load().mm_linear_q8(*(t.data_ptr() for t in args), None, out.data_ptr(), M, N, K, 0, None, 0,
+                                              torch.cuda.current_stream().cuda_stream), "mm_linear_q8")
+    assert torch.equal(out, mm.linear_q8(*args))
 
 
 @pytest.mark.parametrize("M,N,K,epi", [
