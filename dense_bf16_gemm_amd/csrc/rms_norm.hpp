@@ -197,8 +197,11 @@ __global__ void __launch_bounds__(1024) rms_norm(RmsNormParams p) {
 //
 // A row's vectors are held as stored and widened where they are used, which
 // keeps four vectors per thread within the 128 registers of 1024 threads.
-template <bool F32, int VPT>
-__global__ void __launch_bounds__(1024) rms_norm_grad(RmsNormGradParams p) {
+// AHEAD (up to 512 threads): a row's loads are issued while the row before is
+// summed.  8192 x 4096 bf16 with dres: 58.0 us (4.63 TB/s); 63.6 without AHEAD,
+// on twice the workgroups and so with twice the parts of dw to write and add.
+template <bool F32, int VPT, bool AHEAD>
+__global__ void __launch_bounds__(AHEAD ? 512 : 1024) rms_norm_grad(RmsNormGradParams p) {
   __shared__ float slot[2][16];
   const int T = blockDim.x;
   const int vectors = p.hidden >> 3;
@@ -211,31 +214,46 @@ __global__ void __launch_bounds__(1024) rms_norm_grad(RmsNormGradParams p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
     w[i].clear();
-    if (c < vectors) w[i].load(p.weight, 8 * c);
+    if (AHEAD && c < vectors) w[i].load(p.weight, 8 * c);
   }
-  int turn = 0;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const float r = p.rstd[row];
-    Raw8<F32> h[VPT];
+  const bool has_dres = p.dres != nullptr;
+  struct Row {
+    Raw8<F32> h[VPT], dres[VPT];
     Raw8<false> dy[VPT];
-    float dot = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) asm volatile("" : "+v"(w[i].w[0]));  // (widened here, not once before the loop)
+    float rstd;
+  };
+  auto load = [&](int64_t row, Row& v) __attribute__((always_inline)) {
+    v.rstd = p.rstd[row];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = threadIdx.x + i * T;
-      h[i].clear();
-      dy[i].clear();
       if (c < vectors) {
-        h[i].load(p.h, row * p.hidden + 8 * c);
-        dy[i].load(p.dy, row * p.hidden + 8 * c);
+        v.h[i].load(p.h, row * p.hidden + 8 * c);
+        v.dy[i].load(p.dy, row * p.hidden + 8 * c);
+        if constexpr (AHEAD) {
+          if (has_dres) v.dres[i].load(p.dres, row * p.hidden + 8 * c);
+        }
+      } else {
+        v.h[i].clear();
+        v.dy[i].clear();
+        if constexpr (AHEAD) v.dres[i].clear();
       }
     }
+  };
+  auto process = [&](int64_t row, Row& v, int turn) __attribute__((always_inline)) {
+    const float r = v.rstd;
+    float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
+      // (in registers and widened here, not once before the loop; or, where
+      // registers are short, read again)
+      if constexpr (AHEAD)
+        settle(w[i].w[0]);
+      else if ((int)threadIdx.x + i * T < vectors)
+        w[i].load(p.weight, 8 * (threadIdx.x + i * T));
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float t = dy[i][j] * (h[i][j] * r);
+        const float t = v.dy[i][j] * (v.h[i][j] * r);
         dw[i][j] += t;
         dot = __builtin_fmaf(t, w[i][j], dot);
       }
@@ -243,21 +261,44 @@ __global__ void __launch_bounds__(1024) rms_norm_grad(RmsNormGradParams p) {
     // two slot rows in turn: a wave may start the next row's sum while
     // another still reads this one's
     const float mean = block_sum(dot, slot[turn]) * inv_n;
-    turn ^= 1;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = threadIdx.x + i * T;
+      // (widened again, not kept across the sum)
+      settle(v.dy[i].w[0]);
+      settle(w[i].w[0]);
+#pragma unroll
+      for (int q = 0; q < (F32 ? 2 : 1); ++q) settle(v.h[i].w[q]);
       if (c >= vectors) continue;
       float o[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = r * (dy[i][j] * w[i][j] - h[i][j] * r * mean);
-      if (p.dres) {
-        float d[8];
-        load8<F32>(p.dres, row * p.hidden + 8 * c, d);
+      for (int j = 0; j < 8; ++j) o[j] = r * (v.dy[i][j] * w[i][j] - v.h[i][j] * r * mean);
+      if (has_dres) {
+        if constexpr (!AHEAD) v.dres[i].load(p.dres, row * p.hidden + 8 * c);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] += d[j];
+        for (int j = 0; j < 8; ++j) o[j] += v.dres[i][j];
       }
       store8<F32>(p.dh, row * p.hidden + 8 * c, o);
+    }
+  };
+  if constexpr (AHEAD) {
+    // the next row's loads go out before this row's sum is waited for
+    Row a, b;
+    const int64_t G = gridDim.x, last = p.rows - 1;
+    load(blockIdx.x, a);
+    for (int64_t row = blockIdx.x; row < p.rows; row += 2 * G) {
+      load(min(row + G, last), b);
+      process(row, a, 0);
+      load(min(row + 2 * G, last), a);
+      if (row + G < p.rows) process(row + G, b, 1);
+    }
+  } else {
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+      Row a;
+      load(row, a);
+      process(row, a, turn);
+      turn ^= 1;
     }
   }
 #pragma unroll
