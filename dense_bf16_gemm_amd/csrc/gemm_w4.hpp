@@ -74,7 +74,8 @@ __device__ __forceinline__ float w4_dot(const W4Params& p, int m, int n) {
 }
 
 // XR activation rows (4: the first four of a block of 16, whose others are
-// never used) by NB blocks of 16 columns per workgroup.  Its WV waves take
+// never used; 16, 32, 48 or 64: 37 rows take 14.0 us at 3001 x 4104 as 48 and
+// 16.4 as 64) by NB blocks of 16 columns per workgroup.  Its WV waves take
 // every WV-th 128-k step, each step's loads issued one step ahead, and their
 // sums meet in LDS, added in wave order.  No barrier until then: what a wave
 // stages in LDS is its own.
@@ -89,27 +90,38 @@ __device__ __forceinline__ float w4_dot(const W4Params& p, int m, int n) {
 // offset -(16 + z), and leaves the pairs in LDS, from where the lanes of each
 // column read theirs (a load per column block and group would cost more of
 // the address unit than the weight does).
+//
+// Measured: 16 x 28672 x 8192 28.4 us, 4.2 TB/s of weight (a large copy runs at
+// 4.8, and the floor is 26 us); 1 x 4096 x 4096 4.1 us, where the launch and the
+// one step's latency are most of it.  From 33 rows on the vector ALU bounds it
+// (the nibbles' widening and two FMAs per output and group) together with the
+// activations, which every workgroup fetches from L2: 64 x 14336 x 4096 18.3 us
+// against a floor of 7.
 template <int XR, int NB, int G, int WV>
 __global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
   constexpr int MB = XR < 16 ? 1 : XR / 16;
   constexpr int AB = MB * NB;
   constexpr int GP = 128 / G;             // groups per step
-  constexpr int SLOTS = XR < 64 ? 2 : 1;  // tiles of activations in LDS per wave
+  // HALVES: the two LDS tiles of a wave are the halves (64 k) of one step, not
+  // two steps: half the LDS and half the fragment registers, so that two
+  // workgroups of 48 or 64 rows fit a CU
+  constexpr bool HALVES = XR >= 48;
   // a chunk: what shares one scale and one pass over the accumulators; JC
   // MFMAs, whose fragments are read JR at a time
-  constexpr int JC = (SLOTS == 1 && G > 64 ? 64 : G) / 32;
-  constexpr int JR = SLOTS == 1 ? 2 : JC;
+  constexpr int JC = (HALVES && G > 64 ? 64 : G) / 32;
+  constexpr int JR = HALVES ? 2 : JC;
   // The compiler would start all of a step's products at once.  Where that
   // takes more registers than there are (or than the waves of two workgroups
   // share), a column block's products wait for those BB blocks before.
-  constexpr bool CALM = MB == 4 || AB * GP > (MB == 2 ? 16 : 4);
-  constexpr int BB = MB < 4 && NB > 1 ? 2 : 1;
-  constexpr int XC = XR / 4;    // copies per step: four rows of 256 bytes each
+  constexpr bool CALM = MB >= 3 || AB * GP > (MB == 2 ? 16 : 4);
+  constexpr int BB = MB < 3 && NB > 1 ? 2 : 1;
+  // copies per tile: four rows of 256 bytes each, or eight of 128
+  constexpr int XC = HALVES ? XR / 8 : XR / 4, XT = XC * 1024;
   // scale pairs: a column's GP * NB, in an odd number of 16-byte units (reads
   // of 16 columns then fall in 16 bank groups)
   constexpr int PB = GP * NB, SU = PB < 2 ? 1 : (PB / 2) | 1;
   constexpr int kSc = 16 * SU * 16;
-  constexpr int kX = SLOTS * XR * 256, kWave = kX + kSc;  // LDS bytes per wave
+  constexpr int kX = 2 * XT, kWave = kX + kSc;  // LDS bytes per wave
   constexpr int RS = AB > 8 ? WV / 2 : WV;  // waves whose sums are in LDS at once
   constexpr int kRed = RS * AB * 1024;
   __shared__ __attribute__((aligned(1024))) char smem[WV * kWave > kRed ? WV * kWave : kRed];
@@ -130,12 +142,14 @@ __global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
   const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint16_t*>(p.x + (int64_t)m0 * p.K), (short)0, (int)((uint32_t)min(p.M - m0, XR) * row_bytes),
       0x00020000);
-  uint32_t voff[XC], tail[XC < 4 ? XC : 4];
+  constexpr int kTails = HALVES ? 2 : XC < 4 ? XC : 4;
+  uint32_t voff[XC], tail[kTails];
 #pragma unroll
   for (int i = 0; i < XC; ++i) {
-    const int r = 4 * i + lg, chunk = lx ^ (r & 15);
+    const int r = HALVES ? 8 * i + (lane >> 3) : 4 * i + lg;
+    const int chunk = HALVES ? (lane & 7) ^ (lane >> 3) : lx ^ (r & 15);
     voff[i] = (uint32_t)r * row_bytes + 16u * (uint32_t)chunk;
-    if (i < 4) tail[i] = (kblocks - 1) * 128 + 8 * chunk < p.K ? 0u : 0x80000000u;
+    if (i < kTails) tail[i] = (kblocks - 1) * 128 + 8 * chunk + (HALVES ? 64 * i : 0) < p.K ? 0u : 0x80000000u;
   }
   // scales: lane (group sg of the step, columns sn .. sn + 3); lanes past the
   // step's groups repeat earlier ones.  The last columns' loads start early
@@ -151,11 +165,13 @@ __global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
     uint64_t s;  // four bf16
     uint32_t z;
   };
-  auto copy = [&](int kb, int slot) __attribute__((always_inline)) {
+  // tile: of step kb, or (HALVES) half `tile` of it
+  auto copy = [&](int kb, int tile) __attribute__((always_inline)) {
     const bool last = kb == kblocks - 1;
 #pragma unroll
     for (int i = 0; i < XC; ++i)
-      copy_to_lds(rx, xs + slot * (XR * 256) + i * 1024, voff[i] | (last ? tail[i & 3] : 0u), (uint32_t)kb * 256u);
+      copy_to_lds(rx, xs + tile * XT + i * 1024, voff[i] | (last ? tail[HALVES ? tile : i & 3] : 0u),
+                  (uint32_t)kb * 256u + (HALVES ? 128u * (uint32_t)tile : 0u));
   };
   auto load = [&](int kb, Step& t) __attribute__((always_inline)) {
     const int group = min(kb * GP + sg, groups - 1);
@@ -176,21 +192,24 @@ __global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
   uint32_t mask = 0x00780078u, sixteen = 0x41804180u;
   keep_in_registers(mask, sixteen);
 
-  // Step kb, and the loads of the wave's next.  Two slots: the next step's
+  // Step kb, and the loads of the wave's next.  Whole steps: the next one's
   // copies go out first (loads arrive in order, so once a step's weights are
-  // there its activations are).  One slot (64 rows): the next step's weights
-  // go out first, its copies once this step's last fragments are in registers.
-  auto step = [&](int kb, int slot, Step& t, Step& next) __attribute__((always_inline)) {
+  // there its activations are).  Halves: the next step's weights go out first,
+  // the copies of each half once this step's fragments of it are in registers;
+  // so what a wait may leave in flight are the loads issued after its half.
+  constexpr int kLoads = NB + 2;
+  auto step = [&](int kb, int tile, Step& t, Step& next) __attribute__((always_inline)) {
     const int kn = min(kb + WV, kblocks - 1);
-    if constexpr (SLOTS == 2) {
-      copy(kn, slot ^ 1);
+    if constexpr (HALVES) {
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(XC));
+      order();
+      load(kn, next);
+      order();
+    } else {
+      copy(kn, tile ^ 1);
       load(kn, next);
 #pragma unroll
       for (int b = 0; b < NB; ++b) arrived(t.w[b]);
-    } else {
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
-      order();
-      load(kn, next);
     }
     // (a group past K has no activations: scale 0, whatever the last group's is)
     const uint64_t s = kb * GP + sg < groups ? t.s >> (2 * shift) : 0u;
@@ -203,24 +222,30 @@ __global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
           f32x2{__builtin_bit_cast(float, bits), -16.0f - (float)((z >> (8 * i)) & 255u)};
     }
     order();  // (a wave's LDS operations run in order)
-    const char* xt = xs + (SLOTS == 2 ? slot * (XR * 256) : 0);
     f32x4 so = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int r = 0; r < 4 / JR; ++r) {
+      if (HALVES && r == 1) {
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(kLoads + XC));
+        order();
+      }
+      const char* xt = xs + (HALVES ? r : tile) * XT;
       u32x4 x[MB][JR];
 #pragma unroll
       for (int a = 0; a < MB; ++a)
 #pragma unroll
         for (int j = 0; j < JR; ++j) {
           const int row = XR < 16 ? lx & (XR - 1) : 16 * a + lx;
-          x[a][j] = *reinterpret_cast<const u32x4*>(xt + row * 256 + (((4 * (r * JR + j) + lg) ^ (row & 15)) << 4));
+          x[a][j] = *reinterpret_cast<const u32x4*>(
+              xt + (HALVES ? row * 128 + (((4 * j + lg) ^ (row & 7)) << 4)
+                           : row * 256 + (((4 * (r * JR + j) + lg) ^ (row & 15)) << 4)));
         }
-      if (r == 4 / JR - 1) {
-        // every read of the tile has returned before a copy into it is issued
-        // (two slots: at the next step's start)
+      // every read of a tile has returned before a copy into it is issued
+      // (whole steps: at the next one's start)
+      if (HALVES || r == 4 / JR - 1) {
         __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(63));
         order();
-        if constexpr (SLOTS == 1) copy(kn, 0);
+        if constexpr (HALVES) copy(kn, r);
       }
 #pragma unroll
       for (int c = 0; c < JR / JC; ++c) {
@@ -282,8 +307,15 @@ __global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
     // (past its last step a wave loads the last one of all again, unused: the
     // loop then has one shape, and its waits count loads exactly)
     Step s0, s1;
-    copy(wave, 0);
-    load(wave, s0);
+    if constexpr (HALVES) {
+      load(wave, s0);
+      order();
+      copy(wave, 0);
+      copy(wave, 1);
+    } else {
+      copy(wave, 0);
+      load(wave, s0);
+    }
     for (int kb = wave; kb < kblocks; kb += 2 * WV) {
       step(kb, 0, s0, s1);
       if (kb + WV < kblocks) step(kb + WV, 1, s1, s0);

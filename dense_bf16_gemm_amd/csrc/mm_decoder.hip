@@ -156,6 +156,20 @@ mm_status check_product(int64_t M, int64_t N, int64_t K, const void* bias, const
   return MM_OK;
 }
 
+// Column blocks (1, 2 or 4 of 16 columns) per workgroup for few rows.  Each
+// workgroup reads all activations for itself, which costs about `share` tenths
+// of a block's weights, and the CU with the most workgroups ends last: the count
+// with the least of (workgroups to a CU, rounded up) x (blocks + share) is taken.
+int column_blocks(int64_t blocks, int64_t gy, int cus, int share) {
+  int best = 1;
+  int64_t cost = 0;
+  for (int nb = 1; nb <= 4; nb *= 2) {
+    const int64_t c = cdiv(cdiv(blocks, nb) * gy, cus) * (10 * nb + share);
+    if (nb == 1 || c < cost) best = nb, cost = c;
+  }
+  return best;
+}
+
 template <int XR, int NB>
 const void* w4_kernel(int group) {
   switch (group) {
@@ -173,6 +187,7 @@ const void* w4_kernel(int rows, int nb, int group) {
     case 4: return w4_kernel<4>(nb, group);
     case 16: return w4_kernel<16>(nb, group);
     case 32: return w4_kernel<32>(nb, group);
+    case 48: return w4_kernel<48>(nb, group);
   }
   return w4_kernel<64>(nb, group);
 }
@@ -388,15 +403,16 @@ mm_status mm_linear_w4(const void* x, const void* W, const void* scales, const v
     void* args[] = {&p};
     return launch(fn(&mmk::gemm_w4_narrow), dim3((unsigned)cdiv(M * N, 64)), 64, args, stream, "linear_w4 narrow");
   }
-  const int xr = M <= 4 ? 4 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
-  const int64_t blocks = cdiv(N, 16);
-  // Column blocks per workgroup: each workgroup reads the activations for
-  // itself, so as many as leave most CUs a workgroup.  Measured (us, 1 / 2 / 4
-  // blocks): 1 x 8192 x 8192 9.8 / 8.7 / 10.9, 16 x 14336 x 4096 15.9 / 11.5 /
-  // 9.6, 64 x 14336 x 4096 40 / 26 / 20, 37 x 3001 x 4104 12.4 / 14.4 / 19.3.
-  const int nb = blocks >= 800 ? 4 : blocks >= 400 ? 2 : 1;
+  const int xr = M <= 4 ? 4 : M <= 16 ? 16 : M <= 32 ? 32 : M <= 48 ? 48 : 64;
   const int64_t gy = cdiv(M, xr);
   if (gy > 65535) return fail(MM_ERR_UNSUPPORTED, "M too large");
+  // Measured (us, 1 / 2 / 4 column blocks): 1 x 4096 x 4096 4.1 / 5.1 / 6.7, 12 x
+  // 6000 x 4096 8.7 / 6.6 / 8.7, 24 x 8192 x 8192 23.8 / 16.7 / 18.7, 10 x 11000 x
+  // 4096 12.7 / 11.8 / 10.4, 64 x 14336 x 4096 39 / 26 / 20.
+  int cus = 0;
+  if ((s = device_cus(&cus)) != MM_OK) return s;
+  const int64_t blocks = cdiv(N, 16);
+  const int nb = column_blocks(blocks, gy, cus, 10);
   void* args[] = {&p};
   return launch(w4_kernel(xr, nb, (int)group), dim3((unsigned)cdiv(blocks, nb), (unsigned)gy), mmk::kW4Waves * 64, args,
                 stream, "linear_w4");
@@ -451,15 +467,17 @@ mm_status mm_linear_q8(const void* x, const float* x_scale, const void* W, const
   if (M <= kQ8Rows || K == 0) {
     const int xr = M <= 4 ? 4 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
     const int64_t blocks = cdiv(N, 16);
-    // Column blocks per workgroup.  Many small workgroups stream W best (1 x
-    // 28672 x 8192: 41.9 us with one block, 51.9 / 48.8 with 2 / 4), but each
-    // reads x for itself, and one of few steps is mostly its start and end (us,
-    // 1 / 2 / 4 blocks: 4 x 14336 x 4096 14.6 / 13.9 / 13.3; 16 x 8192 x 8192
-    // 13.9 / 16.2 / 20.0; 16 x 28672 x 8192 56.7 / 53.5 / 52.6; 64 x 8192 x 8192
-    // 23.2 / 18.2 / 25.2; 64 x 28672 x 8192 102 / 81 / 68).
-    const int nb = blocks < 400 || (M <= 4 && K >= 8192) || (M <= 16 && blocks < 800) ? 1 : blocks < 800 ? 2 : 4;
     const int64_t gy = cdiv(M, xr);
     if (gy > 65535) return fail(MM_ERR_UNSUPPORTED, "M too large");
+    // Few rows with at most two workgroups to a CU: one column block streams W
+    // best (us, 1 / 2 / 4 blocks: 16 x 8192 x 8192 13.9 / 16.2 / 20.0, though 12 x
+    // 6000 x 4096 9.3 / 8.6 / 12.6).  Otherwise by the shares of the CUs: 1 x 28672 x
+    // 8192 41.9 / 51.9 / 48.8, 16 x 14336 x 4096 15.1 / 14.4 / 13.6, 12 x 20000 x 8192
+    // 37.5 / 38.7 / 46.8, 24 x 20000 x 8192 47.0 / 42.6 / 50.0, 64 x 8192 x 8192
+    // 23.2 / 18.2 / 25.2, 64 x 28672 x 8192 102 / 82 / 68.
+    int cus = 0;
+    if ((s = device_cus(&cus)) != MM_OK) return s;
+    const int nb = M <= 16 && blocks <= 2 * cus ? 1 : column_blocks(blocks, gy, cus, M <= 4 ? 1 : M <= 16 ? 3 : 10);
     return launch(q8_rows_kernel(xr, nb), dim3((unsigned)cdiv(blocks, nb), (unsigned)gy), mmk::kW4Waves * 64, args, stream,
                   "linear_q8 rows");
   }
