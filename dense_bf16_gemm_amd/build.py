@@ -7,7 +7,8 @@ kept per source in ``_build/resource_usage*.txt`` next to this file.
 
 A second library, ``libmm_fullsync.so``, is built from the same sources with
 MM_DEBUG_FULL_SYNC: the slab kernel then drains every copy and waits at a
-barrier before each super-step.  It is a race check for the tests (its
+barrier before each super-step, and so do the kernels of 4-bit and 8-bit
+weights before each of their steps.  It is a race check for the tests (its
 results must equal libmm.so's bit for bit), never the product.
 """
 from __future__ import annotations

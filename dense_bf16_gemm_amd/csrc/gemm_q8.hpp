@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(WV * 64) gemm_q8_rows(Q8Params p) {
     const int sn = min(st + WV, ksteps - 1);
     copy(sn, slot ^ 1);
     load(sn, next);
+    race_check_drain();
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       arrived(t.w[b][0]);
@@ -433,6 +434,11 @@ __global__ void __launch_bounds__(256, FM * FN <= 4 ? 2 : 1) gemm_q8_tile(Q8Para
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
     for (int q = q0; q < q1; ++q) {
+#ifdef MM_DEBUG_FULL_SYNC
+      race_check_drain();  // every copy issued so far has landed, for every wave
+      __builtin_amdgcn_s_barrier();
+      order();
+#endif
       // step 0
 #pragma unroll
       for (int a = 0; a < FM; ++a) x[1][a] = frag_x(a, xb, 1);

@@ -74,8 +74,8 @@ __device__ __forceinline__ float w4_dot(const W4Params& p, int m, int n) {
 }
 
 // XR activation rows (4: the first four of a block of 16, whose others are
-// never used; 16, 32, 48 or 64: 37 rows take 14.0 us at 3001 x 4104 as 48 and
-// 16.4 as 64) by NB blocks of 16 columns per workgroup.  Its WV waves take
+// never used; 16, 32, 48 or 64: 48 rows by 14336 x 4096 take 16.9 us as 48 and
+// 19.5 as 64) by NB blocks of 16 columns per workgroup.  Its WV waves take
 // every WV-th 128-k step, each step's loads issued one step ahead, and their
 // sums meet in LDS, added in wave order.  No barrier until then: what a wave
 // stages in LDS is its own.
@@ -205,9 +205,11 @@ __global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
       order();
       load(kn, next);
       order();
+      race_check_drain();
     } else {
       copy(kn, tile ^ 1);
       load(kn, next);
+      race_check_drain();
 #pragma unroll
       for (int b = 0; b < NB; ++b) arrived(t.w[b]);
     }
@@ -228,6 +230,7 @@ __global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
       if (HALVES && r == 1) {
         __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(kLoads + XC));
         order();
+        race_check_drain();
       }
       const char* xt = xs + (HALVES ? r : tile) * XT;
       u32x4 x[MB][JR];

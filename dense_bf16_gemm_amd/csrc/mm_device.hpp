@@ -69,6 +69,16 @@ __device__ __forceinline__ void settle(u32x4& v) { asm volatile("" : "+v"(v)); }
 // The value of a load is there before anything after this point runs:
 __device__ __forceinline__ void arrived(u32x4 v) { asm volatile("" ::"v"(v) : "memory"); }
 
+// Nothing, and in the race-check build (MM_DEBUG_FULL_SYNC) a wait for every
+// load, copy and LDS operation of the wave: where a kernel's own waits let some
+// stay in flight.
+__device__ __forceinline__ void race_check_drain() {
+#ifdef MM_DEBUG_FULL_SYNC
+  __builtin_amdgcn_s_waitcnt(0);
+  order();
+#endif
+}
+
 // A 16-byte read of LDS.  The restrict parameter tells the compiler that no copy
 // in flight writes what is read (the kernel's waits and barriers see to it);
 // without it, it waits for every copy before reads it cannot tell apart.
