@@ -265,15 +265,19 @@ __device__ __forceinline__ void q8_block(const Q8Params& p, float (&v)[16], floa
 // (v_mfma_f32_32x32x64_f8f6f4: 64 cycles, twice the bf16 rate).
 //
 // K runs in super-steps of 128 (whole lines of both operands), two MFMA steps
-// of 64 each, through three LDS slots of x and two of W (all 160 KiB at 256 x
-// 256).  During step 0 of super-step q the wave multiplies fragments that it
-// read before, and reads those of step 1; then one wait and barrier: every wave
-// has read all of q's slots, and q + 1 has landed everywhere.  During step 1 it
-// reads the first fragments of q + 1 and issues the copies of W for q + 2 and
-// of x for q + 3 into q's slots.  So no MFMA waits on an LDS read, and a copy
-// has 1.5 (W) or 2.5 (x) super-steps of 2048 cycles to land (with two slots
-// each, and one super-step, the same loop took 458 us at 8192^3).  The copies
-// run on into the workgroup's next tile, which arrives during the epilogue.
+// of 64 each, through SX LDS slots of x and SW of W.  During step 0 of super-step
+// q the wave multiplies fragments that it read before, and reads those of step
+// 1; then one wait and barrier: every wave has read all of q's slots, and q + 1
+// has landed everywhere.  During step 1 it reads the first fragments of q + 1
+// and issues the copies of W for q + SW and of x for q + SX into q's slots.  So no
+// MFMA waits on an LDS read, and a copy has SX - 1/2 (SW - 1/2) super-steps to
+// land.  256 x 256 tiles fill the LDS with 3 and 2 slots (with two each the loop
+// took 458 us at 8192^3).  What bounds the smaller tiles is the bytes in flight per
+// CU, and the 10 to 13 TB/s that all of them get out of L2; those for
+// products with few tiles take the LDS of a whole CU for their rings: 256 x 8192 x
+// 4096 33.1 us with 128 x 128 tiles of 3 and 2 slots, 25.6 with 5 each, 20.8 with
+// 128 x 64 tiles of 6 each.  The copies run on into the workgroup's next tile,
+// which arrives during the epilogue.
 //
 // LDS rows of 128 bytes, chunk c (16 bytes) at position c ^ (row / 2 & 7): a
 // fragment read of 32 rows then hits every bank once in each of its four
@@ -283,12 +287,15 @@ __device__ __forceinline__ void q8_block(const Q8Params& p, float (&v)[16], floa
 // 8 (i / 4 % 2) + 4 (i / 8 % 2) + i % 4, which makes those sums two runs of 8
 // columns, the runs of the two lanes of a row side by side.
 // SPLIT: the instance for a K cut into chunks.
-template <int FM, int FN, bool SPLIT>
-__global__ void __launch_bounds__(256, FM * FN <= 4 ? 2 : 1) gemm_q8_tile(Q8Params p) {
+template <int FM, int FN, int SX, int SW, bool SPLIT>
+__global__ void __launch_bounds__(256, SX * FM + SW * FN <= 10 ? 2 : 1) gemm_q8_tile(Q8Params p) {
   constexpr int BM = 64 * FM, BN = 64 * FN, XS = BM * 128, WS = BN * 128;
   constexpr int CX = 2 * FM, CW = 2 * FN;  // copies of 8 rows per wave and super-step
+  // copies that a wait for a super-step may leave in flight: those issued after
+  // the later of its own
+  constexpr int kAhead = SX <= SW ? (SX - 2) * (CX + CW) : CX + (SW - 2) * (CX + CW);
   constexpr int PER = (CX + CW + FM * FN - 1) / (FM * FN);  // copies (and fragment reads) per MFMA of a step
-  __shared__ __attribute__((aligned(1024))) char smem[3 * XS + 2 * WS];
+  __shared__ __attribute__((aligned(1024))) char smem[SX * XS + SW * WS];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l32 = lane & 31, h = lane >> 5;
@@ -377,7 +384,7 @@ __global__ void __launch_bounds__(256, FM * FN <= 4 ? 2 : 1) gemm_q8_tile(Q8Para
     copy_to_lds(rx, smem + slot * XS + (wave * CX + c) * 1024, vx[c], 128u * (uint32_t)xq);
   };
   auto copy_w = [&](int c, int slot) __attribute__((always_inline)) {
-    copy_to_lds(rw, smem + 3 * XS + slot * WS + (wave * CW + c) * 1024, vw[c], 128u * (uint32_t)wq);
+    copy_to_lds(rw, smem + SX * XS + slot * WS + (wave * CW + c) * 1024, vw[c], 128u * (uint32_t)wq);
   };
 
   // fragments: chunks 4 s + 2 j + h of a row, j = 0, 1
@@ -394,7 +401,7 @@ __global__ void __launch_bounds__(256, FM * FN <= 4 ? 2 : 1) gemm_q8_tile(Q8Para
     return frag(slot * XS + (wm + 32 * a) * 128, s);
   };
   auto frag_w = [&](int b, int slot, int s) __attribute__((always_inline)) {
-    return frag(3 * XS + slot * WS + (wn + 32 * b) * 128, s);
+    return frag(SX * XS + slot * WS + (wn + 32 * b) * 128, s);
   };
 
   enter_x();
@@ -404,17 +411,19 @@ __global__ void __launch_bounds__(256, FM * FN <= 4 ? 2 : 1) gemm_q8_tile(Q8Para
     toggle_w();
   }
 #pragma unroll
-  for (int q = 0; q < 3; ++q) {
-    if (q > 0) advance_x();
-    if (q == 1) advance_w();
-    if (q < 2) {
+  for (int q = 0; q < max(SX, SW); ++q) {
+    if (q > 0 && q < SW) advance_w();
+    if (q > 0 && q < SX) advance_x();
+    if (q < SW) {
 #pragma unroll
       for (int c = 0; c < CW; ++c) copy_w(c, q);
     }
+    if (q < SX) {
 #pragma unroll
-    for (int c = 0; c < CX; ++c) copy_x(c, q);
+      for (int c = 0; c < CX; ++c) copy_x(c, q);
+    }
   }
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(2 * CX + CW));
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((SX - 1) * CX + (SW - 1) * CW));
   order();
   __builtin_amdgcn_s_barrier();
   order();
@@ -455,7 +464,7 @@ __global__ void __launch_bounds__(256, FM * FN <= 4 ? 2 : 1) gemm_q8_tile(Q8Para
         __builtin_amdgcn_sched_group_barrier(0x100, 2 * PER, 0);     // LDS reads
       }
       __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(CX));
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(kAhead));
       order();
       __builtin_amdgcn_s_barrier();
       order();
@@ -463,7 +472,7 @@ __global__ void __launch_bounds__(256, FM * FN <= 4 ? 2 : 1) gemm_q8_tile(Q8Para
       // the scheduler, whose groups otherwise mix the two)
       advance_w();
       advance_x();
-      const int xn = xb == 2 ? 0 : xb + 1;
+      const int xn = xb == SX - 1 ? 0 : xb + 1, wnext = wb == SW - 1 ? 0 : wb + 1;
       // step 1.  The compiler keeps the order of copies and reads: a copy after
       // each fragment, the others after those.
       auto copy = [&](int c) __attribute__((always_inline)) {
@@ -477,7 +486,7 @@ __global__ void __launch_bounds__(256, FM * FN <= 4 ? 2 : 1) gemm_q8_tile(Q8Para
         if (i < FM)
           x[0][i] = frag_x(i, xn, 0);
         else
-          w[0][i - FM] = frag_w(i - FM, wb ^ 1, 0);
+          w[0][i - FM] = frag_w(i - FM, wnext, 0);
         copy(i);
       }
 #pragma unroll
@@ -499,7 +508,7 @@ __global__ void __launch_bounds__(256, FM * FN <= 4 ? 2 : 1) gemm_q8_tile(Q8Para
         __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
       }
       xb = xn;
-      wb ^= 1;
+      wb = wnext;
     }
 
     if constexpr (SPLIT) {

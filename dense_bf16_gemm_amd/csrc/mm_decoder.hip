@@ -207,6 +207,29 @@ const void* q8_rows_kernel(int rows, int nb) {
   return q8_rows_kernel<64>(nb);
 }
 
+template <int FM, int FN, int SX, int SW>
+const void* q8_tile_kernel(bool split) {
+  return split ? fn(&mmk::gemm_q8_tile<FM, FN, SX, SW, true>) : fn(&mmk::gemm_q8_tile<FM, FN, SX, SW, false>);
+}
+const void* q8_tile_kernel(int kind, bool split) {
+  switch (kind) {
+    case 0: return q8_tile_kernel<4, 4, 3, 2>(split);
+    case 1: return q8_tile_kernel<4, 2, 3, 4>(split);
+    case 2: return q8_tile_kernel<2, 2, 3, 2>(split);
+    case 3: return q8_tile_kernel<2, 2, 5, 5>(split);
+  }
+  return q8_tile_kernel<2, 1, 6, 6>(split);
+}
+const void* q8_join_kernel(int kind) {
+  switch (kind) {
+    case 0: return fn(&mmk::gemm_q8_join<4, 4>);
+    case 1: return fn(&mmk::gemm_q8_join<4, 2>);
+    case 2:
+    case 3: return fn(&mmk::gemm_q8_join<2, 2>);
+  }
+  return fn(&mmk::gemm_q8_join<2, 1>);
+}
+
 // ----------------------------------------------------------------------------
 // 8-bit products of more than kQ8Rows rows: the kind of tile, and whether K is
 // cut so that few tiles fill the GPU.
@@ -215,15 +238,19 @@ constexpr int64_t kQ8Rows = 64;
 constexpr int64_t kQ8MaxChunks = 8;
 constexpr int64_t kQ8Cus = 256;  // of the target GPU
 
-// A kind's cost is the time (us) of one 128-k super-step of a full GPU of
-// workgroups (measured at K = 8192: 4096 x 4096, 4096 x 2048, 2048 x 4096); a
-// partly filled GPU runs its tiles faster, down to 0.45 of that (128 tiles of
-// each kind: 0.73, 0.70 and 0.63 of it).
+// A kind's cost is the time (us) of one 128-k super-step with every CU at work
+// and with few (`low`); operands from HBM.  A small tile reads more per product,
+// but its ring holds more super-steps (us, the kinds in turn, K whole or in the
+// chunks that suit each best): 4096 x 4096 x 4096 61.6 / 70.7 / 69.3 / 81.1 / 105;
+// 2048 x 3008 x 4096 44.2 / 34.3 / 39.3 / 42.2 / 45.5; 6000 x 6000 x 4096 159 /
+// 157 / 151 / 176 / 236; 1024 x 4096 x 4096 38.2 / 32.9 / 32.3 / 25.4 / 32.0; 256 x 8192
+// x 4096 55 / 27.5 / 26.1 / 24.3 / 20.8.
 struct Q8Kind {
   int fm, fn, resident;  // tile of 64 fm x 64 fn, workgroups per CU
-  double step;
+  double step, low;
 };
-constexpr Q8Kind kQ8Kinds[] = {{4, 4, 1, 1.90}, {4, 2, 1, 1.16}, {2, 2, 2, 1.09}};
+constexpr Q8Kind kQ8Kinds[] = {
+    {4, 4, 1, 1.72, 1.30}, {4, 2, 1, 1.12, 0.72}, {2, 2, 2, 1.12, 0.75}, {2, 2, 1, 0.66, 0.60}, {2, 1, 1, 0.52, 0.43}};
 
 struct Q8Plan {
   int kind = 0;
@@ -240,7 +267,7 @@ Q8Plan q8_plan(int64_t M, int64_t N, int64_t K, int64_t max_chunks) {
   const int64_t steps = cdiv(K, 128);
   Q8Plan best;
   double bc = -1.0;
-  for (int kind = 0; kind < 3; ++kind) {
+  for (int kind = 0; kind < (int)std::size(kQ8Kinds); ++kind) {
     const Q8Kind& k = kQ8Kinds[kind];
     Q8Plan p;
     p.kind = kind;
@@ -252,11 +279,13 @@ Q8Plan q8_plan(int64_t M, int64_t N, int64_t K, int64_t max_chunks) {
       if (p.chunks != c || (c > 1 && p.chunk_steps < 4)) continue;
       const int64_t units = p.tiles_m * p.tiles_n * c, slots = kQ8Cus * k.resident;
       const int64_t rem = units % slots;
-      const double passes = (double)(units / slots) + (rem ? 0.45 + 0.55 * (double)rem / (double)slots : 0.0);
+      const double pass =
+          (double)(units / slots) * k.step + (rem ? k.low + (k.step - k.low) * (double)rem / (double)slots : 0.0);
       // per pass, a start and an end worth about four super-steps
-      double cost = passes * k.step * (double)(p.chunk_steps + 4);
-      // the chunks' sums written and read at about 4 TB/s, and a second launch
-      if (c > 1) cost += 2.0 * (double)q8_ws_bytes(p) / 4e6 + 4.0;
+      double cost = pass * (double)(p.chunk_steps + 4);
+      // the chunks' sums written and read (they stay in the cache behind L2), and
+      // a second launch
+      if (c > 1) cost += 2.0 * (double)q8_ws_bytes(p) / 8e6 + 3.0;
       if (bc < 0.0 || cost < bc) {
         bc = cost;
         best = p;
@@ -499,15 +528,11 @@ mm_status mm_linear_q8(const void* x, const float* x_scale, const void* W, const
   const int64_t units = plan.tiles_m * plan.tiles_n * plan.chunks;
   const int64_t grid = std::min<int64_t>(units, (int64_t)cus * kQ8Kinds[plan.kind].resident);
   const bool split = plan.chunks > 1;
-  s = launch(plan.kind == 0   ? (split ? fn(&mmk::gemm_q8_tile<4, 4, true>) : fn(&mmk::gemm_q8_tile<4, 4, false>))
-             : plan.kind == 1 ? (split ? fn(&mmk::gemm_q8_tile<4, 2, true>) : fn(&mmk::gemm_q8_tile<4, 2, false>))
-                              : (split ? fn(&mmk::gemm_q8_tile<2, 2, true>) : fn(&mmk::gemm_q8_tile<2, 2, false>)),
+  s = launch(q8_tile_kernel(plan.kind, split),
              dim3((unsigned)grid), 256, args, stream, "linear_q8 tiles");
   if (s != MM_OK || !split) return s;
   const int64_t blocks = plan.tiles_m * plan.tiles_n * kQ8Kinds[plan.kind].fm * kQ8Kinds[plan.kind].fn;
-  return launch(plan.kind == 0   ? fn(&mmk::gemm_q8_join<4, 4>)
-                : plan.kind == 1 ? fn(&mmk::gemm_q8_join<4, 2>)
-                                 : fn(&mmk::gemm_q8_join<2, 2>),
+  return launch(q8_join_kernel(plan.kind),
                 dim3((unsigned)blocks), 256, args, stream, "linear_q8 join");
 }
 

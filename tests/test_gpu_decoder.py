@@ -349,6 +349,21 @@ def test_linear_q8_exact(dev, M, N, K):
     assert torch.equal(got.cpu(), want)
 
 
+@pytest.mark.parametrize("M,N,K", [
+    # 256 x 256 tiles whole and in chunks, 256 x 128, 128 x 128 with short and with
+    # long rings, 128 x 64
+    (129, 36981, 144), (144, 10898, 9344), (142, 21458, 144), (11208, 70, 8368), (79, 33206, 144), (67, 16681, 5248),
+    (16393, 66, 144), (6389, 69, 3360), (67, 71, 144), (71, 66, 1616)])
+def test_linear_q8_every_tile_exact(dev, M, N, K):
+    x, xs, W, ws, _ = q8_inputs(M, N, K, M + N + K, exact=True)
+    out, intact = guarded((M, N), torch.bfloat16, dev)
+    got = mm.linear_q8(*on(dev, x, xs, W, ws), out=out)
+    intact()
+    # (sums of at most 16 K: exact in fp32)
+    want = ((x.float() @ W.float().t()) * xs[:, None] * ws).bfloat16()
+    assert torch.equal(got.cpu(), want)
+
+
 def test_linear_q8_without_a_workspace(dev):
     """The same product uncut: equal to fp32 rounding, here exactly (whole numbers)."""
     M, N, K = 130, 300, 4112

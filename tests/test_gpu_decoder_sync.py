@@ -45,7 +45,8 @@ def test_linear_w4(libs, M, N, K, group, zeros):  # noqa: F811
     (1, 520, 8208, False), (4, 14000, 2048, False), (13, 1000, 4112, False), (32, 9600, 1040, False),
     (64, 9600, 2064, False), (50, 300, 8192, False),
     (70, 520, 16400, False), (70, 520, 16400, True), (300, 3001, 4112, True), (1100, 4200, 1040, True),
-    (2500, 8200, 272, False), (4096, 4096, 1024, True),
+    (2500, 8200, 272, False), (4096, 4096, 1024, True), (142, 21458, 1040, True), (11208, 70, 8368, True),
+    (67, 16681, 5248, True), (6389, 69, 3360, True), (16393, 66, 1040, False), (71, 66, 8016, True),
 ])
 def test_linear_q8(libs, M, N, K, ws):  # noqa: F811
     dev = torch.device("cuda:0")
