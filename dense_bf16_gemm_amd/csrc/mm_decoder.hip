@@ -493,7 +493,10 @@ mm_status mm_linear_q8(const void* x, const float* x_scale, const void* W, const
   p.K = (int)K;
   p.epi = epi;
   void* args[] = {&p};
-  if (M <= kQ8Rows || K == 0) {
+  // (33 to 64 rows by a wide weight: in the rows' kernel every 64 columns read the
+  // activations again; 64 x 28672 x 8192 68 us there, 59 as tiles, 60 x 11000 x 4096
+  // 20.2 and 19.3, 60 x 6000 x 4096 13.6 and 16.6)
+  if (M <= 32 || (M <= kQ8Rows && N < 11000) || K == 0) {
     const int xr = M <= 4 ? 4 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
     const int64_t blocks = cdiv(N, 16);
     const int64_t gy = cdiv(M, xr);
@@ -503,14 +506,14 @@ mm_status mm_linear_q8(const void* x, const float* x_scale, const void* W, const
     // 6000 x 4096 9.3 / 8.6 / 12.6).  Otherwise by the shares of the CUs: 1 x 28672 x
     // 8192 41.9 / 51.9 / 48.8, 16 x 14336 x 4096 15.1 / 14.4 / 13.6, 12 x 20000 x 8192
     // 37.5 / 38.7 / 46.8, 24 x 20000 x 8192 47.0 / 42.6 / 50.0, 64 x 8192 x 8192
-    // 23.2 / 18.2 / 25.2, 64 x 28672 x 8192 102 / 82 / 68.
+    // 23.2 / 18.2 / 25.2, 32 x 28672 x 8192 69.8 / 60.6 / 57.2.
     int cus = 0;
     if ((s = device_cus(&cus)) != MM_OK) return s;
     const int nb = M <= 16 && blocks <= 2 * cus ? 1 : column_blocks(blocks, gy, cus, M <= 4 ? 1 : M <= 16 ? 3 : 10);
     return launch(q8_rows_kernel(xr, nb), dim3((unsigned)cdiv(blocks, nb), (unsigned)gy), mmk::kW4Waves * 64, args, stream,
                   "linear_q8 rows");
   }
-  const Q8Plan plan = q8_plan(M, N, K, workspace ? kQ8MaxChunks : 1);
+  const Q8Plan plan = q8_plan(M, N, K, workspace && M > kQ8Rows ? kQ8MaxChunks : 1);
   if (plan.tiles_m * plan.tiles_n * plan.chunks >= kLimit) return fail(MM_ERR_UNSUPPORTED, "more than 2^31 output tiles");
   const int64_t need = q8_ws_bytes(plan);
   if (need > 0) {

@@ -353,7 +353,9 @@ def test_linear_q8_exact(dev, M, N, K):
     # 256 x 256 tiles whole and in chunks, 256 x 128, 128 x 128 with short and with
     # long rings, 128 x 64
     (129, 36981, 144), (144, 10898, 9344), (142, 21458, 144), (11208, 70, 8368), (79, 33206, 144), (67, 16681, 5248),
-    (16393, 66, 144), (6389, 69, 3360), (67, 71, 144), (71, 66, 1616)])
+    (16393, 66, 144), (6389, 69, 3360), (67, 71, 144), (71, 66, 1616),
+    # few rows by a wide weight
+    (33, 11000, 272), (64, 14001, 1040), (47, 33000, 144)])
 def test_linear_q8_every_tile_exact(dev, M, N, K):
     x, xs, W, ws, _ = q8_inputs(M, N, K, M + N + K, exact=True)
     out, intact = guarded((M, N), torch.bfloat16, dev)
