@@ -206,6 +206,7 @@ __device__ __forceinline__ void q8_scales(const Q8Params& p, int first, bool ins
       if (has_bias) __builtin_memcpy(&bs[4 * r], p.bias + first + 16 * r, 16);
     }
   } else {
+    asm volatile("" : "+v"(first));  // (as in q8_block)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int n = first + 16 * (i >> 2) + 2 * (i & 3);
@@ -244,18 +245,23 @@ __device__ __forceinline__ void q8_block(const Q8Params& p, float (&v)[16], floa
       pk[0][i] = t[0];
       pk[1][i] = t[1];
     }
-    const int n = nb + 16 * ((lane >> 4) & 1) + 8 * (lane >> 5);
+    int n = nb + 16 * ((lane >> 4) & 1) + 8 * (lane >> 5);
+    asm volatile("" : "+v"(n));  // (as below)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int m = mb + 16 * r + (lane & 15);
       if (m < p.M) __builtin_memcpy(p.out + (int64_t)m * p.N + n, &pk[r], 16);
     }
   } else if (mb + (lane & 31) < p.M) {
-    uint16_t* o = p.out + (int64_t)(mb + (lane & 31)) * p.N;
+    // (opaque, or the compiler prepares the columns of all blocks in registers
+    // that it does not have)
+    int first = nb + 8 * (lane >> 5);
+    asm volatile("" : "+v"(first));
+    uint16_t* o = p.out + (int64_t)(mb + (lane & 31)) * p.N + first;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int n = nb + 8 * (lane >> 5) + 16 * (i >> 3) + (i & 7);
-      if (n < p.N) o[n] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[i]));
+      const int n = 16 * (i >> 3) + (i & 7);
+      if (n < p.N - first) o[n] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[i]));
     }
   }
 }
@@ -528,21 +534,20 @@ __global__ void __launch_bounds__(256, SX * FM + SW * FN <= 10 ? 2 : 1) gemm_q8_
     float xs[FM];
 #pragma unroll
     for (int a = 0; a < FM; ++a) xs[a] = p.xs[min(m0 + 32 * a + l32, p.M - 1)];
-    // a block's scales and biases are loaded while the block before is computed
     const bool inside = tn * BN + BN <= p.N;
-    float ws[2][16];
-    uint32_t bs[2][8];
-    q8_scales(p, n0 + 8 * h, inside, has_bias, ws[0], bs[0]);
 #pragma unroll
     for (int b = 0; b < FN; ++b) {
-      if (b + 1 < FN) q8_scales(p, n0 + 8 * h + 32 * (b + 1), inside, has_bias, ws[(b + 1) & 1], bs[(b + 1) & 1]);
+      // (loaded a block ahead, these took registers that were not there)
+      float ws[16];
+      uint32_t bs[8];
+      q8_scales(p, n0 + 8 * h + 32 * b, inside, has_bias, ws, bs);
       order();
 #pragma unroll
       for (int a = 0; a < FM; ++a) {
         float v[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = acc[a][b][i];
-        q8_block(p, v, xs[a], ws[b & 1], bs[b & 1], m0 + 32 * a, n0 + 32 * b, lane, has_bias, gelu);
+        q8_block(p, v, xs[a], ws, bs, m0 + 32 * a, n0 + 32 * b, lane, has_bias, gelu);
       }
     }
     // (no load of the epilogue is left pending: the next tile's K loop would

@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
   constexpr int AB = MB * NB;
   constexpr int GP = 128 / G;             // groups per step
   // HALVES: the two LDS tiles of a wave are the halves (64 k) of one step, not
-  // two steps: half the LDS and half the fragment registers, so that two
-  // workgroups of 48 or 64 rows fit a CU
+  // two steps: half the LDS and half the fragment registers, which 64 rows by
+  // four column blocks would not have otherwise
   constexpr bool HALVES = XR >= 48;
   // a chunk: what shares one scale and one pass over the accumulators; JC
   // MFMAs, whose fragments are read JR at a time
