@@ -56,7 +56,7 @@ CSRC = os.path.join(ROOT, "dense_bf16_gemm_amd", "csrc")
 # the headers the benchmarked workloads' kernels are built from, and the host
 # code that chooses their tile order and launch
 SLAB_SOURCES = ("gemm_kernel.hpp", "gemm_nt_pipe.hpp", "gemm_nt_slab.hpp", "gemm_skinny.hpp", "gemm_small.hpp",
-                "mm_api.hip")
+                "mm_device.hpp", "mm_api.hip")
 
 
 def kernel_source_hash() -> str:
