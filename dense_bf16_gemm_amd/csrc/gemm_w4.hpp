@@ -132,7 +132,9 @@ __global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
   const int nblocks = (p.N + 15) >> 4;
   const int groups = (p.K + G - 1) / G;
   const int m0 = blockIdx.y * XR;
-  const int b0 = blockIdx.x * NB;
+  // neighbouring blocks on one XCD: they share the lines of the scales and zeros
+  // (1 x 28672 x 8192 by groups of 32: 28.8 -> 27.8 us)
+  const int b0 = remap_workgroup(blockIdx.x, gridDim.x, 1) * NB;
   char* xs = smem + wave * kX;
   char* sc = smem + WV * kX + wave * kSc;
 
