@@ -278,7 +278,8 @@ __device__ __forceinline__ void q8_block(const Q8Params& p, float (&v)[16], floa
 // and issues the copies of W for q + SW and of x for q + SX into q's slots.  So no
 // MFMA waits on an LDS read, and a copy has SX - 1/2 (SW - 1/2) super-steps to
 // land.  256 x 256 tiles fill the LDS with 3 and 2 slots (with two each the loop
-// took 458 us at 8192^3).  What bounds the smaller tiles is the bytes in flight per
+// took 458 us at 8192^3, now 415 with bias and GELU, where MFMAs issue in 65 % of
+// the cycles).  What bounds the smaller tiles is the bytes in flight per
 // CU, and the 10 to 13 TB/s that all of them get out of L2; those for
 // products with few tiles take the LDS of a whole CU for their rings: 256 x 8192 x
 // 4096 33.1 us with 128 x 128 tiles of 3 and 2 slots, 25.6 with 5 each, 20.8 with
