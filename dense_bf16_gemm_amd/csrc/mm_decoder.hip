@@ -115,6 +115,19 @@ mm_status norm(const void* x, int64_t ld_x, const void* residual, const void* we
   return launch(k, dim3((unsigned)rows), threads, args, stream, "rms_norm");
 }
 
+template <bool F32>
+const void* norm_grad_few_kernel(int vpt) {
+  return vpt == 1   ? fn(&mmk::rms_norm_grad_few<F32, 1>)
+         : vpt == 2 ? fn(&mmk::rms_norm_grad_few<F32, 2>)
+                    : fn(&mmk::rms_norm_grad_few<F32, 4>);
+}
+
+// Up to this many rows the gradient is one launch, whose columns' workgroups read
+// dy and h again.  Measured (us, one launch / two, bf16): 16 x 4096 2.8 / 5.9, 256 x
+// 4096 5.1 / 10.7, 1024 x 4096 13.1 / 19.2, 2048 x 1024 17.1 / 20.1, 2048 x 4096
+// 23.3 / 22.9, 2048 x 8192 33.5 / 35.5, 4096 x 4096 42.4 / 33.2.
+constexpr int64_t kFewRows = 2048;
+
 // Workgroups of the gradient, each with a part of dweight: as few as keep the
 // memory busy.  Measured (us, 1 / 2 / 4 per CU): 4096 x 8192 fp32 112 / 118 / 133,
 // 8192 x 4096 bf16 68 / 58 / 68, 8192 x 2048 bf16 54 / 37 / 40.
@@ -316,6 +329,7 @@ mm_status mm_rms_norm_backward_workspace_size(int64_t rows, int64_t hidden, int6
   *bytes = 0;
   mm_status s = check_norm_sizes(rows, hidden, MM_OUT_BF16);
   if (s != MM_OK || rows == 0 || hidden == 0) return s;
+  if (rows <= kFewRows) return MM_OK;
   int64_t parts = 0;
   if ((s = norm_grad_parts(rows, hidden, &parts)) != MM_OK) return s;
   *bytes = parts * hidden * 4;
@@ -328,7 +342,8 @@ mm_status mm_rms_norm_backward(const void* dy, const void* h, const void* weight
   mm_status s = check_norm_sizes(rows, hidden, stream_dtype);
   if (s != MM_OK) return s;
   if (hidden == 0) return MM_OK;
-  if (!dweight || (rows > 0 && (!dy || !h || !weight || !rstd || !dh || !workspace)))
+  const bool few = rows <= kFewRows;
+  if (!dweight || (rows > 0 && (!dy || !h || !weight || !rstd || !dh || (!few && !workspace))))
     return fail(MM_ERR_INVALID_VALUE, "null pointer");
   if (!aligned(dweight, 16) || (rows > 0 && (!aligned(dy, 16) || !aligned(h, 16) || !aligned(weight, 16) ||
                                              !aligned(rstd, 4) || !aligned(dres, 16) || !aligned(dh, 16) ||
@@ -354,7 +369,7 @@ mm_status mm_rms_norm_backward(const void* dy, const void* h, const void* weight
   }
   int64_t parts = 0;
   if (rows > 0) {
-    if ((s = norm_grad_parts(rows, hidden, &parts)) != MM_OK) return s;
+    if (!few && (s = norm_grad_parts(rows, hidden, &parts)) != MM_OK) return s;
     if (workspace_bytes < parts * hidden * 4)
       return fail(MM_ERR_INVALID_VALUE, "workspace smaller than mm_rms_norm_backward_workspace_size reports");
     mmk::RmsNormGradParams p;
@@ -369,6 +384,12 @@ mm_status mm_rms_norm_backward(const void* dy, const void* h, const void* weight
     p.hidden = (int)hidden;
     int threads, vpt;
     norm_shape(hidden, 512, &threads, &vpt);
+    if (few) {
+      threads = std::max(threads, 512);  // (for the columns' sums)
+      void* args[] = {&p, &dweight};
+      return launch(stream_dtype == MM_OUT_F32 ? norm_grad_few_kernel<true>(vpt) : norm_grad_few_kernel<false>(vpt),
+                    dim3((unsigned)(rows + cdiv(hidden, 64))), threads, args, stream, "rms_norm gradient");
+    }
     if (vpt == 4) norm_shape(hidden, 1024, &threads, &vpt);
     void* args[] = {&p};
     s = launch(stream_dtype == MM_OUT_F32 ? norm_grad_kernel<true>(vpt, threads) : norm_grad_kernel<false>(vpt, threads),

@@ -310,6 +310,86 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) rms_norm_grad(RmsNormGradP
   }
 }
 
+// The gradient of few rows in one launch (a second one costs the call 4 us, and
+// a row per CU leaves most of a CU idle): the first workgroups sum 64 columns of
+// dw each, reading dy and h for it once more, the others take one row each, as
+// above.  1 x 4096 takes 2.7 us, which is latency, 512 x 8192 11.3 (3 TB/s).
+template <bool F32, int VPT>
+__global__ void __launch_bounds__(1024) rms_norm_grad_few(RmsNormGradParams p, float* dweight) {
+  __shared__ float slot[16];
+  __shared__ float sums[128][64];
+  const int T = blockDim.x;
+  const int vectors = p.hidden >> 3;
+  const int wide = (vectors + 7) >> 3;  // workgroups of columns
+  if ((int)blockIdx.x < wide) {
+    // 8 lanes of 8 columns by T / 8 interleaved runs of rows
+    const int lane = threadIdx.x & 7, run = threadIdx.x >> 3, runs = T >> 3;
+    const int c = blockIdx.x * 8 + lane;
+    float dw[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[j] = 0.f;
+    if (c < vectors) {
+#pragma unroll 4
+      for (int64_t row = run; row < p.rows; row += runs) {
+        Raw8<F32> h;
+        Raw8<false> dy;
+        h.load(p.h, row * p.hidden + 8 * c);
+        dy.load(p.dy, row * p.hidden + 8 * c);
+        const float r = p.rstd[row];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[j] += dy[j] * (h[j] * r);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sums[run][8 * lane + j] = dw[j];
+    __syncthreads();
+    const int col = blockIdx.x * 64 + threadIdx.x;
+    if (threadIdx.x < 64 && col < p.hidden) {
+      float s = 0.f;
+      for (int b = 0; b < runs; ++b) s += sums[b][threadIdx.x];
+      dweight[col] = s;
+    }
+    return;
+  }
+  const int64_t row = (int64_t)blockIdx.x - wide;
+  const float r = p.rstd[row];
+  Raw8<F32> h[VPT];
+  Raw8<false> dy[VPT], w[VPT];
+  float dot = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = threadIdx.x + i * T;
+    h[i].clear();
+    dy[i].clear();
+    w[i].clear();
+    if (c < vectors) {
+      h[i].load(p.h, row * p.hidden + 8 * c);
+      dy[i].load(p.dy, row * p.hidden + 8 * c);
+      w[i].load(p.weight, 8 * c);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dot = __builtin_fmaf(dy[i][j] * (h[i][j] * r), w[i][j], dot);
+  const float mean = block_sum(dot, slot) * (1.0f / (float)p.hidden);
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = threadIdx.x + i * T;
+    if (c >= vectors) continue;
+    float o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = r * (dy[i][j] * w[i][j] - h[i][j] * r * mean);
+    if (p.dres) {
+      Raw8<F32> dres;
+      dres.load(p.dres, row * p.hidden + 8 * c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] += dres[j];
+    }
+    store8<F32>(p.dh, row * p.hidden + 8 * c, o);
+  }
+}
+
 // dw[c] = sum over b of part[b][c]: 32 columns per workgroup (8 lanes of four)
 // by 32 interleaved runs of b, joined in LDS in a fixed order.
 __global__ void __launch_bounds__(256) rms_norm_dweight(const float* part, float* dw, int parts, int hidden) {

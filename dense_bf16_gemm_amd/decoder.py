@@ -128,11 +128,11 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, r
     stream = _stream(index)
     dweight = torch.empty(hidden, dtype=_F32, device=h.device)
     nbytes = binding.rms_norm_backward_workspace_size(rows, hidden)
-    ws = torch.empty(nbytes, dtype=_U8, device=h.device)
+    ws = torch.empty(nbytes, dtype=_U8, device=h.device) if nbytes else None
     st = binding.load().mm_rms_norm_backward(
         dy.data_ptr(), h.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
         None if dres is None else dres.data_ptr(), out.data_ptr(), dweight.data_ptr(), rows, hidden,
-        _STREAM[dtype], ws.data_ptr(), nbytes, stream)
+        _STREAM[dtype], None if ws is None else ws.data_ptr(), nbytes, stream)
     if st:
         binding.check(st, "mm_rms_norm_backward")
     return out, dweight

@@ -100,7 +100,7 @@ def test_norm_gradient_refusals(lib):
         return lib.mm_rms_norm_backward(dy, h, w, rstd, dres, dh, dw, rows, hidden, dtype, ws, nbytes, None)
 
     for bad in (dict(dy=NULL), dict(h=NULL), dict(w=NULL), dict(rstd=NULL), dict(dh=NULL), dict(dw=NULL),
-                dict(ws=NULL), dict(rows=-1), dict(dtype=3), dict(nbytes=-1), dict(dh=P[0]), dict(dh=P[1]),
+                dict(ws=NULL, rows=4096), dict(rows=-1), dict(dtype=3), dict(nbytes=-1), dict(dh=P[0]), dict(dh=P[1]),
                 dict(dh=P[4] + 16), dict(dw=P[2]), dict(ws=P[5]), dict(dw=P[5] + 16)):
         assert grad(**bad) == INVALID, bad
     for bad in (dict(hidden=4), dict(dy=P[0] + 2), dict(dw=P[6] + 4), dict(ws=P[7] + 4), dict(dres=P[4] + 8)):

@@ -185,6 +185,33 @@ def test_rms_norm_backward(dev, rows, hidden, dtype, dres):
         assert inplace is buf and torch.equal(buf, got)
 
 
+@pytest.mark.parametrize("rows,hidden", [(2048, 1032), (2049, 64), (2049, 520), (2050, 4096), (3100, 5000), (2049, 8192),
+                                         (2051, 16384), (2049, 16392), (2055, 32768)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dres", [False, True])
+def test_rms_norm_backward_many_rows(dev, rows, hidden, dtype, dres):
+    """Both sides of the row count from which the gradient is two launches;
+    the 64-bit form runs on the GPU."""
+    g = torch.Generator(device=dev).manual_seed(rows + hidden)
+    h = (torch.randn((rows, hidden), generator=g, device=dev) * 2.0).to(dtype)
+    dy = torch.randn((rows, hidden), generator=g, device=dev).bfloat16()
+    w = (torch.randn(hidden, generator=g, device=dev) * 0.3 + 1.0).bfloat16()
+    d = torch.randn((rows, hidden), generator=g, device=dev).to(dtype) if dres else None
+    rstd = torch.rsqrt(h.float().square().mean(1) + 1e-6)
+    got, gw = mm.rms_norm_backward(dy, h, w, rstd, d)
+    dh, dw = ref.norm_grad(dy, h, w, rstd, d)
+    # (tolerances as in test_rms_norm_backward)
+    r = rstd.double()[:, None]
+    gg, n = (dy.double() * w.double()).abs(), h.double().abs() * r
+    terms = r * (gg + n * (gg * n).mean(1, keepdim=True)) + (d.double().abs() if dres else 0.0)
+    off = (got.double() - dh).abs() - (torch.finfo(dtype).eps / 2 * dh.abs() + NORM_U * terms)
+    assert float(off.max()) <= 0, float(off.max())
+    off = (gw.double() - dw).abs() - (rows + 40) * U * (dy.double().abs() * n).sum(0)
+    assert float(off.max()) <= 0, float(off.max())
+    again, gw2 = mm.rms_norm_backward(dy, h, w, rstd, d)
+    assert torch.equal(again, got) and torch.equal(gw, gw2), "not reproducible"
+
+
 def test_rms_norm_past_32_bits(dev):
     """rows * hidden past 2^31 elements: the last rows against the same rows alone."""
     rows, hidden = 66000, 32768
