@@ -62,7 +62,10 @@ const void* norm_kernel(int vpt) {
 template <bool F32>
 const void* norm_grad_kernel(int vpt, int threads) {
   if (threads <= 512) return vpt == 1 ? fn(&mmk::rms_norm_grad<F32, 1, true>) : fn(&mmk::rms_norm_grad<F32, 2, true>);
-  return vpt == 2 ? fn(&mmk::rms_norm_grad<F32, 2, false>) : fn(&mmk::rms_norm_grad<F32, 4, false>);
+  if constexpr (F32) {
+    if (vpt == 4) return fn(&mmk::rms_norm_grad<F32, 4, false>);
+  }
+  return fn(&mmk::rms_norm_grad<F32, 2, false>);
 }
 
 mm_status norm(const void* x, int64_t ld_x, const void* residual, const void* weight, void* h, void* y, float* stat,
@@ -126,7 +129,10 @@ const void* norm_grad_few_kernel(int vpt) {
 // dy and h again.  Measured (us, one launch / two, bf16): 16 x 4096 2.8 / 5.9, 256 x
 // 4096 5.1 / 10.7, 1024 x 4096 13.1 / 19.2, 2048 x 1024 17.1 / 20.1, 2048 x 4096
 // 23.3 / 22.9, 2048 x 8192 33.5 / 35.5, 4096 x 4096 42.4 / 33.2.
-constexpr int64_t kFewRows = 2048;
+// A row longer than kLongRow does not fit the registers of 1024 threads together
+// with its dw, and in bf16 one launch is then faster at any count: 4096 x 16392
+// 189 / 267, 8192 x 32768 656 / 695 (fp32: 266 / 254, 1003 / 796).
+constexpr int64_t kFewRows = 2048, kLongRow = 16384;
 
 // Workgroups of the gradient, each with a part of dweight: as few as keep the
 // memory busy.  Measured (us, 1 / 2 / 4 per CU): 4096 x 8192 fp32 112 / 118 / 133,
@@ -342,7 +348,7 @@ mm_status mm_rms_norm_backward(const void* dy, const void* h, const void* weight
   mm_status s = check_norm_sizes(rows, hidden, stream_dtype);
   if (s != MM_OK) return s;
   if (hidden == 0) return MM_OK;
-  const bool few = rows <= kFewRows;
+  const bool few = rows <= kFewRows || (hidden > kLongRow && stream_dtype == MM_OUT_BF16);
   if (!dweight || (rows > 0 && (!dy || !h || !weight || !rstd || !dh || (!few && !workspace))))
     return fail(MM_ERR_INVALID_VALUE, "null pointer");
   if (!aligned(dweight, 16) || (rows > 0 && (!aligned(dy, 16) || !aligned(h, 16) || !aligned(weight, 16) ||

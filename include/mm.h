@@ -259,9 +259,10 @@ mm_status mm_rms_norm_q8(const void* x, int64_t ld_x, const void* residual, cons
  *   dy    [rows][hidden] bf16;  h, rstd as mm_rms_norm left them
  *   dres  [rows][hidden] of type T or NULL: the gradient that reached h past
  *         the norm;  dh of type T may be dres itself
- * Up to 2048 rows one kernel, which takes no workspace (NULL, 0 bytes); above,
- * two: the rows, each workgroup keeping its part of dweight, and the
- * sum of the parts in a fixed order (results are reproducible).  rows == 0
+ * Up to 2048 rows, and for bf16 rows longer than 16384 values, one kernel, which
+ * uses no workspace (up to 2048 rows the function below reports 0 bytes);
+ * otherwise two: the rows, each workgroup keeping its part of dweight, and the
+ * sum of the parts.  Sums run in a fixed order (results are reproducible).  rows == 0
  * writes zeros to dweight.  The workspace (size from the function below, a
  * device query; 16-byte aligned, any contents) holds the parts; two calls in
  * flight at once must not share it. */
