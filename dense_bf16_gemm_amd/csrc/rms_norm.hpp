@@ -173,16 +173,28 @@ __global__ void __launch_bounds__(1024) rms_norm(RmsNormParams p) {
     top = block_max(top, slot_max);
     float s = __builtin_bit_cast(float, top) / 448.0f;
     s = s < 0x1p-126f ? 0x1p-126f : s;  // (a NaN stays)
+    // y / s: the product with 1 / s, then the remainder that it leaves, by one FMA
+    // each (y - q s is exact unless it underflows).  The product alone decides
+    // wrongly where a quotient lies on the border of two codes, which it often
+    // does: the values have few bits.  4096 x 8192: 47.3 us with the product alone, 47.8
+    // so, 50.3 with the division operator.
     const float inv = 1.0f / s;
+    const float d = s > 3.4028235e38f ? 3.4028235e38f : s;  // (y / inf is 0 for a finite y)
+    auto quotient = [&](float y) __attribute__((always_inline)) {
+      const float q = y * inv;
+      return __builtin_fmaf(__builtin_fmaf(-q, d, y), inv, q);
+    };
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = threadIdx.x + i * T;
       if (c >= vectors) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = quotient(v[i][j]);
       int lo = 0, hi = 0;
-      lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[i][0] * inv, v[i][1] * inv, lo, false);
-      lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[i][2] * inv, v[i][3] * inv, lo, true);
-      hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[i][4] * inv, v[i][5] * inv, hi, false);
-      hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[i][6] * inv, v[i][7] * inv, hi, true);
+      lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[i][0], v[i][1], lo, false);
+      lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[i][2], v[i][3], lo, true);
+      hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[i][4], v[i][5], hi, false);
+      hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[i][6], v[i][7], hi, true);
       reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + row * p.hidden)[c] = uint2{(uint32_t)lo, (uint32_t)hi};
     }
     if (threadIdx.x == 0) p.stat[row] = s;

@@ -96,6 +96,24 @@ def test_rms_norm(dev, rows, hidden, dtype, residual):
     close(val, wy, tol, "q")
 
 
+@pytest.mark.parametrize("rows,hidden", [(1, 8192), (64, 4096), (300, 1032), (5, 16384)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rms_norm_q8_codes_are_the_rounded_quotients(dev, rows, hidden, dtype):
+    """scale and q bit for bit from the fp32 y: max|y| / 448 and y / scale, each
+    rounded once.  (Quotients at the border of two codes are common, since the
+    values have few bits: a product with a rounded 1 / scale misses some.)"""
+    x, w, res = norm_inputs(rows, hidden, dtype, True, rows + hidden)
+    for weight in (w, w.clone().index_fill_(0, torch.tensor([3]), float("inf"))):
+        args = on(dev, x, weight, res)
+        _, h, rstd = mm.rms_norm(*args)
+        q, scale, _ = mm.rms_norm_q8(*args)
+        y = h.float().cpu() * rstd.cpu()[:, None] * weight.float()
+        want = (y.abs().amax(1) / ref.E4M3_MAX).clamp_min(ref.TINY)
+        assert torch.equal(scale.cpu(), want)
+        codes = (y / want[:, None]).to(torch.float8_e4m3fn).float().nan_to_num(1000.0)
+        assert int((q.float().cpu().nan_to_num(1000.0) != codes).sum()) == 0
+
+
 def test_rms_norm_in_place_strided_and_written_where_told(dev):
     g = gen(3)
     wide = randn(g, (37, 1200)).bfloat16().to(dev)
