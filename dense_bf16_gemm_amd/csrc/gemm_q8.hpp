@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(WV * 64) gemm_q8_rows(Q8Params p) {
   auto step = [&](int st, int slot, Step& t, Step& next) __attribute__((always_inline)) {
     const int sn = min(st + WV, ksteps - 1);
     copy(sn, slot ^ 1);
+    order();  // (nothing but the loads' arrival covers the copies')
     load(sn, next);
     race_check_drain();
 #pragma unroll
@@ -143,6 +144,7 @@ __global__ void __launch_bounds__(WV * 64) gemm_q8_rows(Q8Params p) {
     // loop then has one shape, and its waits count loads exactly)
     Step s0, s1;
     copy(wave, 0);
+    order();
     load(wave, s0);
     for (int st = wave; st < ksteps; st += 2 * WV) {
       step(st, 0, s0, s1);

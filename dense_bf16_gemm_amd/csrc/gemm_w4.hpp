@@ -195,8 +195,8 @@ __global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
   keep_in_registers(mask, sixteen);
 
   // Step kb, and the loads of the wave's next.  Whole steps: the next one's
-  // copies go out first (loads arrive in order, so once a step's weights are
-  // there its activations are).  Halves: the next step's weights go out first,
+  // copies go out first, in an order fixed here (loads arrive in order, so once a
+  // step's weights are there its activations are: no other wait covers them).  Halves: the next step's weights go out first,
   // the copies of each half once this step's fragments of it are in registers;
   // so what a wait may leave in flight are the loads issued after its half.
   constexpr int kLoads = NB + 2;
@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
       race_check_drain();
     } else {
       copy(kn, tile ^ 1);
+      order();
       load(kn, next);
       race_check_drain();
 #pragma unroll
@@ -319,6 +320,7 @@ __global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
       copy(wave, 1);
     } else {
       copy(wave, 0);
+      order();
       load(wave, s0);
     }
     for (int kb = wave; kb < kblocks; kb += 2 * WV) {

@@ -66,7 +66,8 @@ __device__ __forceinline__ void order() { asm volatile("" ::: "memory"); }
 __device__ __forceinline__ void settle(float& v) { asm volatile("" : "+v"(v)); }
 __device__ __forceinline__ void settle(f32x4& v) { asm volatile("" : "+v"(v)); }
 __device__ __forceinline__ void settle(u32x4& v) { asm volatile("" : "+v"(v)); }
-// The value of a load is there before anything after this point runs:
+// The value of a load is there before any memory operation after this point (the
+// compiler may move arithmetic on it before):
 __device__ __forceinline__ void arrived(u32x4 v) { asm volatile("" ::"v"(v) : "memory"); }
 
 // Nothing, and in the race-check build (MM_DEBUG_FULL_SYNC) a wait for every
