@@ -73,6 +73,39 @@ __device__ __forceinline__ float w4_dot(const W4Params& p, int m, int n) {
   return v;
 }
 
+// Where a wave's copies of the activations read (the host's tests walk them).  A
+// tile is XR rows by a step (128 k; from 48 rows on a half of one, 64 k); copy i of
+// it takes `chunk` (16 bytes) of `row`, at byte `offset` + (in the last step) `tail`
+// of the lane + `base` of the wave from the block's first row.  The buffer ends
+// with its last row: rows past that read as zeros, and so do the chunks past K,
+// whose tail lies beyond any end.  `base` stays within the shortest buffer, one
+// row: the hardware compares offsets with the end less the base, so the last
+// step's second half, which may start past K, has its 128 bytes in `tail`.
+template <int XR>
+struct W4Tile {
+  static constexpr bool kHalves = XR >= 48;
+  static constexpr int kCopies = kHalves ? XR / 8 : XR / 4;  // of eight rows of 128 bytes, or four of 256
+  // copies i and i + 4 (halves: all of one half) share the chunk, and so the tail
+  static constexpr int kTails = kHalves ? 2 : kCopies < 4 ? kCopies : 4;
+  static __host__ __device__ __forceinline__ int row(int i, int lane) {
+    return kHalves ? 8 * i + (lane >> 3) : 4 * i + (lane >> 4);
+  }
+  static __host__ __device__ __forceinline__ int chunk(int i, int lane) {
+    return kHalves ? (lane & 7) ^ (lane >> 3) : (lane & 15) ^ (row(i, lane) & 15);
+  }
+  static __host__ __device__ __forceinline__ uint32_t offset(int i, int lane, uint32_t row_bytes) {
+    return (uint32_t)row(i, lane) * row_bytes + 16u * (uint32_t)chunk(i, lane);
+  }
+  // t: the half, or the copy (mod 4)
+  static __host__ __device__ __forceinline__ uint32_t tail(int t, int lane, int K) {
+    const int k = ((K + 127) / 128 - 1) * 128 + 8 * chunk(t, lane) + (kHalves ? 64 * t : 0);
+    return k < K ? (kHalves ? 128u * (uint32_t)t : 0u) : 0x80000000u;
+  }
+  static __host__ __device__ __forceinline__ uint32_t base(int kb, int half, bool last) {
+    return (uint32_t)kb * 256u + (kHalves && !last ? 128u * (uint32_t)half : 0u);
+  }
+};
+
 // XR activation rows (4: the first four of a block of 16, whose others are
 // never used; 16, 32, 48 or 64: 48 rows by 14336 x 4096 take 16.9 us as 48 and
 // 19.5 as 64) by NB blocks of 16 columns per workgroup.  Its WV waves take
@@ -105,7 +138,8 @@ __global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
   // HALVES: the two LDS tiles of a wave are the halves (64 k) of one step, not
   // two steps: half the LDS and half the fragment registers, which 64 rows by
   // four column blocks would not have otherwise
-  constexpr bool HALVES = XR >= 48;
+  using Tile = W4Tile<XR>;
+  constexpr bool HALVES = Tile::kHalves;
   // a chunk: what shares one scale and one pass over the accumulators; JC
   // MFMAs, whose fragments are read JR at a time
   constexpr int JC = (HALVES && G > 64 ? 64 : G) / 32;
@@ -115,8 +149,7 @@ __global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
   // share), a column block's products wait for those BB blocks before.
   constexpr bool CALM = MB >= 3 || AB * GP > (MB == 2 ? 16 : 4);
   constexpr int BB = MB < 3 && NB > 1 ? 2 : 1;
-  // copies per tile: four rows of 256 bytes each, or eight of 128
-  constexpr int XC = HALVES ? XR / 8 : XR / 4, XT = XC * 1024;
+  constexpr int XC = Tile::kCopies, XT = XC * 1024;
   // scale pairs: a column's GP * NB, in an odd number of 16-byte units (reads
   // of 16 columns then fall in 16 bank groups)
   constexpr int PB = GP * NB, SU = PB < 2 ? 1 : (PB / 2) | 1;
@@ -138,20 +171,15 @@ __global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
   char* xs = smem + wave * kX;
   char* sc = smem + WV * kX + wave * kSc;
 
-  // rows past M lie past the descriptor's end and arrive as zeros, as do (bit
-  // 31 of the offset) the chunks of the last step past K
   const uint32_t row_bytes = (uint32_t)p.K * 2u;
   const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint16_t*>(p.x + (int64_t)m0 * p.K), (short)0, (int)((uint32_t)min(p.M - m0, XR) * row_bytes),
       0x00020000);
-  constexpr int kTails = HALVES ? 2 : XC < 4 ? XC : 4;
-  uint32_t voff[XC], tail[kTails];
+  uint32_t voff[XC], tail[Tile::kTails];
 #pragma unroll
   for (int i = 0; i < XC; ++i) {
-    const int r = HALVES ? 8 * i + (lane >> 3) : 4 * i + lg;
-    const int chunk = HALVES ? (lane & 7) ^ (lane >> 3) : lx ^ (r & 15);
-    voff[i] = (uint32_t)r * row_bytes + 16u * (uint32_t)chunk;
-    if (i < kTails) tail[i] = (kblocks - 1) * 128 + 8 * chunk + (HALVES ? 64 * i : 0) < p.K ? 0u : 0x80000000u;
+    voff[i] = Tile::offset(i, lane, row_bytes);
+    if (i < Tile::kTails) tail[i] = Tile::tail(i, lane, p.K);
   }
   // scales: lane (group sg of the step, columns sn .. sn + 3); lanes past the
   // step's groups repeat earlier ones.  The last columns' loads start early
@@ -172,8 +200,8 @@ __global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
     const bool last = kb == kblocks - 1;
 #pragma unroll
     for (int i = 0; i < XC; ++i)
-      copy_to_lds(rx, xs + tile * XT + i * 1024, voff[i] | (last ? tail[HALVES ? tile : i & 3] : 0u),
-                  (uint32_t)kb * 256u + (HALVES ? 128u * (uint32_t)tile : 0u));
+      copy_to_lds(rx, xs + tile * XT + i * 1024, voff[i] + (last ? tail[HALVES ? tile : i & 3] : 0u),
+                  Tile::base(kb, tile, last));
   };
   auto load = [&](int kb, Step& t) __attribute__((always_inline)) {
     const int group = min(kb * GP + sg, groups - 1);

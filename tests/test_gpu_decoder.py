@@ -289,6 +289,21 @@ def test_linear_w4_exact(dev, M, N, K, group, zeros):
     assert torch.equal(got.cpu(), want)
 
 
+@pytest.mark.parametrize("M,N,K", [(65, 70, 8), (65, 100, 64), (71, 50, 8), (66, 64, 16), (129, 67, 392),
+                                   (193, 97, 4104), (257, 130, 1032)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_linear_w4_few_rows_in_the_last_block(dev, M, N, K, group):
+    """Blocks of 64 rows, few in the last, and a K that ends in the first half
+    of a step: the second half's copies lie past all of the block's rows."""
+    x, codes, s, z, _ = w4_inputs(M, N, K, group, True, M + N + K, exact=True)
+    out, intact = guarded((M, N), torch.bfloat16, dev)
+    xd, sd, zd = on(dev, x, s, z)
+    got = mm.linear_w4(xd, mm.pack_w4(codes.to(dev)), sd, zd, group=group, out=out)
+    intact()
+    want = (x.double() @ ref.w4_weight(codes, s, z, group).t()).float().bfloat16()
+    assert torch.equal(got.cpu(), want)
+
+
 @pytest.mark.parametrize("M,N,K,group,zeros,epi", [
     (1, 4096, 4096, 128, False, "none"), (3, 1001, 4104, 32, True, "bias"), (16, 512, 8192, 64, True, "gelu_tanh"),
     (31, 300, 2000, 128, True, "bias_gelu_tanh"), (64, 257, 4096, 64, False, "bias_gelu_tanh"),
