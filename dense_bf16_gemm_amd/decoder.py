@@ -5,6 +5,7 @@ current stream; every step of the computation runs in the HIP kernels.
 """
 from __future__ import annotations
 
+import math
 from typing import Optional
 
 import torch
@@ -83,6 +84,8 @@ def _norm(fn, x, weight, residual, eps, h, out_dtype):
             _STREAM[dtype], stream)
     if st:
         binding.check(st, fn.__name__)
+    if not hidden:  # (no launch: the mean of no values is 0, and so is their largest)
+        stat.fill_(2.0 ** -126 if out_dtype is _E4M3 else eps ** -0.5 if eps else math.inf)
     return y, stat, h_out
 
 
@@ -92,7 +95,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     h = x + residual in x's type (bf16 or fp32; h is x without a residual),
     rstd = 1 / sqrt(mean(h^2) + eps), y = h * rstd * weight in bf16.
     Returns (y, h, rstd).  x may have a row stride; `h` may name the tensor
-    to write the sum to, residual itself or x among them."""
+    to write the sum to, residual itself or x among them.  Rows of no values
+    have rstd 1 / sqrt(eps)."""
     y, rstd, h = _norm(binding.load().mm_rms_norm, x, weight, residual, eps, h, _BF16)
     return y, h, rstd
 
@@ -101,7 +105,8 @@ def rms_norm_q8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
                 eps: float = 1e-6, h: Optional[torch.Tensor] = None):
     """rms_norm with an 8-bit output, the activations linear_q8 takes: returns
     (q, scale, h) with q e4m3 [rows, hidden] and scale fp32 [rows]; q stands
-    for q * scale[:, None], scale = max(max|y| / 448, 2^-126) of each row."""
+    for q * scale[:, None], scale = max(max|y| / 448, 2^-126) of each row (2^-126
+    for rows of no values)."""
     return _norm(binding.load().mm_rms_norm_q8, x, weight, residual, eps, h, _E4M3)
 
 

@@ -241,7 +241,8 @@ mm_status mm_ffn_glu(const void* x, const void* W_gate, const void* W_up, void* 
  *   y         [rows][hidden] bf16 (RNE)
  *   rstd      [rows] fp32 (the backward pass reads it)
  * hidden: a multiple of 8, at most 32768; 16-byte aligned pointers.  A row
- * with a NaN is NaN; one with an infinity has rstd = 0. */
+ * with a NaN is NaN; one with an infinity has rstd = 0.  hidden == 0 is a no-op
+ * too: rstd (scale below) is not written. */
 mm_status mm_rms_norm(const void* x, int64_t ld_x, const void* residual, const void* weight, void* h,
                       void* y, float* rstd, int64_t rows, int64_t hidden, float eps,
                       mm_out_dtype stream_dtype, void* stream);

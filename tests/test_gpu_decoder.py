@@ -172,6 +172,35 @@ def test_rms_norm_empty(dev):
     assert dh.shape == (0, 64) and torch.equal(dw, torch.zeros(64, device=dev))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("residual", [False, True])
+def test_rms_norm_of_no_values(dev, dtype, residual):
+    """Rows without values: the mean of none is 0, the largest of none is 0."""
+    x = torch.empty((300, 0), dtype=dtype, device=dev)
+    res = x.clone() if residual else None
+    w = torch.empty(0, dtype=torch.bfloat16, device=dev)
+    for _ in range(3):
+        junk = torch.full((300,), float("nan"), device=dev)  # what the statistics' memory may hold
+        del junk
+        y, h, rstd = mm.rms_norm(x, w, res, eps=0.25)
+        assert y.shape == h.shape == (300, 0) and rstd.dtype == torch.float32
+        assert torch.equal(rstd, torch.full((300,), 2.0, device=dev))
+        del rstd
+        junk = torch.full((300,), float("nan"), device=dev)
+        del junk
+        q, scale, h = mm.rms_norm_q8(x, w, res)
+        assert q.shape == (300, 0) and torch.equal(scale, torch.full((300,), ref.TINY, device=dev))
+        bias = torch.ones(24, device=dev).bfloat16()
+        W = torch.empty((24, 0), device=dev).to(torch.float8_e4m3fn)
+        out = mm.linear_q8(q, scale, W, torch.ones(24, device=dev), bias, "bias")
+        assert torch.equal(out, bias.expand(300, 24))
+        del scale
+    _, _, rstd = mm.rms_norm(x, w, eps=0.0)
+    assert rstd.isposinf().all()
+    dh, dw = mm.rms_norm_backward(torch.empty((300, 0), device=dev).bfloat16(), x, w, rstd, res)
+    assert dh.shape == (300, 0) and dw.shape == (0,)
+
+
 @pytest.mark.parametrize("rows,hidden", [(1, 8), (2, 2056), (700, 520), (1500, 1024), (2200, 64), (300, 4096),
                                          (37, 5000), (9, 16384), (5, 16392), (3, 32768)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
