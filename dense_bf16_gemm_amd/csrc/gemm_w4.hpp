@@ -417,10 +417,10 @@ __global__ void __launch_bounds__(64) gemm_w4_narrow(W4Params p) {
 }
 
 // Lays out codes [N][K] (one byte each, the low four bits taken) as packed
-// words, one per thread; what pads N and K is code 0.
-__global__ void __launch_bounds__(256) w4_pack(const uint8_t* codes, uint32_t* packed, int N, int K, int64_t words) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= words) return;
+// words, one per thread from word `first` on (256 of them make a kilobyte); what pads
+// N and K is code 0.
+__global__ void __launch_bounds__(256) w4_pack(const uint8_t* codes, uint32_t* packed, int N, int K, int64_t first) {
+  const int64_t i = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int kblocks = (K + 127) / 128;
   const int64_t block = i >> 8;
   const int j = i & 3, n = (int)(block / kblocks) * 16 + ((i >> 2) & 15), g = (i >> 6) & 3;

@@ -17,7 +17,14 @@ namespace {
 
 constexpr int64_t kLimit = int64_t(1) << 31;
 
+// A launch takes fewer than 2^32 threads along x; longer ones go out in parts (or
+// their sizes are refused before).
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;
+constexpr int64_t kMaxGridY = 65535;
+
 mm_status launch(const void* kernel, dim3 grid, int threads, void** args, void* stream, const char* what) {
+  if ((int64_t)grid.x * threads > kMaxThreads)
+    return fail(MM_ERR_UNSUPPORTED, std::string(what) + ": more than 2^32 - 1 threads");
   const hipError_t e = hipLaunchKernel(kernel, grid, dim3(threads), args, 0, static_cast<hipStream_t>(stream));
   if (e != hipSuccess)
     return fail(MM_ERR_HIP, std::string("hipLaunchKernel (") + what + "): " + hipGetErrorString(e));
@@ -97,13 +104,7 @@ mm_status norm(const void* x, int64_t ld_x, const void* residual, const void* we
       if (overlaps(out[o].p, out[o].n, out[q].p, out[q].n)) return fail(MM_ERR_INVALID_VALUE, "outputs overlap");
   }
   mmk::RmsNormParams p;
-  p.x = x;
-  p.residual = residual;
   p.weight = static_cast<const uint16_t*>(weight);
-  p.h = h;
-  p.y = y;
-  p.stat = stat;
-  p.rows = rows;
   p.ld_x = ld_x;
   p.hidden = (int)hidden;
   p.eps = eps;
@@ -115,7 +116,18 @@ mm_status norm(const void* x, int64_t ld_x, const void* residual, const void* we
   void* args[] = {&p};
   const void* k = dtype == MM_OUT_F32 ? (q8 ? norm_kernel<true, true>(vpt) : norm_kernel<true, false>(vpt))
                                       : (q8 ? norm_kernel<false, true>(vpt) : norm_kernel<false, false>(vpt));
-  return launch(k, dim3((unsigned)rows), threads, args, stream, "rms_norm");
+  const int64_t most = kMaxThreads / threads;
+  for (int64_t r0 = 0; r0 < rows; r0 += most) {
+    const int64_t n = std::min(rows - r0, most);
+    p.x = static_cast<const char*>(x) + r0 * ld_x * e;
+    p.residual = residual ? static_cast<const char*>(residual) + r0 * hidden * e : nullptr;
+    p.h = residual ? static_cast<char*>(h) + r0 * hidden * e : nullptr;
+    p.y = static_cast<char*>(y) + r0 * hidden * (q8 ? 1 : 2);
+    p.stat = stat + r0;
+    p.rows = n;
+    if ((s = launch(k, dim3((unsigned)n), threads, args, stream, "rms_norm")) != MM_OK) return s;
+  }
+  return MM_OK;
 }
 
 template <bool F32>
@@ -180,12 +192,16 @@ mm_status check_product(int64_t M, int64_t N, int64_t K, const void* bias, const
 // workgroup reads all activations for itself, which costs about `share` tenths
 // of a block's weights, and the CU with the most workgroups ends last: the count
 // with the least of (workgroups to a CU, rounded up) x (blocks + share) is taken.
+// (A launch takes kMaxRowsGridX workgroups along x.)
+constexpr int64_t kMaxRowsGridX = kMaxThreads / (mmk::kW4Waves * 64);
+
 int column_blocks(int64_t blocks, int64_t gy, int cus, int share) {
-  int best = 1;
-  int64_t cost = 0;
+  int best = 4;
+  int64_t cost = -1;
   for (int nb = 1; nb <= 4; nb *= 2) {
-    const int64_t c = cdiv(cdiv(blocks, nb) * gy, cus) * (10 * nb + share);
-    if (nb == 1 || c < cost) best = nb, cost = c;
+    const int64_t gx = cdiv(blocks, nb);
+    const int64_t c = cdiv(gx * gy, cus) * (10 * nb + share);
+    if (gx <= kMaxRowsGridX && (cost < 0 || c < cost)) best = nb, cost = c;
   }
   return best;
 }
@@ -415,14 +431,19 @@ mm_status mm_w4_pack(const void* codes, void* packed, int64_t N, int64_t K, void
   if (N == 0 || K == 0) return MM_OK;
   if (!codes || !packed) return fail(MM_ERR_INVALID_VALUE, "null pointer");
   if (!aligned(packed, 16)) return fail(MM_ERR_MISALIGNED, "packed must be 16-byte aligned");
-  if (cdiv(N, 16) * cdiv(K, 128) >= kLimit) return fail(MM_ERR_UNSUPPORTED, "more than 2^31 packed kilobytes");
-  int64_t words = cdiv(N, 16) * cdiv(K, 128) * 256;
+  const int64_t words = cdiv(N, 16) * cdiv(K, 128) * 256;
   if (overlaps(packed, words * 4, codes, N * K)) return fail(MM_ERR_INVALID_VALUE, "packed overlaps codes");
   const uint8_t* c = static_cast<const uint8_t*>(codes);
   uint32_t* w = static_cast<uint32_t*>(packed);
   int n = (int)N, k = (int)K;
-  void* args[] = {&c, &w, &n, &k, &words};
-  return launch(fn(&mmk::w4_pack), dim3((unsigned)(words / 256)), 256, args, stream, "w4_pack");
+  const int64_t most = kMaxThreads / 256 * 256;
+  for (int64_t first = 0; first < words; first += most) {
+    void* args[] = {&c, &w, &n, &k, &first};
+    const mm_status s = launch(fn(&mmk::w4_pack), dim3((unsigned)(std::min(words - first, most) / 256)), 256, args, stream,
+                               "w4_pack");
+    if (s != MM_OK) return s;
+  }
+  return MM_OK;
 }
 
 mm_status mm_linear_w4(const void* x, const void* W, const void* scales, const void* zeros, const void* bias,
@@ -445,34 +466,46 @@ mm_status mm_linear_w4(const void* x, const void* W, const void* scales, const v
       return fail(MM_ERR_INVALID_VALUE, "out overlaps an input");
   }
   mmk::W4Params p;
-  p.x = static_cast<const uint16_t*>(x);
   p.W = static_cast<const mmk::u32x4*>(W);
   p.scales = static_cast<const uint16_t*>(scales);
   p.zeros = static_cast<const uint8_t*>(zeros);
   p.bias = static_cast<const uint16_t*>(bias);
-  p.out = static_cast<uint16_t*>(out);
-  p.M = (int)M;
   p.N = (int)N;
   p.K = (int)K;
   p.group = (int)group;
   p.epi = epi;
+  void* args[] = {&p};
+  // rows m0 .. m0 + m - 1
+  auto part = [&](int64_t m0, int64_t m) {
+    p.x = static_cast<const uint16_t*>(x) + m0 * K;
+    p.out = static_cast<uint16_t*>(out) + m0 * N;
+    p.M = (int)m;
+  };
   if (N < 4) {
-    void* args[] = {&p};
-    return launch(fn(&mmk::gemm_w4_narrow), dim3((unsigned)cdiv(M * N, 64)), 64, args, stream, "linear_w4 narrow");
+    const int64_t most = int64_t(1) << 30;
+    for (int64_t m0 = 0; m0 < M; m0 += most) {
+      part(m0, std::min(M - m0, most));
+      s = launch(fn(&mmk::gemm_w4_narrow), dim3((unsigned)cdiv(p.M * N, 64)), 64, args, stream, "linear_w4 narrow");
+      if (s != MM_OK) return s;
+    }
+    return MM_OK;
   }
   const int xr = M <= 4 ? 4 : M <= 16 ? 16 : M <= 32 ? 32 : M <= 48 ? 48 : 64;
-  const int64_t gy = cdiv(M, xr);
-  if (gy > 65535) return fail(MM_ERR_UNSUPPORTED, "M too large");
   // Measured (us, 1 / 2 / 4 column blocks): 1 x 4096 x 4096 4.1 / 5.1 / 6.7, 12 x
   // 6000 x 4096 8.7 / 6.6 / 8.7, 24 x 8192 x 8192 23.8 / 16.7 / 18.7, 10 x 11000 x
   // 4096 12.7 / 11.8 / 10.4, 64 x 14336 x 4096 39 / 26 / 20.
+  const int64_t blocks = cdiv(N, 16);
+  if (cdiv(blocks, 4) > kMaxRowsGridX) return fail(MM_ERR_UNSUPPORTED, "N must be at most 2^29 - 64");
   int cus = 0;
   if ((s = device_cus(&cus)) != MM_OK) return s;
-  const int64_t blocks = cdiv(N, 16);
-  const int nb = column_blocks(blocks, gy, cus, 10);
-  void* args[] = {&p};
-  return launch(w4_kernel(xr, nb, (int)group), dim3((unsigned)cdiv(blocks, nb), (unsigned)gy), mmk::kW4Waves * 64, args,
-                stream, "linear_w4");
+  const int nb = column_blocks(blocks, cdiv(M, xr), cus, 10);
+  for (int64_t m0 = 0; m0 < M; m0 += kMaxGridY * xr) {
+    part(m0, std::min(M - m0, kMaxGridY * xr));
+    s = launch(w4_kernel(xr, nb, (int)group), dim3((unsigned)cdiv(blocks, nb), (unsigned)cdiv(p.M, xr)),
+               mmk::kW4Waves * 64, args, stream, "linear_w4");
+    if (s != MM_OK) return s;
+  }
+  return MM_OK;
 }
 
 mm_status mm_linear_q8_workspace_size(int64_t M, int64_t N, int64_t K, int64_t* bytes) {
@@ -527,8 +560,7 @@ mm_status mm_linear_q8(const void* x, const float* x_scale, const void* W, const
   if (M <= 32 || (M <= kQ8Rows && N < 11000) || K == 0) {
     const int xr = M <= 4 ? 4 : M <= 16 ? 16 : M <= 32 ? 32 : 64;
     const int64_t blocks = cdiv(N, 16);
-    const int64_t gy = cdiv(M, xr);
-    if (gy > 65535) return fail(MM_ERR_UNSUPPORTED, "M too large");
+    if (cdiv(blocks, 4) > kMaxRowsGridX) return fail(MM_ERR_UNSUPPORTED, "N must be at most 2^29 - 64");
     // Few rows with at most two workgroups to a CU: one column block streams W
     // best (us, 1 / 2 / 4 blocks: 16 x 8192 x 8192 13.9 / 16.2 / 20.0, though 12 x
     // 6000 x 4096 9.3 / 8.6 / 12.6).  Otherwise by the shares of the CUs: 1 x 28672 x
@@ -537,9 +569,17 @@ mm_status mm_linear_q8(const void* x, const float* x_scale, const void* W, const
     // 23.2 / 18.2 / 25.2, 32 x 28672 x 8192 69.8 / 60.6 / 57.2.
     int cus = 0;
     if ((s = device_cus(&cus)) != MM_OK) return s;
-    const int nb = M <= 16 && blocks <= 2 * cus ? 1 : column_blocks(blocks, gy, cus, M <= 4 ? 1 : M <= 16 ? 3 : 10);
-    return launch(q8_rows_kernel(xr, nb), dim3((unsigned)cdiv(blocks, nb), (unsigned)gy), mmk::kW4Waves * 64, args, stream,
-                  "linear_q8 rows");
+    const int nb = M <= 16 && blocks <= 2 * cus ? 1 : column_blocks(blocks, cdiv(M, xr), cus, M <= 4 ? 1 : M <= 16 ? 3 : 10);
+    for (int64_t m0 = 0; m0 < M; m0 += kMaxGridY * xr) {  // (more than one turn only with K == 0)
+      p.x = static_cast<const uint8_t*>(x) + m0 * K;
+      p.xs = x_scale + m0;
+      p.out = static_cast<uint16_t*>(out) + m0 * N;
+      p.M = (int)std::min(M - m0, kMaxGridY * xr);
+      s = launch(q8_rows_kernel(xr, nb), dim3((unsigned)cdiv(blocks, nb), (unsigned)cdiv(p.M, xr)), mmk::kW4Waves * 64,
+                 args, stream, "linear_q8 rows");
+      if (s != MM_OK) return s;
+    }
+    return MM_OK;
   }
   const Q8Plan plan = q8_plan(M, N, K, workspace && M > kQ8Rows ? kQ8MaxChunks : 1);
   if (plan.tiles_m * plan.tiles_n * plan.chunks >= kLimit) return fail(MM_ERR_UNSUPPORTED, "more than 2^31 output tiles");

@@ -282,6 +282,7 @@ mm_status mm_rms_norm_backward(const void* dy, const void* h, const void* weight
  *   scales  [ceil(K / group)][N] bf16;  zeros the same shape, one byte each
  *   group   32, 64 or 128;  K a multiple of 8 (the last group may be short), at
  *           most 2^22
+ *   N       at most 2^29 - 64
  * Other arguments, the epilogue and errors as for mm_linear.
  *
  * Packed layout: [ceil(N/16)][ceil(K/128)] kilobytes.  In a kilobyte, 32-bit
@@ -297,7 +298,7 @@ mm_status mm_linear_w4(const void* x, const void* W, const void* scales, const v
 /* LinearOp form with e4m3 operands and row scales:
  *   out[M][N] = epi(x_scale[m] w_scale[n] (x . W^T) + bias), bf16 (RNE)
  *   x [M][K], W [N][K] e4m3 (OCP), K contiguous and a multiple of 16, at most
- *   2^22;  x_scale [M], w_scale [N] fp32.
+ *   2^22;  x_scale [M], w_scale [N] fp32.  Up to 32 rows N is at most 2^29 - 64.
  * fp32 sums; the scales multiply the sum, then the epilogue, then one rounding.
  * With a workspace (NULL: without), of the size the function below reports
  * (host arithmetic only; 0: the shape runs without one), a product of few

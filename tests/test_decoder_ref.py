@@ -157,6 +157,19 @@ def test_q8_refusals(lib):
     assert lib.mm_linear_q8_workspace_size(4, 64, 128, None) == INVALID
 
 
+def test_widths_past_one_launch_are_refused(lib):
+    """Before any device call, wherever the products of few rows would need more
+    than the 2^32 - 1 threads of a launch."""
+    A = [(i + 1) << 50 for i in range(6)]
+    wide = 1 << 29
+    for M in (1, 16, 64, 1000):
+        assert lib.mm_linear_w4(A[0], A[1], A[2], NULL, NULL, A[3], M, wide, 128, 128, 0, None) == UNSUPPORTED
+        assert "2^29" in lib.mm_last_error().decode()
+    for M, K in ((1, 128), (16, 128), (32, 128), (1, 0), (100, 0)):
+        assert lib.mm_linear_q8(A[0], A[1], A[2], A[3], NULL, A[4], M, wide, K, 0, NULL, 0, None) == UNSUPPORTED
+        assert "2^29" in lib.mm_last_error().decode()
+
+
 def test_python_checks_types_and_devices():
     x = torch.zeros((4, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="GPU"):

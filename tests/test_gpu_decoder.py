@@ -271,6 +271,29 @@ def test_rms_norm_past_32_bits(dev):
     close(y[-3:], want.double().cpu(), 2 * BF16 * want.double().abs().cpu(), "last rows")
 
 
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("q8", [False, True])
+def test_rms_norm_of_more_rows_than_a_launch_takes(dev, residual, q8):
+    """64 threads a row: 2^26 rows are 2^32 threads."""
+    rows, hidden, tail = (1 << 26) + 3, 8, 1000
+    x = torch.zeros((rows, hidden), dtype=torch.bfloat16, device=dev)
+    x[-tail:] = randn(gen(1), (tail, hidden)).bfloat16().to(dev)
+    x[0] = x[-1]
+    res = torch.ones_like(x) if residual else None
+    w = randn(gen(2), hidden).bfloat16().to(dev)
+    fn = mm.rms_norm_q8 if q8 else mm.rms_norm
+    got = fn(x, w, res)
+    want = fn(x[-tail:].contiguous(), w, res[-tail:].contiguous() if residual else None)
+    for g, e in zip(got, want):
+        g, e = (t.float() if t.dtype == torch.float8_e4m3fn else t for t in (g[-tail:], e))
+        assert torch.equal(g, e)
+    same = [t.float() if t.dtype == torch.float8_e4m3fn else t for t in (got[0][0], got[0][-1])]
+    assert torch.equal(*same)
+    # rows of zeros (of ones with the residual), the same all along
+    middle = got[1][1:rows - tail]
+    assert bool((middle == middle[0]).all())
+
+
 # ---- products with 4-bit weights -------------------------------------------
 
 def w4_inputs(M, N, K, group, zeros, seed, exact=False):
@@ -403,6 +426,35 @@ def test_linear_w4_past_32_bits(dev):
     assert torch.equal(got[:, -48:], want)
 
 
+def test_pack_w4_of_more_words_than_a_launch_takes(dev):
+    """A packed weight past 16 GiB (2^32 words, a thread each)."""
+    N, K = (1 << 21) + 16, 1 << 14
+    codes = torch.zeros((N, K), dtype=torch.uint8, device=dev)
+    tail = torch.randint(0, 16, (16, K), generator=gen(6), dtype=torch.uint8).to(dev)
+    codes[-16:] = tail
+    codes[:16] = tail
+    packed = mm.pack_w4(codes)
+    want = mm.pack_w4(tail)[0]
+    assert torch.equal(packed[0], want) and torch.equal(packed[-1], want)
+    assert not bool(packed[1:-1].view(torch.int64).any())
+
+
+@pytest.mark.parametrize("M,N,K", [(1431655777, 3, 8), (65535 * 64 + 70, 20, 128)])
+def test_linear_w4_of_more_rows_than_a_launch_takes(dev, M, N, K):
+    """Few columns: a thread per output.  Otherwise 65535 blocks of 64 rows."""
+    _, codes, s, z, bias = w4_inputs(1, N, K, 32, True, 9)
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device=dev)
+    tail = randn(gen(7), (200, K)).bfloat16().to(dev)
+    x[-200:] = tail
+    x[:200] = tail
+    W = mm.pack_w4(codes.to(dev))
+    args = (*on(dev, s, z, bias), "bias", 32)
+    got = mm.linear_w4(x, W, *args)
+    want = mm.linear_w4(tail, W, *args)
+    assert torch.equal(got[-200:], want) and torch.equal(got[:200], want)
+    assert torch.equal(got[200:-200].amax(0), bias.to(dev)) and torch.equal(got[200:-200].amin(0), bias.to(dev))
+
+
 # ---- products of e4m3 operands ---------------------------------------------
 
 def q8_inputs(M, N, K, seed, exact=False):
@@ -505,6 +557,14 @@ def test_linear_q8_empty(dev):
                            torch.empty((48, 0), device=dev).to(torch.float8_e4m3fn), torch.ones(48, device=dev),
                            bias, "bias")
         assert torch.equal(got, bias.expand(M, 48))
+
+
+def test_linear_q8_of_no_k_and_more_rows_than_a_launch_takes(dev):
+    M, N = 65535 * 64 + 70, 20
+    bias = randn(gen(1), N).bfloat16().to(dev)
+    got = mm.linear_q8(torch.empty((M, 0), device=dev).to(torch.float8_e4m3fn), torch.ones(M, device=dev),
+                       torch.empty((N, 0), device=dev).to(torch.float8_e4m3fn), torch.ones(N, device=dev), bias, "bias")
+    assert torch.equal(got.amax(0), bias) and torch.equal(got.amin(0), bias)
 
 
 @pytest.mark.parametrize("M", [2, 130])
