@@ -16,6 +16,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -58,39 +59,44 @@ def _link(out: str, objs) -> list:
 def build(verbose: bool = False) -> str:
     """Builds libmm.so and the race-check libmm_fullsync.so (the hipcc runs of
     every source side by side, then the two links); returns the path of
-    libmm.so.  Objects are linked in the order of SOURCES."""
+    libmm.so.  Objects are linked in the order of SOURCES.  They and the
+    compiler's output lie in a directory of this build's own, and the libraries
+    and the remarks are moved into place at the end: builds at the same time
+    do not read each other's files, and a failed one changes none."""
     os.makedirs(BUILD_DIR, exist_ok=True)
-    jobs = []
-    for lib, defines in ((LIB, ()), (LIB_FULLSYNC, ("MM_DEBUG_FULL_SYNC",))):
-        for source in SOURCES:
-            stem = os.path.splitext(source)[0] + ("" if lib == LIB else "_fullsync")
-            obj = os.path.join(BUILD_DIR, stem + ".o")
-            cmd = _compile(source, obj, defines)
+    with tempfile.TemporaryDirectory(dir=BUILD_DIR) as work:
+        jobs = []
+        for lib, defines in ((LIB, ()), (LIB_FULLSYNC, ("MM_DEBUG_FULL_SYNC",))):
+            for source in SOURCES:
+                stem = os.path.join(work, os.path.splitext(source)[0] + ("" if lib == LIB else "_fullsync"))
+                cmd = _compile(source, stem + ".o", defines)
+                if verbose:
+                    print(" ".join(cmd), flush=True)
+                # compiler output to a file (a pipe could fill while the other jobs run)
+                with open(stem + ".txt", "w") as f:
+                    proc = subprocess.Popen(cmd, stdout=subprocess.DEVNULL, stderr=f)
+                jobs.append((lib, source, stem, proc))
+        failed = []
+        for lib, source, stem, proc in jobs:
+            if proc.wait() != 0:
+                with open(stem + ".txt") as f:
+                    errs = [ln for ln in f.read().splitlines() if "error" in ln]
+                failed.append(f"hipcc failed for {source} ({os.path.basename(lib)}):\n" + "\n".join(errs[:40]))
+        if failed:
+            raise RuntimeError("\n".join(failed))
+        linked = []
+        for lib in (LIB, LIB_FULLSYNC):
+            out = os.path.join(work, os.path.basename(lib))
+            cmd = _link(out, [stem + ".o" for (of, _, stem, _) in jobs if of == lib])
             if verbose:
                 print(" ".join(cmd), flush=True)
-            # compiler output to a file (a pipe could fill while the other jobs run)
+            subprocess.run(cmd, check=True)
+            linked.append((out, lib))
+        for lib, source, stem, _ in jobs:
             if lib == LIB:
-                log = REMARKS if source == "mm_api.hip" else REMARKS_DECODER
-            else:
-                log = os.path.join(BUILD_DIR, stem + "_build.txt")
-            with open(log, "w") as f:
-                proc = subprocess.Popen(cmd, stdout=subprocess.DEVNULL, stderr=f)
-            jobs.append((lib, source, obj, log, proc))
-    failed = []
-    for lib, source, obj, log, proc in jobs:
-        if proc.wait() != 0:
-            with open(log) as f:
-                errs = [ln for ln in f.read().splitlines() if "error" in ln]
-            failed.append(f"hipcc failed for {source} ({os.path.basename(lib)}):\n" + "\n".join(errs[:40]))
-    if failed:
-        raise RuntimeError("\n".join(failed))
-    for lib in (LIB, LIB_FULLSYNC):
-        tmp = lib + ".tmp%d" % os.getpid()
-        cmd = _link(tmp, [obj for (of, _, obj, _, _) in jobs if of == lib])
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        subprocess.run(cmd, check=True)
-        os.replace(tmp, lib)
+                linked.append((stem + ".txt", REMARKS if source == "mm_api.hip" else REMARKS_DECODER))
+        for made, place in linked:
+            os.replace(made, place)
     return LIB
 
 
