@@ -54,21 +54,71 @@ __device__ __forceinline__ uint16_t decoder_epilogue(float v, const uint16_t* bi
 __device__ __forceinline__ void keep_in_registers(uint32_t& mask, uint32_t& bits) {
   asm volatile("" : "+s"(mask), "+v"(bits));
 }
-// Output (m, n) from the definition, term by term.  The kernel's offset form
-// turns an infinite activation (or a sum that overflows) into a NaN of its
-// own making; those outputs, rare and never in a finite model, are computed
-// again this way, which gives them their IEEE class.
-__device__ __forceinline__ float w4_dot(const W4Params& p, int m, int n) {
-  const int kblocks = (p.K + 127) / 128;
-  const uint32_t* W = reinterpret_cast<const uint32_t*>(p.W);
-  float v = 0.f;
-  for (int k = 0; k < p.K; ++k) {
-    const int g = (k >> 3) & 3, j = (k >> 5) & 3, e = k & 7;
-    const uint32_t word = W[(((int64_t)(n >> 4) * kblocks + (k >> 7)) * 64 + 16 * g + (n & 15)) * 4 + j];
-    const int q = (word >> (4 * ((e >> 1) + 4 * (e & 1)))) & 15;
+// 32 terms of output (m, n) from the definition, added to v: those of 16 bytes of W,
+// its words j = 0..3 at k = 128 kb + 32 j + 8 g .. + 7.
+__device__ __forceinline__ float w4_terms(const W4Params& p, int m, int n, int kb, int g, float v) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(
+      p.W + ((int64_t)(n >> 4) * ((p.K + 127) / 128) + kb) * 64 + 16 * g + (n & 15));
+#pragma unroll 1
+  for (int j = 0; j < 4; ++j) {
+    const int k = 128 * kb + 32 * j + 8 * g;
+    if (k >= p.K) break;
     const int64_t at = (int64_t)(k / p.group) * p.N + n;
-    const float z = p.zeros ? (float)p.zeros[at] : 8.0f;
-    v = __builtin_fmaf(bf16_float(p.x[(int64_t)m * p.K + k]), ((float)q - z) * bf16_float(p.scales[at]), v);
+    const u32x4 x = *reinterpret_cast<const u32x4*>(p.x + (int64_t)m * p.K + k);
+    const float s = bf16_float(p.scales[at]), z = p.zeros ? (float)p.zeros[at] : 8.0f;
+    const uint32_t word = w[j];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int q = (word >> (4 * ((e >> 1) + 4 * (e & 1)))) & 15;
+      v = __builtin_fmaf(bf16_float((uint16_t)(x[e >> 1] >> (16 * (e & 1)))), ((float)q - z) * s, v);
+    }
+  }
+  return v;
+}
+
+// Outputs (m, 16 block + 0..15) from the definition, by a whole wave: a lane gets that
+// of column lane % 16, right where `wanted`.  The kernel's offset form turns an
+// infinite activation (or a sum that overflows) into a NaN of its own making; outputs
+// that are not finite are computed again this way, which gives them their IEEE class.
+// The first pass takes only the steps with an activation or a scale that is not
+// finite: they decide the class, and steps of finite terms leave it.  The second,
+// where a sum of finite terms overflowed, takes every step.  A row of 16 x 28672 x
+// 8192 with a NaN or an infinity somewhere takes the call from 32 to 43 or 50 us, 16 rows of
+// NaN or infinities to 125 (a thread per output, term by term: 1850 and 7300).
+__device__ __forceinline__ float w4_again(const W4Params& p, int m, int block, bool wanted, int lane) {
+  // (opaque, or what depends on the lane alone is computed before the K loop and
+  // kept in registers there)
+  asm volatile("" : "+v"(lane));
+  const int kblocks = (p.K + 127) / 128, n = min(16 * block + (lane & 15), p.N - 1);
+  float v = 0.f;
+  for (int pass = 0; pass < 2; ++pass) {
+    v = 0.f;
+    for (int t = 0; t < kblocks; t += 4) {
+      uint64_t steps = ~uint64_t(0);  // 16 bits (lanes) each
+      if (pass == 0) {
+        // lanes 16 i .. 16 i + 15 look at step t + i: 8 activations each, a column's scales
+        bool odd = false;
+        if (t + (lane >> 4) < kblocks) {
+          const u32x4 x = *reinterpret_cast<const u32x4*>(p.x + (int64_t)m * p.K + min(128 * t + 8 * lane, p.K - 8));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int group = min(128 * (t + (lane >> 4)) + 32 * j, p.K - 8) / p.group;
+            odd |= (x[j] & 0x7f80u) == 0x7f80u || (x[j] >> 16 & 0x7f80u) == 0x7f80u ||
+                   (p.scales[(int64_t)group * p.N + n] & 0x7f80u) == 0x7f80u;
+          }
+        }
+        steps = __ballot(odd);
+      }
+      const int end = min(t + 4, kblocks);
+      for (int kb = t; kb < end; ++kb, steps >>= 16)
+        if (steps & 0xffff) v = w4_terms(p, m, n, kb, lane >> 4, v);
+      // a NaN (in any of a column's four lanes) is its result
+      const uint64_t nan = __ballot(v != v);
+      if (!__any(wanted && !((nan | nan >> 16 | nan >> 32 | nan >> 48) >> (lane & 15) & 1))) break;
+    }
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+    if (!__any(wanted && __builtin_isfinite(v))) break;
   }
   return v;
 }
@@ -130,8 +180,10 @@ struct W4Tile {
 // (the nibbles' widening and two FMAs per output and group) together with the
 // activations, which every workgroup fetches from L2: 64 x 14336 x 4096 18.1 us
 // against a floor of 7.
+//
+// (16 rows: the LDS holds two workgroups, and so do the registers, of at most 128.)
 template <int XR, int NB, int G, int WV>
-__global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
+__global__ void __launch_bounds__(WV * 64, XR == 16 ? 4 : 2) gemm_w4(W4Params p) {
   constexpr int MB = XR < 16 ? 1 : XR / 16;
   constexpr int AB = MB * NB;
   constexpr int GP = 128 / G;             // groups per step
@@ -395,25 +447,40 @@ __global__ void __launch_bounds__(WV * 64) gemm_w4(W4Params p) {
       for (int i = 0; i < 4; ++i) v[i] += u[i];
     }
     // lane l of block (a, b): rows 16 a + 4 (l / 16) + i, column 16 b + l % 16
-    const int n = 16 * (b0 + ab % NB) + (l & 15);
-    if (n >= p.N) continue;
+    const int block = b0 + ab % NB, n = 16 * block + (l & 15), mb = m0 + 16 * (ab / NB);
+    uint32_t again = 0;  // which of the four are not finite
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int m = m0 + 16 * (ab / NB) + 4 * (l >> 4) + i;
-      if (m >= p.M) continue;
-      float o = v[i];
-      if (!__builtin_isfinite(o)) o = w4_dot(p, m, n);
-      p.out[(int64_t)m * p.N + n] = decoder_epilogue(o, p.bias, p.epi, n);
+      const int m = mb + 4 * (l >> 4) + i;
+      if (n >= p.N || m >= p.M) continue;
+      if (__builtin_isfinite(v[i]))
+        p.out[(int64_t)m * p.N + n] = decoder_epilogue(v[i], p.bias, p.epi, n);
+      else
+        again |= 1u << i;
+    }
+    // row by row (whole waves get here: AB * 64 values, WV * 64 threads)
+    for (int r = 0; __any(again != 0); ++r) {
+      const bool mine = (l >> 4) == (r >> 2) && (again >> (r & 3) & 1);
+      const uint64_t lanes = __ballot(mine);
+      if (lanes == 0) continue;
+      const bool column = (lanes | lanes >> 16 | lanes >> 32 | lanes >> 48) >> (l & 15) & 1;
+      const float o = w4_again(p, mb + r, block, column, l);
+      if (mine) {
+        p.out[(int64_t)(mb + r) * p.N + n] = decoder_epilogue(o, p.bias, p.epi, n);
+        again &= ~(1u << (r & 3));
+      }
     }
   }
 }
 
-// Fewer than four columns: every output term by term, one per thread.
+// Fewer than four columns: every output from the definition, one per thread.
 __global__ void __launch_bounds__(64) gemm_w4_narrow(W4Params p) {
   const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x;
   if (i >= (int64_t)p.M * p.N) return;
   const int m = (int)(i / p.N), n = (int)(i % p.N);
-  p.out[i] = decoder_epilogue(w4_dot(p, m, n), p.bias, p.epi, n);
+  float v = 0.f;
+  for (int c = 0; c < 4 * ((p.K + 127) / 128); ++c) v = w4_terms(p, m, n, c >> 2, c & 3, v);
+  p.out[i] = decoder_epilogue(v, p.bias, p.epi, n);
 }
 
 // Lays out codes [N][K] (one byte each, the low four bits taken) as packed

@@ -402,6 +402,55 @@ def test_linear_w4_not_finite(dev, M):
     assert got[3:].isfinite().all()
 
 
+@pytest.mark.parametrize("M", [2, 30, 64])
+def test_linear_w4_sums_that_only_the_offset_form_overflows(dev, M):
+    """x (16 + code) passes fp32's range where x (code - zero) does not, and an
+    infinite scale takes its own column alone."""
+    N, K, group = 70, 392, 64
+    x, codes, s, z, _ = w4_inputs(M, N, K, group, True, 12, exact=True)
+    x[1] = 0.0
+    x[1, 3], x[1, 390] = 2.0 ** 125, -2.0 ** 124
+    codes[:, 3], codes[:, 390] = 9, 12
+    z[0], z[6] = 8, 7
+    s[0], s[6] = 2.0, 0.5
+    s[2, 5] = float("inf")
+    got = mm.linear_w4(*on(dev, x), mm.pack_w4(codes.to(dev)), *on(dev, s, z), group=group).cpu()
+    want = (x.double() @ ref.w4_weight(codes, s, z, group).t()).float().bfloat16()
+    same_class(got.float(), want.float())
+    fine = want.isfinite()
+    assert fine[1].sum() == N - 1 and torch.equal(got[fine], want[fine])
+
+
+@pytest.mark.parametrize("rows", ["one", "all"])
+@pytest.mark.parametrize("what", ["a NaN", "NaN", "an infinity", "infinities"])
+def test_linear_w4_not_finite_takes_no_hundredfold(dev, rows, what):
+    """Padded rows may hold anything: a call whose outputs are not finite takes
+    longer, but by no orders of magnitude (here at most 25 times and 1 ms)."""
+    M, N, K = 16, 8192, 8192
+    W = torch.randint(0, 256, (N // 16, K // 128, 1024), generator=gen(32), dtype=torch.uint8).to(dev)
+    x = randn(gen(33), (M, K)).bfloat16()
+    s = (randn(gen(34), (K // 128, N), 0.3, 1.0) * K ** -0.5).bfloat16().to(dev)
+    bad = x.clone()
+    value = float("nan") if "NaN" in what else float("inf")
+    for row in ([M - 1] if rows == "one" else range(M)):
+        bad[row, slice(None) if what in ("NaN", "infinities") else 17 * row + 5] = value
+
+    def median(t):
+        times = []
+        for _ in range(6):
+            start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            start.record()
+            mm.linear_w4(t, W, s)
+            end.record()
+            end.synchronize()
+            times.append(start.elapsed_time(end))
+        return sorted(times[1:])[2]
+
+    fine, slow = median(x.to(dev)), median(bad.to(dev))
+    print(f"{fine * 1e3:.0f} us, not finite {slow * 1e3:.0f} us")
+    assert slow <= 25 * fine and slow <= 1.0
+
+
 def test_linear_w4_empty(dev):
     bias = randn(gen(1), 40).bfloat16().to(dev)
     s = torch.ones((0, 40), device=dev).bfloat16()
