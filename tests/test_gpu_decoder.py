@@ -96,6 +96,16 @@ def test_rms_norm(dev, rows, hidden, dtype, residual):
     close(val, wy, tol, "q")
 
 
+@pytest.mark.parametrize("hidden", [4096, 8192])
+def test_rms_norm_rstd_is_mostly_the_nearest(dev, hidden):
+    """A sum in fp32 and one rounding after it leave most rows' rstd the nearest
+    fp32 value; a square root and a division, each rounded, left 61 %."""
+    x = randn(gen(hidden), (4096, hidden), 2.0).bfloat16().to(dev)
+    _, _, rstd = mm.rms_norm(x, torch.ones(hidden, device=dev).bfloat16())
+    want = (1.0 / (x.double().square().mean(1) + 1e-6).sqrt()).float()
+    assert float((rstd == want).float().mean()) >= 0.7
+
+
 @pytest.mark.parametrize("rows,hidden", [(1, 8192), (64, 4096), (300, 1032), (5, 16384)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_rms_norm_q8_codes_are_the_rounded_quotients(dev, rows, hidden, dtype):
