@@ -298,14 +298,16 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) rms_norm_grad(RmsNormGradP
     }
   };
   if constexpr (AHEAD) {
-    // the next row's loads go out before this row's sum is waited for
+    // the next row's loads go out before this row's sum is waited for (past the
+    // last, this row's again, unused: another workgroup's may be written meanwhile,
+    // where dh is dres)
     Row a, b;
-    const int64_t G = gridDim.x, last = p.rows - 1;
+    const int64_t G = gridDim.x;
     load(blockIdx.x, a);
     for (int64_t row = blockIdx.x; row < p.rows; row += 2 * G) {
-      load(min(row + G, last), b);
+      load(row + G < p.rows ? row + G : row, b);
       process(row, a, 0);
-      load(min(row + 2 * G, last), a);
+      load(row + 2 * G < p.rows ? row + 2 * G : row, a);
       if (row + G < p.rows) process(row + G, b, 1);
     }
   } else {

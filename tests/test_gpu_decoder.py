@@ -269,6 +269,20 @@ def test_rms_norm_backward_many_rows(dev, rows, hidden, dtype, dres):
     assert torch.equal(again, got) and torch.equal(gw, gw2), "not reproducible"
 
 
+@pytest.mark.parametrize("rows,hidden", [(2049, 64), (2051, 520), (3100, 4096), (2500, 8192), (2049, 16392)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rms_norm_backward_many_rows_in_place(dev, rows, hidden, dtype):
+    """dh over dres, with counts of rows that leave workgroups with one row fewer than others."""
+    g = torch.Generator(device=dev).manual_seed(rows)
+    h, d = (torch.randn((rows, hidden), generator=g, device=dev).to(dtype) for _ in range(2))
+    dy = torch.randn((rows, hidden), generator=g, device=dev).bfloat16()
+    w = torch.randn(hidden, generator=g, device=dev).bfloat16()
+    rstd = torch.rsqrt(h.float().square().mean(1) + 1e-6)
+    dh, dw = mm.rms_norm_backward(dy, h, w, rstd, d)
+    into, dw2 = mm.rms_norm_backward(dy, h, w, rstd, d, out=d)
+    assert into is d and torch.equal(d, dh) and torch.equal(dw2, dw)
+
+
 def test_rms_norm_past_32_bits(dev):
     """rows * hidden past 2^31 elements: the last rows against the same rows alone."""
     rows, hidden = 66000, 32768
