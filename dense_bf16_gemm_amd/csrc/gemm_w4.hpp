@@ -174,12 +174,14 @@ struct W4Tile {
 // column read theirs (a load per column block and group would cost more of
 // the address unit than the weight does).
 //
-// Measured: 16 x 28672 x 8192 by groups of 128 with zeros 26.6 us, 4.7 TB/s (a
-// large copy runs at 4.8); 1 x 4096 x 4096 4.3 us, where the launch and the
-// one step's latency are most of it.  From 33 rows on the vector ALU bounds it
-// (the nibbles' widening and two FMAs per output and group) together with the
-// activations, which every workgroup fetches from L2: 64 x 14336 x 4096 18.1 us
-// against a floor of 7.
+// Measured: 16 x 28672 x 8192 by groups of 128 with zeros 26.9 us, 4.6 TB/s (a
+// large copy runs at 4.8); 1 x 4096 x 4096 4.4 us, where the launch and the
+// one step's latency are most of it.  From 17 rows on no unit is at its limit; a step
+// fetches its activations from L2 (every workgroup all of them), widens and multiplies
+// in turn, and two waves per SIMD and few steps per wave do not overlap these
+// fully: 64 x 14336 x 4096 takes 18.5 us against a floor of 7, with 177 MB of L2 requests
+// (117 of activations; 9.6 TB/s), the vector ALU busy in 51 % of a working CU's cycles and the
+// matrix units in 27; 24 x 8192 x 8192 13.6 against 7.5, 148 MB, 43 and 23 %.
 //
 // (16 rows: the LDS holds two workgroups, and so do the registers, of at most 128.)
 template <int XR, int NB, int G, int WV>
@@ -391,7 +393,10 @@ __global__ void __launch_bounds__(WV * 64, XR == 16 ? 4 : 2) gemm_w4(W4Params p)
 
   if (wave < kblocks) {
     // (past its last step a wave loads the last one of all again, unused: the
-    // loop then has one shape, and its waits count loads exactly)
+    // loop then has one shape, which the halves' counted waits need.  Of whole steps
+    // every second one first waits, in the built code, for all of its own loads:
+    // where the second step of a turn is left out its loads are still pending at
+    // the loop's head)
     Step s0, s1;
     if constexpr (HALVES) {
       load(wave, s0);

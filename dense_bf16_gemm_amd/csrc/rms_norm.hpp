@@ -213,9 +213,13 @@ __global__ void __launch_bounds__(1024) rms_norm(RmsNormParams p) {
 //
 // A row's vectors are held as stored and widened where they are used, which
 // keeps four vectors per thread within the 128 registers of 1024 threads.
-// AHEAD (up to 512 threads): a row's loads are issued while the row before is
-// summed.  8192 x 4096 bf16 with dres: 58.0 us (4.63 TB/s); 63.6 without AHEAD,
-// on twice the workgroups and so with twice the parts of dw to write and add.
+// AHEAD (up to 512 threads): a row's loads, dres among them, are issued before the
+// row before is summed, and the weight stays in registers.  8192 x 4096 bf16 with dres:
+// 58.7 us (4.6 TB/s); 63.6 without AHEAD, which loads dres and the weight after the sum, on
+// twice the workgroups and so with twice the parts of dw to write and add.  The
+// compiler waits for most of those loads ahead of the sum all the same (around the
+// branch on dres it merges registers that are being loaded with ones that are not),
+// so what keeps the memory busy meanwhile are the CU's other waves.
 template <bool F32, int VPT, bool AHEAD>
 __global__ void __launch_bounds__(AHEAD ? 512 : 1024) rms_norm_grad(RmsNormGradParams p) {
   __shared__ float slot[2][16];
@@ -329,7 +333,9 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) rms_norm_grad(RmsNormGradP
 // The gradient of few rows in one launch (a second one costs the call 4 us, and
 // a row per CU leaves most of a CU idle): the first workgroups sum 64 columns of
 // dw each, reading dy and h for it once more, the others take one row each, as
-// above.  1 x 4096 takes 2.7 us, which is latency, 512 x 8192 11.3 (3 TB/s).
+// above.  1 x 4096 takes 2.7 us, which is latency, 512 x 8192 10 (3.4 TB/s), 2048 x 1024
+// 16.6 (1 TB/s): there 16 workgroups sum the columns, whose threads have one of
+// their 32 rows in flight at a time.
 template <bool F32, int VPT>
 __global__ void __launch_bounds__(1024) rms_norm_grad_few(RmsNormGradParams p, float* dweight) {
   __shared__ float slot[16];

@@ -212,7 +212,8 @@ def linear_q8(x: torch.Tensor, x_scale: torch.Tensor, W: torch.Tensor, w_scale: 
               out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """out = epi(x_scale[:, None] * w_scale * (x @ W.T) + bias) with e4m3 x
     [M, K] and W [N, K] (K a multiple of 16) and fp32 row scales x_scale [M],
-    w_scale [N]; fp32 sums, bf16 output.  Epilogues and bias as for linear."""
+    w_scale [N]; bf16 output, sums as mm_linear_q8 in mm.h says.  Epilogues and
+    bias as for linear."""
     index = _operand(x, "x", (_E4M3,))
     M, K = x.shape
     if not x.is_contiguous():

@@ -299,7 +299,10 @@ mm_status mm_linear_w4(const void* x, const void* W, const void* scales, const v
  *   out[M][N] = epi(x_scale[m] w_scale[n] (x . W^T) + bias), bf16 (RNE)
  *   x [M][K], W [N][K] e4m3 (OCP), K contiguous and a multiple of 16, at most
  *   2^22;  x_scale [M], w_scale [N] fp32.  Up to 32 rows N is at most 2^29 - 64.
- * fp32 sums; the scales multiply the sum, then the epilogue, then one rounding.
+ * Sums are fp32 from one matrix instruction to the next; inside one, e4m3 products are
+ * added with the hardware's fewer bits (some 1.5e-5 of a sum of normally distributed
+ * operands, at worst 2^-14.8 of the sum of the magnitudes that one instruction adds).
+ * The scales multiply the sum, then the epilogue, then one rounding.
  * With a workspace (NULL: without), of the size the function below reports
  * (host arithmetic only; 0: the shape runs without one), a product of few
  * output tiles has its K cut into chunks, whose fp32 sums a second kernel adds
