@@ -83,38 +83,46 @@ __device__ __forceinline__ float w4_terms(const W4Params& p, int m, int n, int k
 // The first pass takes only the steps with an activation or a scale that is not
 // finite: they decide the class, and steps of finite terms leave it.  The second,
 // where a sum of finite terms overflowed, takes every step.  A row of 16 x 28672 x
-// 8192 with a NaN or an infinity somewhere takes the call from 32 to 43 or 50 us, 16 rows of
-// NaN or infinities to 125 (a thread per output, term by term: 1850 and 7300).
+// 8192 with a NaN or an infinity somewhere takes the call from 32 to 44 us, 16 rows of NaN or
+// infinities to 135 (a thread per output, term by term: 1850 and 7300).
 __device__ __forceinline__ float w4_again(const W4Params& p, int m, int block, bool wanted, int lane) {
   // (opaque, or what depends on the lane alone is computed before the K loop and
   // kept in registers there)
   asm volatile("" : "+v"(lane));
   const int kblocks = (p.K + 127) / 128, n = min(16 * block + (lane & 15), p.N - 1);
+  // lanes 16 i .. 16 i + 15 look at step t + i: 8 activations each, a column's scales
+  auto odd = [&](int t) __attribute__((always_inline)) {
+    const int kb = t + (lane >> 4);
+    const u32x4 x = *reinterpret_cast<const u32x4*>(p.x + (int64_t)m * p.K + min(128 * t + 8 * lane, p.K - 8));
+    bool o = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t s = p.scales[(int64_t)(min(128 * kb + 32 * j, p.K - 8) / p.group) * p.N + n];
+      o |= (x[j] & 0x7f80u) == 0x7f80u || (x[j] >> 16 & 0x7f80u) == 0x7f80u || (s & 0x7f80u) == 0x7f80u;
+    }
+    return kb < kblocks && o;
+  };
   float v = 0.f;
   for (int pass = 0; pass < 2; ++pass) {
     v = 0.f;
-    for (int t = 0; t < kblocks; t += 4) {
-      uint64_t steps = ~uint64_t(0);  // 16 bits (lanes) each
+    for (int t = 0; t < kblocks; t += 8) {
+      uint64_t steps[2] = {~uint64_t(0), ~uint64_t(0)};  // 16 bits (lanes) each
       if (pass == 0) {
-        // lanes 16 i .. 16 i + 15 look at step t + i: 8 activations each, a column's scales
-        bool odd = false;
-        if (t + (lane >> 4) < kblocks) {
-          const u32x4 x = *reinterpret_cast<const u32x4*>(p.x + (int64_t)m * p.K + min(128 * t + 8 * lane, p.K - 8));
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int group = min(128 * (t + (lane >> 4)) + 32 * j, p.K - 8) / p.group;
-            odd |= (x[j] & 0x7f80u) == 0x7f80u || (x[j] >> 16 & 0x7f80u) == 0x7f80u ||
-                   (p.scales[(int64_t)group * p.N + n] & 0x7f80u) == 0x7f80u;
-          }
-        }
-        steps = __ballot(odd);
+        const bool o0 = odd(t), o1 = odd(t + 4);
+        steps[0] = __ballot(o0);
+        steps[1] = __ballot(o1);
       }
-      const int end = min(t + 4, kblocks);
-      for (int kb = t; kb < end; ++kb, steps >>= 16)
-        if (steps & 0xffff) v = w4_terms(p, m, n, kb, lane >> 4, v);
-      // a NaN (in any of a column's four lanes) is its result
-      const uint64_t nan = __ballot(v != v);
-      if (!__any(wanted && !((nan | nan >> 16 | nan >> 32 | nan >> 48) >> (lane & 15) & 1))) break;
+      bool done = false;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (done || steps[h] == 0) continue;
+        for (int i = 0; i < 4; ++i, steps[h] >>= 16)
+          if ((steps[h] & 0xffff) && t + 4 * h + i < kblocks) v = w4_terms(p, m, n, t + 4 * h + i, lane >> 4, v);
+        // a NaN (in any of a column's four lanes) is its result
+        const uint64_t nan = __ballot(v != v);
+        done = !__any(wanted && !((nan | nan >> 16 | nan >> 32 | nan >> 48) >> (lane & 15) & 1));
+      }
+      if (done) break;
     }
     v += __shfl_xor(v, 16);
     v += __shfl_xor(v, 32);
