@@ -1,7 +1,8 @@
 // mm_decoder.hip -- C ABI of the decoder-layer operators (declared in
-// include/mm.h): the residual addition with its RMS norm and gradient, and
-// the products with 4-bit and 8-bit weights.  Argument checks, the choice of
-// a kernel's shape, launches.
+// include/mm.h): the residual addition with its RMS norm or layer norm and their
+// gradients, the products with 4-bit and 8-bit weights, the linear layer with an adapter
+// per row, and the mixture-of-experts FFN.  Argument checks, the choice of a
+// kernel's shape, launches.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -10,6 +11,9 @@
 #include "rms_norm.hpp"
 #include "gemm_w4.hpp"
 #include "gemm_q8.hpp"
+#include "layer_norm.hpp"
+#include "moe_ffn.hpp"
+#include "linear_lora.hpp"
 
 using namespace mmh;
 
@@ -331,6 +335,120 @@ Q8Plan q8_plan(int64_t M, int64_t N, int64_t K, int64_t max_chunks) {
   return best;
 }
 
+// ----------------------------------------------------------------------------
+// Layer norm
+// ----------------------------------------------------------------------------
+struct Span {
+  const void* p;
+  int64_t n;
+};
+
+// Whether an output shares memory with an input or another output.
+template <size_t I, size_t O>
+bool any_overlap(const Span (&in)[I], const Span (&out)[O]) {
+  for (size_t o = 0; o < O; ++o) {
+    for (size_t i = 0; i < I; ++i)
+      if (overlaps(out[o].p, out[o].n, in[i].p, in[i].n)) return true;
+    for (size_t q = 0; q < o; ++q)
+      if (overlaps(out[o].p, out[o].n, out[q].p, out[q].n)) return true;
+  }
+  return false;
+}
+
+template <bool F32>
+const void* layer_norm_kernel(int vpt) {
+  return vpt == 1 ? fn(&mmk::layer_norm<F32, 1>) : vpt == 2 ? fn(&mmk::layer_norm<F32, 2>) : fn(&mmk::layer_norm<F32, 4>);
+}
+template <bool F32>
+const void* layer_norm_grad_kernel(int vpt, int threads) {
+  if (threads <= 512)
+    return vpt == 1 ? fn(&mmk::layer_norm_grad<F32, 1, true>) : fn(&mmk::layer_norm_grad<F32, 2, true>);
+  return fn(&mmk::layer_norm_grad<F32, 2, false>);
+}
+template <bool F32>
+const void* layer_norm_grad_few_kernel(int vpt) {
+  return vpt == 1   ? fn(&mmk::layer_norm_grad_few<F32, 1>)
+         : vpt == 2 ? fn(&mmk::layer_norm_grad_few<F32, 2>)
+                    : fn(&mmk::layer_norm_grad_few<F32, 4>);
+}
+
+// Rows whose gradient is one launch (as of the RMS norm).
+bool layer_norm_few(int64_t rows, int64_t hidden) { return rows <= kFewRows || hidden > kLongRow; }
+
+// ----------------------------------------------------------------------------
+// Linear layer with an adapter per row
+// ----------------------------------------------------------------------------
+constexpr int64_t kLoraRows = 32;
+
+struct LoraPlan {
+  int64_t slices = 1, kc = 0;  // of K, for the adapters' first product
+  int mb = 1;                  // blocks of 16 rows there
+  int64_t v = 0, acc = 0, split = 0;  // workspace bytes
+};
+
+int64_t round256(int64_t n) { return cdiv(n, 256) * 256; }
+
+mm_status lora_plan(int64_t M, int64_t N, int64_t K, int64_t R, LoraPlan* p) {
+  p->mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+  const int64_t blocks = cdiv(M, 16 * p->mb);
+  const int64_t want = std::min<int64_t>(16, std::max<int64_t>(1, 512 / blocks));
+  p->kc = std::max<int64_t>(512, cdiv(cdiv(K, want), 64) * 64);
+  p->slices = cdiv(K, p->kc);
+  p->v = round256(p->slices * M * R * 4);
+  if (M <= kLoraRows) return MM_OK;
+  p->acc = round256(M * N * 4);
+  int64_t split = 0;
+  const mm_status s = mm_workspace_size(0, M, N, K, MM_NT, &split);
+  p->split = round256(split);
+  return s;
+}
+
+mm_status check_lora(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
+  if (M < 0 || N < 0 || K < 0 || R < 0 || L < 0) return fail(MM_ERR_INVALID_VALUE, "negative size");
+  if (M >= kLimit || N >= kLimit || K >= kLimit || L >= kLimit)
+    return fail(MM_ERR_UNSUPPORTED, "M, N, K and the number of adapters must be below 2^31");
+  if (R > mmk::kLoraMaxRank) return fail(MM_ERR_UNSUPPORTED, "rank must be at most 256");
+  if (R % 8 != 0) return fail(MM_ERR_MISALIGNED, "rank must be a multiple of 8");
+  if (K % 8 != 0) return fail(MM_ERR_MISALIGNED, "K must be a multiple of 8 elements");
+  if (K > (int64_t(1) << 22)) return fail(MM_ERR_UNSUPPORTED, "K must be at most 2^22");
+  if (N > (int64_t(1) << 27) - 16) return fail(MM_ERR_UNSUPPORTED, "N must be at most 2^27 - 16");
+  const int64_t room = int64_t(1) << 60;
+  if (M > 0 && (N > room / M || K > room / M)) return fail(MM_ERR_UNSUPPORTED, "an operand spans 2^60 elements or more");
+  if (L * R > 0 && (N > room / (L * R) || K > room / (L * R)))
+    return fail(MM_ERR_UNSUPPORTED, "an operand spans 2^60 elements or more");
+  return MM_OK;
+}
+
+// ----------------------------------------------------------------------------
+// Mixture of experts
+// ----------------------------------------------------------------------------
+constexpr int64_t kMoeMaxWidth = int64_t(1) << 18;
+constexpr int64_t kMoeTableBytes = (sizeof(mmk::MoeTables) + 255) / 256 * 256;
+
+mm_status check_moe(int64_t T, int64_t E, int64_t H, int64_t I, int64_t k) {
+  if (T < 0 || E < 0 || H < 0 || I < 0 || k < 0) return fail(MM_ERR_INVALID_VALUE, "negative size");
+  if (k > E) return fail(MM_ERR_INVALID_VALUE, "top_k must not be larger than the number of experts");
+  if (T > mmk::kMoeTokens) return fail(MM_ERR_UNSUPPORTED, "at most 64 tokens");
+  if (E > mmk::kMoeExperts) return fail(MM_ERR_UNSUPPORTED, "at most 512 experts");
+  if (k > mmk::kMoeTopK) return fail(MM_ERR_UNSUPPORTED, "top_k must be at most 16");
+  if (H > kMoeMaxWidth || I > kMoeMaxWidth) return fail(MM_ERR_UNSUPPORTED, "H and I must be at most 2^18");
+  if (H % 8 != 0 || I % 8 != 0) return fail(MM_ERR_MISALIGNED, "H and I must be multiples of 8 elements");
+  return MM_OK;
+}
+
+const void* moe_route_kernel(int64_t E) {
+  return E <= 64    ? fn(&mmk::moe_route<1>)
+         : E <= 128 ? fn(&mmk::moe_route<2>)
+         : E <= 256 ? fn(&mmk::moe_route<4>)
+                    : fn(&mmk::moe_route<8>);
+}
+const void* moe_gate_up_kernel(int64_t T) {
+  return T <= 16 ? fn(&mmk::moe_gate_up<1>) : T <= 32 ? fn(&mmk::moe_gate_up<2>) : fn(&mmk::moe_gate_up<4>);
+}
+const void* moe_down_kernel(int64_t T) {
+  return T <= 16 ? fn(&mmk::moe_down<1>) : T <= 32 ? fn(&mmk::moe_down<2>) : fn(&mmk::moe_down<4>);
+}
+
 }  // namespace
 
 extern "C" {
@@ -605,6 +723,267 @@ mm_status mm_linear_q8(const void* x, const float* x_scale, const void* W, const
   const int64_t blocks = plan.tiles_m * plan.tiles_n * kQ8Kinds[plan.kind].fm * kQ8Kinds[plan.kind].fn;
   return launch(q8_join_kernel(plan.kind),
                 dim3((unsigned)blocks), 256, args, stream, "linear_q8 join");
+}
+
+mm_status mm_layer_norm(const void* x, int64_t ld_x, const void* residual, const void* weight, const void* bias, void* h,
+                        void* y, float* mean, float* rstd, int64_t rows, int64_t hidden, float eps,
+                        mm_out_dtype stream_dtype, void* stream) {
+  mm_status s = check_norm_sizes(rows, hidden, stream_dtype);
+  if (s != MM_OK) return s;
+  if (!(eps >= 0.0f)) return fail(MM_ERR_INVALID_VALUE, "eps must not be negative");
+  if (rows == 0 || hidden == 0) return MM_OK;
+  if (!x || !weight || !y || !mean || !rstd || (residual && !h)) return fail(MM_ERR_INVALID_VALUE, "null pointer");
+  if (ld_x < hidden || ld_x >= kLimit) return fail(MM_ERR_INVALID_VALUE, "rows of x must not overlap (ld_x < hidden)");
+  if (ld_x % 8 != 0) return fail(MM_ERR_MISALIGNED, "ld_x must be a multiple of 8 elements");
+  if (!residual) h = nullptr;
+  if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(h, 16) ||
+      !aligned(y, 16))
+    return fail(MM_ERR_MISALIGNED, "x, residual, weight, bias, h and y must be 16-byte aligned");
+  if (!aligned(mean, 4) || !aligned(rstd, 4)) return fail(MM_ERR_MISALIGNED, "mean and rstd must be 4-byte aligned");
+  const int64_t e = stream_dtype == MM_OUT_F32 ? 4 : 2;
+  const int64_t xb = ((rows - 1) * ld_x + hidden) * e, hb = rows * hidden * e;
+  // h may be residual itself, or x (a contiguous one): each element is read before it is
+  // written, by one thread
+  const bool over_residual = h && h == residual, over_x = h && h == x && ld_x == hidden;
+  const Span in[] = {{x, xb}, {residual, hb}, {weight, hidden * 2}, {bias, hidden * 2}};
+  const Span out[] = {{y, rows * hidden * 2}, {mean, rows * 4}, {rstd, rows * 4}};
+  const Span h_in[] = {{over_x ? nullptr : x, xb}, {over_residual ? nullptr : residual, hb}, {weight, hidden * 2},
+                       {bias, hidden * 2}, out[0], out[1], out[2]};
+  const Span h_out[] = {{h, hb}};
+  if (any_overlap(in, out) || any_overlap(h_in, h_out))
+    return fail(MM_ERR_INVALID_VALUE, "an output overlaps an input or another output");
+  mmk::LayerNormParams p;
+  p.weight = static_cast<const uint16_t*>(weight);
+  p.bias = static_cast<const uint16_t*>(bias);
+  p.ld_x = ld_x;
+  p.hidden = (int)hidden;
+  p.eps = eps;
+  int threads, vpt;
+  norm_shape(hidden, 512, &threads, &vpt);
+  const void* k = stream_dtype == MM_OUT_F32 ? layer_norm_kernel<true>(vpt) : layer_norm_kernel<false>(vpt);
+  void* args[] = {&p};
+  const int64_t most = kMaxThreads / threads;
+  for (int64_t r0 = 0; r0 < rows; r0 += most) {
+    p.x = static_cast<const char*>(x) + r0 * ld_x * e;
+    p.residual = residual ? static_cast<const char*>(residual) + r0 * hidden * e : nullptr;
+    p.h = residual ? static_cast<char*>(h) + r0 * hidden * e : nullptr;
+    p.y = static_cast<uint16_t*>(y) + r0 * hidden;
+    p.mean = mean + r0;
+    p.rstd = rstd + r0;
+    s = launch(k, dim3((unsigned)std::min(rows - r0, most)), threads, args, stream, "layer_norm");
+    if (s != MM_OK) return s;
+  }
+  return MM_OK;
+}
+
+mm_status mm_layer_norm_backward_workspace_size(int64_t rows, int64_t hidden, int64_t* bytes) {
+  if (!bytes) return fail(MM_ERR_INVALID_VALUE, "null bytes pointer");
+  *bytes = 0;
+  mm_status s = check_norm_sizes(rows, hidden, MM_OUT_BF16);
+  if (s != MM_OK || rows == 0 || hidden == 0 || layer_norm_few(rows, hidden)) return s;
+  int64_t parts = 0;
+  if ((s = norm_grad_parts(rows, hidden, &parts)) != MM_OK) return s;
+  *bytes = parts * hidden * 8;
+  return MM_OK;
+}
+
+mm_status mm_layer_norm_backward(const void* dy, const void* h, const void* weight, const float* mean, const float* rstd,
+                                 const void* dres, void* dh, float* dweight, float* dbias, int64_t rows, int64_t hidden,
+                                 mm_out_dtype stream_dtype, void* workspace, int64_t workspace_bytes, void* stream) {
+  mm_status s = check_norm_sizes(rows, hidden, stream_dtype);
+  if (s != MM_OK) return s;
+  if (hidden == 0) return MM_OK;
+  const bool few = layer_norm_few(rows, hidden);
+  if (!dweight || !dbias ||
+      (rows > 0 && (!dy || !h || !weight || !mean || !rstd || !dh || (!few && !workspace))))
+    return fail(MM_ERR_INVALID_VALUE, "null pointer");
+  if (!aligned(dweight, 16) || !aligned(dbias, 16) ||
+      (rows > 0 && (!aligned(dy, 16) || !aligned(h, 16) || !aligned(weight, 16) || !aligned(mean, 4) ||
+                    !aligned(rstd, 4) || !aligned(dres, 16) || !aligned(dh, 16) || !aligned(workspace, 16))))
+    return fail(MM_ERR_MISALIGNED, "pointers must be 16-byte aligned");
+  if (workspace_bytes < 0) return fail(MM_ERR_INVALID_VALUE, "negative workspace size");
+  const int64_t e = stream_dtype == MM_OUT_F32 ? 4 : 2, n = rows * hidden;
+  // (dh may be dres: read before written, by one thread)
+  const Span in[] = {{dy, n * 2}, {h, n * e}, {weight, hidden * 2}, {mean, rows * 4}, {rstd, rows * 4}};
+  const Span out[] = {{dh, n * e}, {dweight, hidden * 4}, {dbias, hidden * 4}, {workspace, workspace_bytes}};
+  const Span dres_in[] = {{dres, n * e}};
+  const Span dres_out[] = {{dh == dres ? nullptr : dh, n * e}, out[1], out[2], out[3]};
+  if (any_overlap(in, out) || any_overlap(dres_in, dres_out))
+    return fail(MM_ERR_INVALID_VALUE, "an output or the workspace overlaps an input or another output");
+  int64_t parts = 0;
+  if (rows > 0) {
+    if (!few && (s = norm_grad_parts(rows, hidden, &parts)) != MM_OK) return s;
+    if (workspace_bytes < parts * hidden * 8)
+      return fail(MM_ERR_INVALID_VALUE, "workspace smaller than mm_layer_norm_backward_workspace_size reports");
+    mmk::LayerNormGradParams p;
+    p.dy = static_cast<const uint16_t*>(dy);
+    p.h = h;
+    p.dres = dres;
+    p.weight = static_cast<const uint16_t*>(weight);
+    p.mean = mean;
+    p.rstd = rstd;
+    p.dh = dh;
+    p.part = static_cast<float*>(workspace);
+    p.rows = rows;
+    p.hidden = (int)hidden;
+    int threads, vpt;
+    norm_shape(hidden, 512, &threads, &vpt);
+    if (few) {
+      threads = std::max(threads, 512);  // (for the columns' sums)
+      int lanes = 8;
+      while (lanes > 1 && cdiv(hidden, 8 * lanes) < 128) lanes /= 2;
+      void* args[] = {&p, &dweight, &dbias, &lanes};
+      return launch(stream_dtype == MM_OUT_F32 ? layer_norm_grad_few_kernel<true>(vpt) : layer_norm_grad_few_kernel<false>(vpt),
+                    dim3((unsigned)(rows + cdiv(hidden, 8 * lanes))), threads, args, stream, "layer_norm gradient");
+    }
+    if (vpt == 4) norm_shape(hidden, 1024, &threads, &vpt);
+    void* args[] = {&p};
+    s = launch(stream_dtype == MM_OUT_F32 ? layer_norm_grad_kernel<true>(vpt, threads)
+                                          : layer_norm_grad_kernel<false>(vpt, threads),
+               dim3((unsigned)parts), threads, args, stream, "layer_norm gradient");
+    if (s != MM_OK) return s;
+  }
+  const float* part = static_cast<const float*>(workspace);
+  int nparts = (int)parts, hid = (int)hidden;
+  void* args[] = {&part, &dweight, &dbias, &nparts, &hid};
+  return launch(fn(&mmk::layer_norm_dparams), dim3((unsigned)cdiv(hidden, 32), 2), 256, args, stream,
+                "layer_norm parameter gradients");
+}
+
+mm_status mm_linear_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t adapters, int64_t* bytes) {
+  if (!bytes) return fail(MM_ERR_INVALID_VALUE, "null bytes pointer");
+  *bytes = 0;
+  mm_status s = check_lora(M, N, K, rank, adapters);
+  if (s != MM_OK || M == 0 || N == 0 || K == 0 || rank == 0 || adapters == 0) return s;
+  LoraPlan plan;
+  if ((s = lora_plan(M, N, K, rank, &plan)) != MM_OK) return s;
+  *bytes = plan.v + plan.acc + plan.split;
+  return MM_OK;
+}
+
+mm_status mm_linear_lora(const void* x, const void* W, const void* A, const void* B, const int32_t* index,
+                         const float* scale, const void* bias, void* out, int64_t M, int64_t N, int64_t K, int64_t rank,
+                         int64_t adapters, mm_epilogue epilogue, void* workspace, int64_t workspace_bytes, void* stream) {
+  int epi = 0;
+  mm_status s = check_product(M, N, K, bias, out, epilogue, &epi);
+  if (s != MM_OK) return s;
+  if ((s = check_lora(M, N, K, rank, adapters)) != MM_OK) return s;
+  if (M == 0 || N == 0) return MM_OK;
+  // (no terms of an adapter: the linear layer)
+  if (K == 0 || rank == 0 || adapters == 0) return mm_linear(x, W, bias, out, M, N, K, MM_NT, epilogue, stream);
+  if (!x || !W || !A || !B || !index || !scale) return fail(MM_ERR_INVALID_VALUE, "null operand pointer");
+  if (!aligned(x, 16) || !aligned(W, 16) || !aligned(A, 16) || !aligned(B, 16))
+    return fail(MM_ERR_MISALIGNED, "x, W, A and B must be 16-byte aligned");
+  if (!aligned(index, 4) || !aligned(scale, 4)) return fail(MM_ERR_MISALIGNED, "index and scale must be 4-byte aligned");
+  if (workspace_bytes < 0) return fail(MM_ERR_INVALID_VALUE, "negative workspace size");
+  const Span in[] = {{x, M * K * 2},        {W, N * K * 2},     {A, adapters * rank * K * 2}, {B, adapters * N * rank * 2},
+                     {index, M * 4},        {scale, adapters * 4}, {bias, bias ? N * 2 : 0}};
+  const Span outs[] = {{out, M * N * 2}, {workspace, workspace_bytes}};
+  if (any_overlap(in, outs)) return fail(MM_ERR_INVALID_VALUE, "out or the workspace overlaps an operand or each other");
+  LoraPlan plan;
+  if ((s = lora_plan(M, N, K, rank, &plan)) != MM_OK) return s;
+  if (!workspace || workspace_bytes < plan.v + plan.acc + plan.split)
+    return fail(MM_ERR_INVALID_VALUE, "workspace smaller than mm_linear_lora_workspace_size reports");
+  if (!aligned(workspace, 256)) return fail(MM_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+  mmk::LoraParams p;
+  p.x = static_cast<const uint16_t*>(x);
+  p.W = static_cast<const uint16_t*>(W);
+  p.A = static_cast<const uint16_t*>(A);
+  p.B = static_cast<const uint16_t*>(B);
+  p.index = index;
+  p.scale = scale;
+  p.bias = static_cast<const uint16_t*>(bias);
+  p.out = static_cast<uint16_t*>(out);
+  p.v = static_cast<float*>(workspace);
+  p.acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.v);
+  p.M = (int)M;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.R = (int)rank;
+  p.L = (int)adapters;
+  p.slices = (int)plan.slices;
+  p.kc = (int)plan.kc;
+  p.epi = epi;
+  void* args[] = {&p};
+  const int64_t blocks = cdiv(M, 16 * plan.mb);
+  if (blocks > kMaxGridY) return fail(MM_ERR_UNSUPPORTED, "M must be below 2^22");
+  const void* shrink = plan.mb == 1   ? fn(&mmk::lora_shrink<1>)
+                       : plan.mb == 2 ? fn(&mmk::lora_shrink<2>)
+                                      : fn(&mmk::lora_shrink<4>);
+  const int64_t turns = std::min<int64_t>(std::min<int64_t>(M, adapters), M <= 64 ? 16 : 2);
+  s = launch(shrink, dim3((unsigned)plan.slices, (unsigned)blocks, (unsigned)turns), mmk::kLoraWaves * 64, args, stream,
+             "linear_lora shrink");
+  if (s != MM_OK) return s;
+  if (M <= kLoraRows)
+    return launch(M <= 16 ? fn(&mmk::lora_rows<1>) : fn(&mmk::lora_rows<2>), dim3((unsigned)cdiv(N, 16)),
+                  mmk::kLoraWaves * 64, args, stream, "linear_lora rows");
+  void* split = plan.split ? static_cast<char*>(workspace) + plan.v + plan.acc : nullptr;
+  s = mm_matmul_ws(x, W, const_cast<float*>(p.acc), M, N, K, MM_NT, MM_OUT_F32, split, plan.split, stream);
+  if (s != MM_OK) return s;
+  return launch(fn(&mmk::lora_join), dim3((unsigned)cdiv(N, 256), (unsigned)cdiv(M, 64)), 256, args, stream,
+                "linear_lora join");
+}
+
+mm_status mm_moe_ffn_workspace_size(int64_t tokens, int64_t experts, int64_t H, int64_t I, int64_t top_k, int64_t* bytes) {
+  if (!bytes) return fail(MM_ERR_INVALID_VALUE, "null bytes pointer");
+  *bytes = 0;
+  const mm_status s = check_moe(tokens, experts, H, I, top_k);
+  if (s != MM_OK || tokens == 0) return s;
+  *bytes = kMoeTableBytes + round256(tokens * top_k * I * 4);
+  return MM_OK;
+}
+
+mm_status mm_moe_ffn(const void* x, const float* logits, const void* W_gate, const void* W_up, const void* W_down,
+                     void* out, int32_t* experts, float* weights, int64_t tokens, int64_t n_experts, int64_t H, int64_t I,
+                     int64_t top_k, int renormalize, void* workspace, int64_t workspace_bytes, void* stream) {
+  const int64_t T = tokens, E = n_experts;
+  mm_status s = check_moe(T, E, H, I, top_k);
+  if (s != MM_OK) return s;
+  if (T == 0) return MM_OK;
+  if ((H > 0 && !out) || (top_k > 0 && (!logits || !experts || !weights)) || (top_k > 0 && H > 0 && I > 0 &&
+      (!x || !W_gate || !W_up || !W_down)))
+    return fail(MM_ERR_INVALID_VALUE, "null pointer");
+  if (!aligned(x, 16) || !aligned(W_gate, 16) || !aligned(W_up, 16) || !aligned(W_down, 16))
+    return fail(MM_ERR_MISALIGNED, "x and the weights must be 16-byte aligned");
+  if (!aligned(logits, 4) || !aligned(experts, 4) || !aligned(weights, 4) || !aligned(out, 2))
+    return fail(MM_ERR_MISALIGNED, "logits, experts, weights and out must be aligned to their element size");
+  if (workspace_bytes < 0) return fail(MM_ERR_INVALID_VALUE, "negative workspace size");
+  const Span in[] = {{x, T * H * 2}, {logits, T * E * 4}, {W_gate, E * I * H * 2}, {W_up, E * I * H * 2},
+                     {W_down, E * I * H * 2}};
+  const Span outs[] = {{out, T * H * 2}, {experts, T * top_k * 4}, {weights, T * top_k * 4}, {workspace, workspace_bytes}};
+  if (any_overlap(in, outs)) return fail(MM_ERR_INVALID_VALUE, "an output or the workspace overlaps an input or another output");
+  if (!workspace || workspace_bytes < kMoeTableBytes + round256(T * top_k * I * 4))
+    return fail(MM_ERR_INVALID_VALUE, "workspace smaller than mm_moe_ffn_workspace_size reports");
+  if (!aligned(workspace, 256)) return fail(MM_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+  mmk::MoeParams p;
+  p.x = static_cast<const uint16_t*>(x);
+  p.logits = logits;
+  p.wg = static_cast<const uint16_t*>(W_gate);
+  p.wu = static_cast<const uint16_t*>(W_up);
+  p.wd = static_cast<const uint16_t*>(W_down);
+  p.out = static_cast<uint16_t*>(out);
+  p.experts = experts;
+  p.weights = weights;
+  p.tab = static_cast<mmk::MoeTables*>(workspace);
+  p.mid = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + kMoeTableBytes);
+  p.T = (int)T;
+  p.E = (int)E;
+  p.H = (int)H;
+  p.I = (int)I;
+  p.k = (int)top_k;
+  p.renormalize = renormalize != 0;
+  void* args[] = {&p};
+  if ((s = launch(moe_route_kernel(E), dim3(1), 1024, args, stream, "moe_ffn route")) != MM_OK) return s;
+  if (H == 0) return MM_OK;
+  int cus = 0;
+  if ((s = device_cus(&cus)) != MM_OK) return s;
+  const int64_t units = std::min(E, T * top_k) * (I / 8);
+  if (units > 0) {
+    s = launch(moe_gate_up_kernel(T), dim3((unsigned)std::min<int64_t>(units, 4 * (int64_t)cus)), mmk::kMoeWaves * 64, args,
+               stream, "moe_ffn gate and up");
+    if (s != MM_OK) return s;
+  }
+  return launch(moe_down_kernel(T), dim3((unsigned)cdiv(H, 16)), mmk::kMoeWaves * 64, args, stream, "moe_ffn down");
 }
 
 }  // extern "C"

@@ -313,6 +313,76 @@ mm_status mm_linear_q8(const void* x, const float* x_scale, const void* W, const
                        void* workspace, int64_t workspace_bytes, void* stream);
 mm_status mm_linear_q8_workspace_size(int64_t M, int64_t N, int64_t K, int64_t* bytes);
 
+/* Residual addition and layer norm of `rows` rows:
+ *   h = T(x + residual)                 (h = x without a residual)
+ *   mean = mean(h), rstd = 1 / sqrt(mean((h - mean)^2) + eps)   fp32, from h as stored
+ *   y = (h - mean) * rstd * weight + bias
+ *   bias      [hidden] bf16, or NULL (none)
+ *   mean, rstd  [rows] fp32 (the backward pass reads them)
+ * The other arguments, limits and what may share memory as for mm_rms_norm.  A
+ * row with a NaN or an infinity is NaN. */
+mm_status mm_layer_norm(const void* x, int64_t ld_x, const void* residual, const void* weight,
+                        const void* bias, void* h, void* y, float* mean, float* rstd, int64_t rows,
+                        int64_t hidden, float eps, mm_out_dtype stream_dtype, void* stream);
+
+/* Gradient of mm_layer_norm.  With n = (h - mean) rstd and g = dy weight:
+ *   dh = rstd (g - mean(g) - n mean(g n)) + dres    the gradient of x and of residual
+ *   dweight = sum over rows of dy n,  dbias = sum over rows of dy      fp32
+ * dy, h, dres, dh, the workspace and the order of the sums as for
+ * mm_rms_norm_backward; rows == 0 writes zeros to dweight and dbias. */
+mm_status mm_layer_norm_backward_workspace_size(int64_t rows, int64_t hidden, int64_t* bytes);
+mm_status mm_layer_norm_backward(const void* dy, const void* h, const void* weight, const float* mean,
+                                 const float* rstd, const void* dres, void* dh, float* dweight,
+                                 float* dbias, int64_t rows, int64_t hidden, mm_out_dtype stream_dtype,
+                                 void* workspace, int64_t workspace_bytes, void* stream);
+
+/* LinearOp form for the rows of many requests, each with a low-rank adapter of its
+ * own choice beside the shared weight:
+ *   out[m] = epi(W x[m] + bias + scale[a] B[a] (A[a] x[m])),  a = index[m]
+ *   x       [M][K] bf16;  W [N][K] bf16;  out [M][N] bf16 (RNE)
+ *   A       [adapters][rank][K] bf16;  B [adapters][N][rank] bf16
+ *   index   [M]: the row's adapter; a value that names none (below 0, or at least
+ *           `adapters`) leaves the row without one
+ *   scale   [adapters] fp32
+ *   rank    a multiple of 8, at most 256;  K a multiple of 8, at most 2^22;
+ *           N at most 2^27 - 16;  M below 2^22
+ * Sums are fp32; scale * (A x) enters the second product with 16 bits of
+ * significand.  rank == 0, adapters == 0 or K == 0 is mm_linear.
+ * The workspace (size from the function below, a device query; 256-byte aligned, any
+ * contents) is needed by every other call of M > 0 and N > 0; two calls in flight at
+ * once must not share it.  Other arguments, the epilogue and errors as for mm_linear. */
+mm_status mm_linear_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t adapters,
+                                        int64_t* bytes);
+mm_status mm_linear_lora(const void* x, const void* W, const void* A, const void* B, const int32_t* index,
+                         const float* scale, const void* bias, void* out, int64_t M, int64_t N, int64_t K,
+                         int64_t rank, int64_t adapters, mm_epilogue epi, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+
+/* Mixture-of-experts form of mm_ffn_swiglu for a few tokens (a decode step):
+ *   out[t] = sum over j of weights[t][j] W_down[e] (SiLU(W_gate[e] x[t]) * (W_up[e] x[t])),
+ * with e = experts[t][j], j < top_k: the experts of the largest logits of token t
+ * in descending order (of equal ones the lower index first), and their weights, the
+ * softmax over these logits (renormalize != 0) or over all of the token's.
+ *   x        [tokens][H] bf16;  logits [tokens][n_experts] fp32
+ *   W_gate, W_up  [n_experts][I][H] bf16;  W_down [n_experts][H][I] bf16
+ *   out      [tokens][H] bf16 (RNE);  experts, weights [tokens][top_k]: written
+ * A logit of minus infinity takes no part: where fewer than top_k others are there,
+ * the last slots hold expert -1 and weight 0, and a token without any has an output of
+ * zeros.  A logit of NaN counts as the largest; it, or one of plus infinity, makes the
+ * token's weights and output NaN.
+ * tokens <= 64, n_experts <= 512, top_k <= 16 and <= n_experts; H and I multiples of 8, at
+ * most 2^18.  Sums are fp32; the products between the two layers are kept with 16 bits of
+ * significand.  Three kernels.  tokens == 0 is a no-op.
+ * The workspace (size from the function below, host arithmetic only; 256-byte
+ * aligned, any contents) is needed by every other call; two calls in flight at once
+ * must not share it. */
+mm_status mm_moe_ffn_workspace_size(int64_t tokens, int64_t n_experts, int64_t H, int64_t I, int64_t top_k,
+                                    int64_t* bytes);
+mm_status mm_moe_ffn(const void* x, const float* logits, const void* W_gate, const void* W_up,
+                     const void* W_down, void* out, int32_t* experts, float* weights, int64_t tokens,
+                     int64_t n_experts, int64_t H, int64_t I, int64_t top_k, int renormalize,
+                     void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Tile configuration override, parsed from a string such as
  *   "BM=256,BN=256,WM=2,WN=2,G=8,XCD=1,KALT=1,GRID=0"
  * (BM/BN: output tile; WM/WN: wave grid; G: grouped-swizzle band height in
