@@ -4,11 +4,11 @@
 // (rows whose index names no adapter: without the last term).  x [M][K], W [N][K],
 // A [L][R][K], B [L][N][R] bf16, fp32 scales, bf16 output, one rounding.
 //
-// lora_shrink leaves v[m] = A_a x[m] in fp32.  Few rows (a decode step): bound by reading
-// W once; lora_rows streams it and adds B (s v) as further steps of the same sums.  Many
-// rows: the library's tile kernels leave W x in fp32, and lora_join adds the rest.
-// s v enters the matrix products as two bf16 numbers, high and low part, 16 bits
-// of significand: one would round the adapter's term more than the output is.
+// lora_shrink leaves A_a x[m] in fp32, in slices of K.  Few rows (a decode step): bound by
+// reading W once; lora_rows streams it and adds B (s_a A_a x[m]) to the same sums.
+// Many rows: the library's tile kernels leave W x in fp32, and lora_join adds the rest.
+// v = s_a A_a x enters the products with B as two bf16 numbers, high and low part, 16
+// bits of significand: as one, its rounding would be as large as the output's own.
 #pragma once
 
 #include "moe_ffn.hpp"
@@ -16,7 +16,7 @@
 
 namespace mmk {
 
-constexpr int kLoraWaves = 8;
+constexpr int kLoraWaves = 16, kLoraShrinkWaves = 8;
 constexpr int kLoraMaxRank = 256;
 
 struct LoraParams {
@@ -28,10 +28,12 @@ struct LoraParams {
   const float* scale;     // [L]
   const uint16_t* bias;   // [N] or null
   uint16_t* out;          // [M][N]
-  float* v;               // [slices][M][R]
-  const float* acc;       // [M][N]: W x (lora_join)
+  float* low;             // [low_slices][M][R]: parts of A x
+  uint16_t* v;            // [M][2][R]: s A x, high and low parts
+  float* acc;             // [slices][M][N]: parts of W x
   int M, N, K, R, L;
-  int slices, kc;         // K in slices of kc (a multiple of 64)
+  int low_slices, low_k;  // slices of K of low_k (a multiple of 64)
+  int slices;             // of acc
   int epi;
 };
 
@@ -55,258 +57,322 @@ __device__ __forceinline__ void each_adapter(int mine, F f) {
   }
 }
 
-// v of the rows 16 MB y .. + 16 MB - 1 over slice x of K; of the adapters among them,
-// every gridDim.z-th.  The waves share the adapter's blocks of 16 ranks and, where those
-// are fewer than the waves, the slice's steps of 64 k, and meet in LDS.
+// `rows` rows of an operand [rows][K] of bf16 from `base` as a buffer: zeros past the end.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const uint16_t* base, int rows, int K) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), (short)0, rows * K * 2, 0x00020000);
+}
+
+// The same rows from value `from` of the first on: the last ends where the operand's does.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t slice_buffer(const uint16_t* base, int rows, int K, int from) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), (short)0, (rows * K - from) * 2, 0x00020000);
+}
+
+// A lane's piece j (0, 1) of step st of 64 k from a row at byte `row` of a buffer: chunk
+// lane / 16 of 8 values.  Zeros past K; past the last step too (its base, a
+// scalar, has to stay inside the buffer).
+__device__ __forceinline__ u32x4 step_chunk(__amdgpu_buffer_rsrc_t buf, uint32_t row, int st, int j, int K, int steps,
+                                            int lg) {
+  const uint32_t off = 64 * st + 32 * j + 8 * lg < K ? row + 64u * j + 16u * (uint32_t)lg : 0x80000000u;
+  return load_chunk(buf, off, 128u * (uint32_t)min(st, steps - 1));
+}
+
+// A x of the rows 16 MB y .. + 16 MB - 1 over slice x of K, for ranks 16 z .. + 15 (z the
+// first part of blockIdx.z); of the adapters among the rows, every turns-th.  The waves
+// take every eighth step of 64 k, each step's loads one step ahead, and meet in LDS, added in
+// wave order.  A CU by itself reads some 25 bytes per ns, so the slices, adapters
+// and ranks of few rows go to many (one token, rank 16, K 8192: 4.5 us in 16 slices, 12
+// in one).
 template <int MB>
-__global__ void __launch_bounds__(kLoraWaves * 64) lora_shrink(LoraParams p) {
-  __shared__ f32x4 red[kLoraWaves][MB][64];
+__global__ void __launch_bounds__(kLoraShrinkWaves * 64) lora_shrink(LoraParams p, int turns) {
+  __shared__ f32x4 red[kLoraShrinkWaves][MB][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lx = lane & 15, lg = lane >> 4;
   const int m0 = blockIdx.y * (16 * MB), rows = min(16 * MB, p.M - m0);
-  const int K = p.K;
-  const int kbeg = blockIdx.x * p.kc, kend = min(K, kbeg + p.kc), steps = (kend - kbeg + 63) >> 6;
-  const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint16_t*>(p.x) + (int64_t)m0 * K, (short)0, rows * K * 2, 0x00020000);
-  bool out[2];
-  uint32_t tail[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    out[j] = kbeg + 64 * (steps - 1) + 32 * j + 8 * lg >= kend;
-    tail[j] = out[j] ? 0x80000000u : 0u;
-  }
-  const int blocks = (p.R + 15) >> 4;
-  int wide = 1;  // blocks of ranks at work together
-  while (wide < blocks && wide < kLoraWaves) wide *= 2;
-  const int parts = kLoraWaves / wide, part = wave / wide;
+  const int r0 = (int)(blockIdx.z / turns) * 16, my_turn = blockIdx.z % turns;
+  const int K = p.K, kbeg = blockIdx.x * p.low_k, klen = min(p.low_k, K - kbeg), steps = (klen + 63) >> 6;
+  // (of a slice of a row the buffer ends where the last row's does)
+  const __amdgpu_buffer_rsrc_t rx = slice_buffer(p.x + (int64_t)m0 * K + kbeg, rows, K, kbeg);
   struct Step {
     u32x4 w[2], x[MB][2];
   };
   int turn = 0;
   each_adapter(lane < rows ? lora_adapter(p, m0 + lane) : -1, [&](int a, uint64_t same) {
-    if (turn++ % (int)gridDim.z != (int)blockIdx.z) return;
-    uint32_t xo[MB];
+    if (turn++ % turns != my_turn) return;
+    const __amdgpu_buffer_rsrc_t rw = slice_buffer(p.A + ((int64_t)a * p.R + r0) * K + kbeg, min(16, p.R - r0), K, kbeg);
+    const uint32_t row = (uint32_t)lx * (uint32_t)K * 2u;
+    uint32_t xrow[MB];  // (rows of other adapters are not loaded)
 #pragma unroll
     for (int b = 0; b < MB; ++b)
-      xo[b] = (same >> (16 * b + lx)) & 1 ? (uint32_t)(16 * b + lx) * (uint32_t)K * 2u + 16u * (uint32_t)lg : 0x80000000u;
-    for (int c = 0; c < blocks; c += wide) {
-      const int block = c + wave % wide;
-      f32x4 acc[MB];
+      xrow[b] = (same >> (16 * b + lx)) & 1 ? (uint32_t)(16 * b + lx) * (uint32_t)K * 2u : 0x80000000u;
+    auto load = [&](int st, Step& t) __attribute__((always_inline)) {
 #pragma unroll
-      for (int b = 0; b < MB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (block < blocks) {
-        const uint16_t* w = p.A + ((int64_t)a * p.R + min(16 * block + lx, p.R - 1)) * K + kbeg + 8 * lg;
-        auto load = [&](int st, Step& t) __attribute__((always_inline)) {
-          const bool last = st == steps - 1;
+      for (int j = 0; j < 2; ++j) {
+        t.w[j] = step_chunk(rw, row, st, j, klen, steps, lg);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            t.w[j] = *reinterpret_cast<const u32x4*>(w + (last && out[j] ? -8 * lg : 64 * st + 32 * j));
-#pragma unroll
-            for (int b = 0; b < MB; ++b)
-              if ((same >> (16 * b)) & 0xffff)
-                t.x[b][j] = load_chunk(rx, (xo[b] + 64u * j) | (last ? tail[j] : 0u), 2u * (uint32_t)kbeg + 128u * (uint32_t)st);
-          }
-        };
-        auto step = [&](int st, Step& t, Step& next) __attribute__((always_inline)) {
-          load(min(st + parts, steps - 1), next);
-          const bool last = st == steps - 1;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (last && out[j]) t.w[j] = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-            for (int b = 0; b < MB; ++b)
-              if ((same >> (16 * b)) & 0xffff) acc[b] = mfma_bf16(t.x[b][j], t.w[j], acc[b]);
-          }
-        };
-        if (part < steps) {
-          Step s0, s1;
-          load(part, s0);
-          for (int st = part; st < steps; st += 2 * parts) {
-            step(st, s0, s1);
-            if (st + parts < steps) step(st + parts, s1, s0);
-          }
-        }
+        for (int b = 0; b < MB; ++b) t.x[b][j] = step_chunk(rx, xrow[b], st, j, klen, steps, lg);
       }
-      __syncthreads();  // (what was there before has been read)
+    };
+    f32x4 acc[MB];
 #pragma unroll
-      for (int b = 0; b < MB; ++b) red[wave][b][lane] = acc[b];
-      __syncthreads();
-      for (int i = threadIdx.x; i < wide * MB * 64; i += kLoraWaves * 64) {
-        const int l = i & 63, b = (i >> 6) % MB, g = (i >> 6) / MB;
-        const int r = 16 * (c + g) + (l & 15);
-        if (r >= p.R) continue;
-        f32x4 s = red[g][b][l];
-        for (int q = 1; q < parts; ++q) {
-          const f32x4 u = red[q * wide + g][b][l];
+    for (int b = 0; b < MB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto step = [&](int st, Step& t, Step& next) __attribute__((always_inline)) {
+      load(st + kLoraShrinkWaves, next);
 #pragma unroll
-          for (int f = 0; f < 4; ++f) s[f] += u[f];
-        }
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          const int m = 16 * b + 4 * (l >> 4) + f;
-          if ((same >> m) & 1) p.v[((int64_t)blockIdx.x * p.M + m0 + m) * p.R + r] = s[f];
-        }
+        for (int b = 0; b < MB; ++b) acc[b] = mfma_bf16(t.x[b][j], t.w[j], acc[b]);
+    };
+    Step s0, s1;
+    load(wave, s0);
+    for (int st = wave; st < steps; st += 2 * kLoraShrinkWaves) {
+      step(st, s0, s1);
+      step(st + kLoraShrinkWaves, s1, s0);
+    }
+    __syncthreads();  // (what was there before has been read)
+#pragma unroll
+    for (int b = 0; b < MB; ++b) red[wave][b][lane] = acc[b];
+    __syncthreads();
+    if (wave < MB) {
+      f32x4 s = red[0][wave][lane];
+#pragma unroll
+      for (int q = 1; q < kLoraShrinkWaves; ++q) {
+        const f32x4 u = red[q][wave][lane];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) s[f] += u[f];
+      }
+      const int r = r0 + lx;
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const int m = 16 * wave + 4 * lg + f;
+        if (r < p.R && ((same >> m) & 1)) p.low[((int64_t)blockIdx.x * p.M + m0 + m) * p.R + r] = s[f];
       }
     }
   });
 }
 
-// s v of row m, ranks r .. r + 7, summed over the slices in order, as two bf16 fragments.
-__device__ __forceinline__ void lora_low(const LoraParams& p, int m, int r, float scale, u32x4* hi, u32x4* lo) {
-  float v[8];
+// v of row m (adapter a), ranks r .. r + 7: the slices added in order, the scale, two parts.
+__device__ __forceinline__ void lora_v(const LoraParams& p, int m, int a, int r, u32x4* hi, u32x4* lo) {
+  f32x4 v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  const float* at = p.low + (int64_t)m * p.R + r;
+#pragma unroll 4
+  for (int s = 0; s < p.low_slices; ++s, at += (int64_t)p.M * p.R) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = 0.f;
-  const float* at = p.v + (int64_t)m * p.R + r;
-  for (int s = 0; s < p.slices; ++s, at += (int64_t)p.M * p.R) {
-    const f32x4 a = *reinterpret_cast<const f32x4*>(at), b = *reinterpret_cast<const f32x4*>(at + 4);
+    for (int h = 0; h < 2; ++h) {
+      const f32x4 u = *reinterpret_cast<const f32x4*>(at + 4 * h);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] += a[j];
-      v[4 + j] += b[j];
+      for (int f = 0; f < 4; ++f) v[h][f] += u[f];
     }
   }
+  const float scale = p.scale[a];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint16_t h[2], l[2];
-    split_bf16(v[2 * j] * scale, &h[0], &l[0]);
-    split_bf16(v[2 * j + 1] * scale, &h[1], &l[1]);
+    split_bf16(v[j >> 1][2 * (j & 1)] * scale, &h[0], &l[0]);
+    split_bf16(v[j >> 1][2 * (j & 1) + 1] * scale, &h[1], &l[1]);
     (*hi)[j] = (uint32_t)h[0] | (uint32_t)h[1] << 16;
     (*lo)[j] = (uint32_t)l[0] | (uint32_t)l[1] << 16;
   }
 }
 
-// Up to 16 MB rows, 16 columns per workgroup.  The waves take every eighth step of 64 k,
-// each step's loads one step ahead, then every eighth adapter, and meet in LDS,
-// added in wave order.
-template <int MB>
+// v of every row, 8 ranks per thread; rows without an adapter are left out.
+__device__ __forceinline__ void lora_fold_all(const LoraParams& p, int64_t thread, int64_t threads) {
+  const int chunks = p.R >> 3;
+  for (int64_t i = thread; i < (int64_t)p.M * chunks; i += threads) {
+    const int m = (int)(i / chunks), r = 8 * (int)(i - (int64_t)m * chunks);
+    const int a = lora_adapter(p, m);
+    if (a < 0) continue;
+    u32x4 hi, lo;
+    lora_v(p, m, a, r, &hi, &lo);
+    uint16_t* v = p.v + (int64_t)m * 2 * p.R + r;
+    *reinterpret_cast<u32x4*>(v) = hi;
+    *reinterpret_cast<u32x4*>(v + p.R) = lo;
+  }
+}
+__global__ void __launch_bounds__(256) lora_fold(LoraParams p) {
+  lora_fold_all(p, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
+}
+
+// Up to 16 MB rows.  A workgroup takes a slice y of K, 16 SPW steps of 64 k, and every
+// gridDim.x-th block of 16 columns.  Wave w has the slice's steps 16 i + w, i < SPW, and
+// holds x there in registers for all blocks, so that W is all that it loads; each
+// step's loads are issued one step ahead, across blocks.  The waves' sums of a block meet
+// in LDS (two sets in turn: one barrier per block) and are added in wave order, by
+// another wave for each block.
+// FINISH (K in one slice): v comes into LDS first, the adapters' terms join the sums
+// here, each adapter on a wave, and the output is written.  Else lora_join does both,
+// and v is left in memory for it.
+template <int MB, int SPW, bool FINISH>
 __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
-  __shared__ f32x4 red[kLoraWaves][MB][64];
+  static_assert(SPW % 2 == 0 && MB * SPW <= 8, "x in 64 registers, two steps in turn");
+  __shared__ f32x4 red[2][kLoraWaves][MB][64];
+  __shared__ u32x4 v[FINISH ? 16 * MB : 1][2][kLoraMaxRank / 8];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lx = lane & 15, lg = lane >> 4;
-  const int n0 = blockIdx.x * 16, K = p.K, steps = (K + 63) >> 6;
-  const int64_t row = min(n0 + lx, p.N - 1);
-  const uint16_t* w = p.W + row * K + 8 * lg;
-  const __amdgpu_buffer_rsrc_t rx =
-      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p.x), (short)0, p.M * K * 2, 0x00020000);
-  bool out[2];
-  uint32_t tail[2], xo[MB];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    out[j] = 64 * (steps - 1) + 32 * j + 8 * lg >= K;
-    tail[j] = out[j] ? 0x80000000u : 0u;
-  }
-#pragma unroll
-  for (int b = 0; b < MB; ++b) xo[b] = (uint32_t)(16 * b + lx) * (uint32_t)K * 2u + 16u * (uint32_t)lg;
+  const int K = p.K, steps = (K + 63) >> 6, blocks = (p.N + 15) >> 4;
+  const int first = blockIdx.y * (kLoraWaves * SPW) + wave;
+
   struct Step {
-    u32x4 w[2], x[MB][2];
+    u32x4 w[2];
   };
-  auto load = [&](int st, Step& t) __attribute__((always_inline)) {
-    const bool last = st == steps - 1;
+  uint32_t row = (uint32_t)lx * (uint32_t)K * 2u;
+  auto load = [&](int block, int i, Step& t) __attribute__((always_inline)) {
+    // (opaque: the steps' offsets are not all kept in registers)
+    asm volatile("" : "+v"(row));
+    // (past the last block, that one again, unused)
+    const int n0 = 16 * min(block, blocks - 1);
+    const __amdgpu_buffer_rsrc_t rw = rows_buffer(p.W + (int64_t)n0 * K, min(16, p.N - n0), K);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      t.w[j] = *reinterpret_cast<const u32x4*>(w + (last && out[j] ? -8 * lg : 64 * st + 32 * j));
-#pragma unroll
-      for (int b = 0; b < MB; ++b) t.x[b][j] = load_chunk(rx, (xo[b] + 64u * j) | (last ? tail[j] : 0u), 128u * (uint32_t)st);
-    }
+    for (int j = 0; j < 2; ++j) t.w[j] = step_chunk(rw, row, first + kLoraWaves * i, j, K, steps, lg);
   };
-  f32x4 acc[MB];
+  Step t[2];
+  load(blockIdx.x, 0, t[0]);
+  u32x4 x[MB][SPW][2];
+  {
+    const __amdgpu_buffer_rsrc_t rx = rows_buffer(p.x, p.M, K);
 #pragma unroll
-  for (int b = 0; b < MB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto step = [&](int st, Step& t, Step& next) __attribute__((always_inline)) {
-    load(min(st + kLoraWaves, steps - 1), next);
-    const bool last = st == steps - 1;
+    for (int i = 0; i < SPW; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if (last && out[j]) t.w[j] = u32x4{0u, 0u, 0u, 0u};
+      for (int b = 0; b < MB; ++b)
 #pragma unroll
-      for (int b = 0; b < MB; ++b) acc[b] = mfma_bf16(t.x[b][j], t.w[j], acc[b]);
-    }
-  };
-  if (wave < steps) {
-    Step s0, s1;
-    load(wave, s0);
-    for (int st = wave; st < steps; st += 2 * kLoraWaves) {
-      step(st, s0, s1);
-      if (st + kLoraWaves < steps) step(st + kLoraWaves, s1, s0);
-    }
+        for (int j = 0; j < 2; ++j)
+          x[b][i][j] = step_chunk(rx, (uint32_t)(16 * b + lx) * (uint32_t)K * 2u, first + kLoraWaves * i, j, K, steps, lg);
   }
-  int turn = 0;
-  each_adapter(lora_adapter(p, lane), [&](int a, uint64_t same) {
-    if (turn++ % kLoraWaves != wave) return;
-    const float scale = p.scale[a];
-    const uint16_t* bw = p.B + ((int64_t)a * p.N + row) * p.R;
-    for (int r0 = 0; r0 < p.R; r0 += 32) {
-      const int r = r0 + 8 * lg;
-      u32x4 wf = {0u, 0u, 0u, 0u};
-      if (r < p.R) wf = *reinterpret_cast<const u32x4*>(bw + r);
+  // this wave's adapters (of at most 16 MB) and their rows
+  int mine[MB];
+  uint64_t same[MB];
 #pragma unroll
-      for (int b = 0; b < MB; ++b) {
-        if (!((same >> (16 * b)) & 0xffff)) continue;
-        u32x4 hi = {0u, 0u, 0u, 0u}, lo = {0u, 0u, 0u, 0u};
-        if (r < p.R && ((same >> (16 * b + lx)) & 1)) lora_low(p, 16 * b + lx, r, scale, &hi, &lo);
-        // (rows without this adapter get zeros, unless it holds what is not finite:
-        // only their own rows' sums are taken)
-        f32x4 d = mfma_bf16(hi, wf, f32x4{0.f, 0.f, 0.f, 0.f});
-        d = mfma_bf16(lo, wf, d);
+  for (int q = 0; q < MB; ++q) {
+    mine[q] = -1;
+    same[q] = 0;
+  }
+  if constexpr (FINISH) {
+    int turn = 0;
+    each_adapter(lora_adapter(p, lane), [&](int a, uint64_t s) {
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
-          if ((same >> (16 * b + 4 * lg + f)) & 1) acc[b][f] += d[f];
+      for (int q = 0; q < MB; ++q) {
+        if (turn == kLoraWaves * q + wave) {
+          mine[q] = a;
+          same[q] = s;
+        }
+      }
+      ++turn;
+    });
+    const int chunks = p.R >> 3;
+    for (int i = threadIdx.x; i < p.M * chunks; i += kLoraWaves * 64) {
+      const int m = i / chunks, c = i - m * chunks, a = lora_adapter(p, m);
+      if (a >= 0) lora_v(p, m, a, 8 * c, &v[m][0][c], &v[m][1][c]);
+    }
+    __syncthreads();
+  } else {
+    lora_fold_all(p, (int64_t)(blockIdx.y * gridDim.x + blockIdx.x) * (kLoraWaves * 64) + threadIdx.x,
+                  (int64_t)gridDim.x * gridDim.y * (kLoraWaves * 64));
+  }
+
+  int round = 0;
+  for (int block = blockIdx.x; block < blocks; block += gridDim.x, ++round) {
+    const int n0 = 16 * block;
+    f32x4 acc[MB];
+#pragma unroll
+    for (int b = 0; b < MB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < SPW; ++i) {
+      if (i + 1 < SPW)
+        load(block, i + 1, t[(i + 1) & 1]);
+      else
+        load(block + gridDim.x, 0, t[0]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int b = 0; b < MB; ++b) acc[b] = mfma_bf16(x[b][i][j], t[i & 1].w[j], acc[b]);
+    }
+#pragma unroll
+    for (int q = 0; q < MB; ++q) {
+      if (!FINISH || mine[q] < 0) continue;
+      const uint16_t* bw = p.B + ((int64_t)mine[q] * p.N + min(n0 + lx, p.N - 1)) * p.R;
+      for (int r0 = 0; r0 < p.R; r0 += 32) {
+        const int r = r0 + 8 * lg;
+        u32x4 wf = {0u, 0u, 0u, 0u};
+        if (r < p.R) wf = *reinterpret_cast<const u32x4*>(bw + r);
+#pragma unroll
+        for (int b = 0; b < MB; ++b) {
+          if (!((same[q] >> (16 * b)) & 0xffff)) continue;
+          u32x4 hi = {0u, 0u, 0u, 0u}, lo = {0u, 0u, 0u, 0u};
+          if (r < p.R && ((same[q] >> (16 * b + lx)) & 1)) {
+            hi = v[16 * b + lx][0][r >> 3];
+            lo = v[16 * b + lx][1][r >> 3];
+          }
+          f32x4 d = mfma_bf16(hi, wf, f32x4{0.f, 0.f, 0.f, 0.f});
+          d = mfma_bf16(lo, wf, d);
+          // (0 times what is not finite: other rows' sums are left alone)
+#pragma unroll
+          for (int f = 0; f < 4; ++f)
+            if ((same[q] >> (16 * b + 4 * lg + f)) & 1) acc[b][f] += d[f];
+        }
       }
     }
-  });
+    f32x4(*set)[MB][64] = red[round & 1];
 #pragma unroll
-  for (int b = 0; b < MB; ++b) red[wave][b][lane] = acc[b];
-  __syncthreads();
-  for (int i = threadIdx.x; i < MB * 64; i += kLoraWaves * 64) {
-    const int l = i & 63, b = i >> 6, n = n0 + (l & 15);
-    if (n >= p.N) continue;
-    f32x4 s = red[0][b][l];
-#pragma unroll
+    for (int b = 0; b < MB; ++b) set[wave][b][lane] = acc[b];
+    __syncthreads();
+    const int b = (wave - round * MB) & (kLoraWaves - 1);
+    if (b >= MB) continue;
+    f32x4 s = set[0][b][lane];
+#pragma unroll 5
     for (int q = 1; q < kLoraWaves; ++q) {
-      const f32x4 u = red[q][b][l];
+      const f32x4 u = set[q][b][lane];
 #pragma unroll
       for (int f = 0; f < 4; ++f) s[f] += u[f];
     }
+    const int n = n0 + lx;
+    if (n >= p.N) continue;
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
-      const int m = 16 * b + 4 * (l >> 4) + f;
-      if (m < p.M) p.out[(int64_t)m * p.N + n] = decoder_epilogue(s[f], p.bias, p.epi, n);
+      const int m = 16 * b + 4 * lg + f;
+      if (m >= p.M) continue;
+      if constexpr (FINISH)
+        p.out[(int64_t)m * p.N + n] = decoder_epilogue(s[f], p.bias, p.epi, n);
+      else
+        p.acc[((int64_t)blockIdx.y * p.M + m) * p.N + n] = s[f];
     }
   }
 }
 
-// Many rows: out = epi(acc + bias + B (s v)) for 64 rows by 256 columns per workgroup,
-// 64 columns per wave.  B is the MFMA's first operand, so a lane's sums are of one row;
+// out = epi(sum of acc's slices + bias + B v): 64 rows by 64 columns per workgroup, 16
+// rows per wave.  B is the MFMA's first operand, so a lane's sums are of one row;
 // the block pair's rows of B are taken in the order that makes them 8 consecutive columns.
 __global__ void __launch_bounds__(256) lora_join(LoraParams p) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lx = lane & 15, lg = lane >> 4;
-  const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 256 + wave * 64;
-  if (n0 >= p.N) return;
-  f32x4 acc[4][2][2];
+  const int m0 = blockIdx.y * 64 + 16 * wave, n0 = blockIdx.x * 64;
+  if (m0 >= p.M) return;
+  const int m = m0 + lx;
+  f32x4 acc[2][2];
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int m = m0 + 16 * b + lx, n = n0 + 32 * c + 8 * lg;
-      const float* at = p.acc + (int64_t)min(m, p.M - 1) * p.N;
+  for (int c = 0; c < 2; ++c) {
+    const int n = n0 + 32 * c + 8 * lg;
+    const float* at = p.acc + (int64_t)min(m, p.M - 1) * p.N;
+    acc[c][0] = acc[c][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < p.slices; ++s, at += (int64_t)p.M * p.N) {
+      f32x4 u[2];
       if (n + 8 <= p.N) {
-        __builtin_memcpy(&acc[b][c][0], at + n, 16);
-        __builtin_memcpy(&acc[b][c][1], at + n + 4, 16);
+        __builtin_memcpy(&u[0], at + n, 16);
+        __builtin_memcpy(&u[1], at + n + 4, 16);
       } else {
 #pragma unroll
-        for (int f = 0; f < 8; ++f) acc[b][c][f >> 2][f & 3] = at[min(n + f, p.N - 1)];
+        for (int f = 0; f < 8; ++f) u[f >> 2][f & 3] = at[min(n + f, p.N - 1)];
       }
+#pragma unroll
+      for (int f = 0; f < 8; ++f) acc[c][f >> 2][f & 3] += u[f >> 2][f & 3];
     }
   }
-  each_adapter(lora_adapter(p, m0 + lane), [&](int a, uint64_t same) {
-    const float scale = p.scale[a];
+  each_adapter(lane < 16 ? lora_adapter(p, m0 + lane) : -1, [&](int a, uint64_t same) {
+    const bool mine = (same >> lx) & 1;
     for (int r0 = 0; r0 < p.R; r0 += 32) {
       const int r = r0 + 8 * lg;
-      u32x4 wf[2][2];
+      u32x4 wf[2][2], hi = {0u, 0u, 0u, 0u}, lo = {0u, 0u, 0u, 0u};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -316,50 +382,42 @@ __global__ void __launch_bounds__(256) lora_join(LoraParams p) {
           if (r < p.R) wf[c][h] = *reinterpret_cast<const u32x4*>(p.B + ((int64_t)a * p.N + n) * p.R + r);
         }
       }
+      if (r < p.R && mine) {
+        const uint16_t* v = p.v + (int64_t)m * 2 * p.R + r;
+        hi = *reinterpret_cast<const u32x4*>(v);
+        lo = *reinterpret_cast<const u32x4*>(v + p.R);
+      }
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        if (!((same >> (16 * b)) & 0xffff)) continue;
-        const bool mine = (same >> (16 * b + lx)) & 1;
-        u32x4 hi = {0u, 0u, 0u, 0u}, lo = {0u, 0u, 0u, 0u};
-        if (r < p.R && mine) lora_low(p, m0 + 16 * b + lx, r, scale, &hi, &lo);
+      for (int c = 0; c < 2; ++c) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int h = 0; h < 2; ++h) {
+          f32x4 d = mfma_bf16(wf[c][h], hi, f32x4{0.f, 0.f, 0.f, 0.f});
+          d = mfma_bf16(wf[c][h], lo, d);
+          // (0 times what is not finite: other rows' sums are left alone)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            f32x4 d = mfma_bf16(wf[c][h], hi, f32x4{0.f, 0.f, 0.f, 0.f});
-            d = mfma_bf16(wf[c][h], lo, d);
-#pragma unroll
-            for (int f = 0; f < 4; ++f) acc[b][c][h][f] += mine ? d[f] : 0.f;
-          }
+          for (int f = 0; f < 4; ++f) acc[c][h][f] += mine ? d[f] : 0.f;
         }
       }
     }
   });
+  if (m >= p.M) return;
   const bool has_bias = p.epi == EPI_BIAS || p.epi == EPI_BIAS_GELU;
   const bool gelu = p.epi == EPI_GELU || p.epi == EPI_BIAS_GELU;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const int n = n0 + 32 * c + 8 * lg;
-    float bias[8];
+    float v[8];
 #pragma unroll
-    for (int f = 0; f < 8; ++f) bias[f] = has_bias ? bf16_float(p.bias[min(n + f, p.N - 1)]) : 0.f;
+    for (int f = 0; f < 8; ++f) v[f] = acc[c][f >> 2][f & 3] + (has_bias ? bf16_float(p.bias[min(n + f, p.N - 1)]) : 0.f);
+    if (gelu) gelu_tanh_all(v);
+    uint16_t* o = p.out + (int64_t)m * p.N + n;
+    if (n + 8 <= p.N) {
+      const u32x4 pk = pack8(v);
+      __builtin_memcpy(o, &pk, 16);
+    } else {
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int m = m0 + 16 * b + lx;
-      if (m >= p.M) continue;
-      float v[8];
-#pragma unroll
-      for (int f = 0; f < 8; ++f) v[f] = acc[b][c][f >> 2][f & 3] + bias[f];
-      if (gelu) gelu_tanh_all(v);
-      uint16_t* o = p.out + (int64_t)m * p.N + n;
-      if (n + 8 <= p.N) {
-        const u32x4 pk = pack8(v);
-        __builtin_memcpy(o, &pk, 16);
-      } else {
-#pragma unroll
-        for (int f = 0; f < 8; ++f)
-          if (n + f < p.N) o[f] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[f]));
-      }
+      for (int f = 0; f < 8; ++f)
+        if (n + f < p.N) o[f] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[f]));
     }
   }
 }

@@ -378,29 +378,55 @@ bool layer_norm_few(int64_t rows, int64_t hidden) { return rows <= kFewRows || h
 // ----------------------------------------------------------------------------
 // Linear layer with an adapter per row
 // ----------------------------------------------------------------------------
-constexpr int64_t kLoraRows = 32;
-
-struct LoraPlan {
-  int64_t slices = 1, kc = 0;  // of K, for the adapters' first product
-  int mb = 1;                  // blocks of 16 rows there
-  int64_t v = 0, acc = 0, split = 0;  // workspace bytes
-};
+constexpr int64_t kLoraRows = 64;  // at most this many take the rows' kernel
 
 int64_t round256(int64_t n) { return cdiv(n, 256) * 256; }
 
-mm_status lora_plan(int64_t M, int64_t N, int64_t K, int64_t R, LoraPlan* p) {
-  p->mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-  const int64_t blocks = cdiv(M, 16 * p->mb);
-  const int64_t want = std::min<int64_t>(16, std::max<int64_t>(1, 512 / blocks));
-  p->kc = std::max<int64_t>(512, cdiv(cdiv(K, want), 64) * 64);
-  p->slices = cdiv(K, p->kc);
-  p->v = round256(p->slices * M * R * 4);
-  if (M <= kLoraRows) return MM_OK;
+struct LoraPlan {
+  int mb = 0;  // blocks of 16 rows of the rows' kernel (0: tiles)
+  int spw = 0;  // its steps of 64 k per wave
+  int64_t slices = 1;  // of K
+  bool finish = false;  // the rows' kernel writes the output
+  int low_mb = 0, turns = 0;  // the adapters' first product: blocks of 16 rows, adapters at once
+  int64_t low_slices = 1, low_k = 0;  // of K there
+  int64_t low = 0, v = 0, acc = 0, split = 0;  // workspace bytes
+  int64_t bytes() const { return low + v + acc + split; }
+};
+
+mm_status lora_plan(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, LoraPlan* p) {
+  // A x: enough workgroups to draw on every CU, K in slices of 512 or more.  Decode rows
+  // may each have an adapter of their own; of prompts a block of rows has one or two.
+  p->low_mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+  p->turns = M <= 64 ? (int)std::min(M, L) : (int)std::min<int64_t>(2, L);
+  const int64_t at_once = cdiv(M, 16 * p->low_mb) * cdiv(R, 16) * (M <= 64 ? p->turns : 1);
+  const int64_t want = std::min<int64_t>(16, cdiv(512, at_once));
+  p->low_k = std::max<int64_t>(512, cdiv(cdiv(K, want), 64) * 64);
+  p->low_slices = cdiv(K, p->low_k);
+  p->low = round256(p->low_slices * M * R * 4);
+  p->v = round256(M * 2 * R * 2);
+  if (M <= kLoraRows) {
+    p->mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+    const int64_t steps = cdiv(K, 64), most = 8 / p->mb;
+    p->slices = cdiv(steps, mmk::kLoraWaves * most);
+    p->spw = 2;
+    while (mmk::kLoraWaves * p->spw * p->slices < steps) p->spw *= 2;
+    p->finish = p->slices == 1 && p->mb < 4;
+    if (!p->finish) p->acc = round256(p->slices * M * N * 4);
+    return MM_OK;
+  }
   p->acc = round256(M * N * 4);
   int64_t split = 0;
   const mm_status s = mm_workspace_size(0, M, N, K, MM_NT, &split);
   p->split = round256(split);
   return s;
+}
+
+template <bool FINISH>
+const void* lora_rows_kernel(int mb, int spw) {
+  if (mb == 2) return spw == 2 ? fn(&mmk::lora_rows<2, 2, FINISH>) : fn(&mmk::lora_rows<2, 4, FINISH>);
+  return spw == 2   ? fn(&mmk::lora_rows<1, 2, FINISH>)
+         : spw == 4 ? fn(&mmk::lora_rows<1, 4, FINISH>)
+                    : fn(&mmk::lora_rows<1, 8, FINISH>);
 }
 
 mm_status check_lora(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
@@ -442,11 +468,42 @@ const void* moe_route_kernel(int64_t E) {
          : E <= 256 ? fn(&mmk::moe_route<4>)
                     : fn(&mmk::moe_route<8>);
 }
-const void* moe_gate_up_kernel(int64_t T) {
-  return T <= 16 ? fn(&mmk::moe_gate_up<1>) : T <= 32 ? fn(&mmk::moe_gate_up<2>) : fn(&mmk::moe_gate_up<4>);
+const void* moe_gate_up_kernel(int64_t E) {
+  return E <= 64    ? fn(&mmk::moe_gate_up<1, 1>)
+         : E <= 128 ? fn(&mmk::moe_gate_up<2, 1>)
+         : E <= 256 ? fn(&mmk::moe_gate_up<4, 1>)
+                    : fn(&mmk::moe_gate_up<8, 1>);
 }
-const void* moe_down_kernel(int64_t T) {
-  return T <= 16 ? fn(&mmk::moe_down<1>) : T <= 32 ? fn(&mmk::moe_down<2>) : fn(&mmk::moe_down<4>);
+
+// Workgroups that share 16 columns of the second layer: the number that spreads the
+// columns' workgroups most evenly over the CUs, a further one for a twentieth.
+int64_t moe_splits(int64_t H) {
+  const int64_t blocks = cdiv(H, 16);
+  int64_t best = 1;
+  double least = 0.0;
+  for (int64_t s = 1; s <= 8; ++s) {
+    const double c = (double)cdiv(blocks * s, 256) / (double)s * (1.0 + 0.02 * (double)(s - 1)) + (s > 1 ? 0.05 : 0.0);
+    if (s == 1 || c < least) least = c, best = s;
+  }
+  return best;
+}
+
+// Blocks of 16 tokens to a group: two where an expert has 16 on the average.  Measured (us
+// a call, one / two): 64 tokens, 2 of 8 experts of 4096 x 4096 302 / 288, 1 of 8 200 / 217,
+// 6 of 32 of 2048 x 4096 456 / 486.
+int moe_group_blocks(int64_t T, int64_t E, int64_t k) { return T > 16 && T * k >= 16 * E ? 2 : 1; }
+
+struct MoePlan {
+  int64_t splits, mid, part;  // (the last two: workspace bytes, after the tables)
+  int64_t bytes() const { return kMoeTableBytes + mid + part; }
+};
+
+MoePlan moe_plan(int64_t T, int64_t H, int64_t I, int64_t k) {
+  MoePlan p;
+  p.splits = H > 0 ? moe_splits(H) : 1;
+  p.mid = round256(T * k * I * 4);
+  p.part = p.splits > 1 ? round256(p.splits * T * H * 4) : 0;
+  return p;
 }
 
 }  // namespace
@@ -856,8 +913,8 @@ mm_status mm_linear_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t
   mm_status s = check_lora(M, N, K, rank, adapters);
   if (s != MM_OK || M == 0 || N == 0 || K == 0 || rank == 0 || adapters == 0) return s;
   LoraPlan plan;
-  if ((s = lora_plan(M, N, K, rank, &plan)) != MM_OK) return s;
-  *bytes = plan.v + plan.acc + plan.split;
+  if ((s = lora_plan(M, N, K, rank, adapters, &plan)) != MM_OK) return s;
+  *bytes = plan.bytes();
   return MM_OK;
 }
 
@@ -881,8 +938,8 @@ mm_status mm_linear_lora(const void* x, const void* W, const void* A, const void
   const Span outs[] = {{out, M * N * 2}, {workspace, workspace_bytes}};
   if (any_overlap(in, outs)) return fail(MM_ERR_INVALID_VALUE, "out or the workspace overlaps an operand or each other");
   LoraPlan plan;
-  if ((s = lora_plan(M, N, K, rank, &plan)) != MM_OK) return s;
-  if (!workspace || workspace_bytes < plan.v + plan.acc + plan.split)
+  if ((s = lora_plan(M, N, K, rank, adapters, &plan)) != MM_OK) return s;
+  if (!workspace || workspace_bytes < plan.bytes())
     return fail(MM_ERR_INVALID_VALUE, "workspace smaller than mm_linear_lora_workspace_size reports");
   if (!aligned(workspace, 256)) return fail(MM_ERR_MISALIGNED, "workspace must be 256-byte aligned");
   mmk::LoraParams p;
@@ -894,33 +951,48 @@ mm_status mm_linear_lora(const void* x, const void* W, const void* A, const void
   p.scale = scale;
   p.bias = static_cast<const uint16_t*>(bias);
   p.out = static_cast<uint16_t*>(out);
-  p.v = static_cast<float*>(workspace);
-  p.acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.v);
+  char* ws = static_cast<char*>(workspace);
+  p.low = reinterpret_cast<float*>(ws);
+  p.v = reinterpret_cast<uint16_t*>(ws + plan.low);
+  p.acc = reinterpret_cast<float*>(ws + plan.low + plan.v);
   p.M = (int)M;
   p.N = (int)N;
   p.K = (int)K;
   p.R = (int)rank;
   p.L = (int)adapters;
   p.slices = (int)plan.slices;
-  p.kc = (int)plan.kc;
   p.epi = epi;
+  p.low_slices = (int)plan.low_slices;
+  p.low_k = (int)plan.low_k;
   void* args[] = {&p};
-  const int64_t blocks = cdiv(M, 16 * plan.mb);
-  if (blocks > kMaxGridY) return fail(MM_ERR_UNSUPPORTED, "M must be below 2^22");
-  const void* shrink = plan.mb == 1   ? fn(&mmk::lora_shrink<1>)
-                       : plan.mb == 2 ? fn(&mmk::lora_shrink<2>)
-                                      : fn(&mmk::lora_shrink<4>);
-  const int64_t turns = std::min<int64_t>(std::min<int64_t>(M, adapters), M <= 64 ? 16 : 2);
-  s = launch(shrink, dim3((unsigned)plan.slices, (unsigned)blocks, (unsigned)turns), mmk::kLoraWaves * 64, args, stream,
-             "linear_lora shrink");
+  const int64_t row_blocks = cdiv(M, 16 * plan.low_mb);
+  if (row_blocks > kMaxGridY) return fail(MM_ERR_UNSUPPORTED, "M must be below 2^22");
+  void* shrink_args[] = {&p, &plan.turns};
+  s = launch(plan.low_mb == 1   ? fn(&mmk::lora_shrink<1>)
+             : plan.low_mb == 2 ? fn(&mmk::lora_shrink<2>)
+                                : fn(&mmk::lora_shrink<4>),
+             dim3((unsigned)plan.low_slices, (unsigned)row_blocks, (unsigned)(cdiv(rank, 16) * plan.turns)),
+             mmk::kLoraShrinkWaves * 64, shrink_args, stream, "linear_lora shrink");
   if (s != MM_OK) return s;
-  if (M <= kLoraRows)
-    return launch(M <= 16 ? fn(&mmk::lora_rows<1>) : fn(&mmk::lora_rows<2>), dim3((unsigned)cdiv(N, 16)),
-                  mmk::kLoraWaves * 64, args, stream, "linear_lora rows");
-  void* split = plan.split ? static_cast<char*>(workspace) + plan.v + plan.acc : nullptr;
-  s = mm_matmul_ws(x, W, const_cast<float*>(p.acc), M, N, K, MM_NT, MM_OUT_F32, split, plan.split, stream);
-  if (s != MM_OK) return s;
-  return launch(fn(&mmk::lora_join), dim3((unsigned)cdiv(N, 256), (unsigned)cdiv(M, 64)), 256, args, stream,
+  if (plan.mb) {
+    int cus = 0;
+    if ((s = device_cus(&cus)) != MM_OK) return s;
+    const int64_t blocks = cdiv(N, 16), each = cdiv(blocks * plan.slices, cus);
+    const void* k = plan.mb == 4   ? fn(&mmk::lora_rows<4, 2, false>)
+                    : plan.finish ? lora_rows_kernel<true>(plan.mb, plan.spw)
+                                  : lora_rows_kernel<false>(plan.mb, plan.spw);
+    s = launch(k, dim3((unsigned)cdiv(blocks, each), (unsigned)plan.slices),
+               mmk::kLoraWaves * 64, args, stream, "linear_lora rows");
+    if (s != MM_OK || plan.finish) return s;
+  } else {
+    s = launch(fn(&mmk::lora_fold), dim3((unsigned)std::min<int64_t>(cdiv(M * rank / 8, 256), 1024)), 256, args, stream,
+               "linear_lora fold");
+    if (s != MM_OK) return s;
+    void* split = plan.split ? ws + plan.low + plan.v + plan.acc : nullptr;
+    s = mm_matmul_ws(x, W, p.acc, M, N, K, MM_NT, MM_OUT_F32, split, plan.split, stream);
+    if (s != MM_OK) return s;
+  }
+  return launch(fn(&mmk::lora_join), dim3((unsigned)cdiv(N, 64), (unsigned)cdiv(M, 64)), 256, args, stream,
                 "linear_lora join");
 }
 
@@ -929,7 +1001,7 @@ mm_status mm_moe_ffn_workspace_size(int64_t tokens, int64_t experts, int64_t H, 
   *bytes = 0;
   const mm_status s = check_moe(tokens, experts, H, I, top_k);
   if (s != MM_OK || tokens == 0) return s;
-  *bytes = kMoeTableBytes + round256(tokens * top_k * I * 4);
+  *bytes = moe_plan(tokens, H, I, top_k).bytes();
   return MM_OK;
 }
 
@@ -952,7 +1024,8 @@ mm_status mm_moe_ffn(const void* x, const float* logits, const void* W_gate, con
                      {W_down, E * I * H * 2}};
   const Span outs[] = {{out, T * H * 2}, {experts, T * top_k * 4}, {weights, T * top_k * 4}, {workspace, workspace_bytes}};
   if (any_overlap(in, outs)) return fail(MM_ERR_INVALID_VALUE, "an output or the workspace overlaps an input or another output");
-  if (!workspace || workspace_bytes < kMoeTableBytes + round256(T * top_k * I * 4))
+  const MoePlan plan = moe_plan(T, H, I, top_k);
+  if (!workspace || workspace_bytes < plan.bytes())
     return fail(MM_ERR_INVALID_VALUE, "workspace smaller than mm_moe_ffn_workspace_size reports");
   if (!aligned(workspace, 256)) return fail(MM_ERR_MISALIGNED, "workspace must be 256-byte aligned");
   mmk::MoeParams p;
@@ -964,26 +1037,40 @@ mm_status mm_moe_ffn(const void* x, const float* logits, const void* W_gate, con
   p.out = static_cast<uint16_t*>(out);
   p.experts = experts;
   p.weights = weights;
-  p.tab = static_cast<mmk::MoeTables*>(workspace);
-  p.mid = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + kMoeTableBytes);
+  char* ws = static_cast<char*>(workspace);
+  p.tab = reinterpret_cast<mmk::MoeTables*>(ws);
+  p.mid = reinterpret_cast<uint16_t*>(ws + kMoeTableBytes);
+  p.part = reinterpret_cast<float*>(ws + kMoeTableBytes + plan.mid);
   p.T = (int)T;
   p.E = (int)E;
   p.H = (int)H;
   p.I = (int)I;
   p.k = (int)top_k;
   p.renormalize = renormalize != 0;
+  p.splits = (int)plan.splits;
   void* args[] = {&p};
-  if ((s = launch(moe_route_kernel(E), dim3(1), 1024, args, stream, "moe_ffn route")) != MM_OK) return s;
+  // Few tokens: every workgroup of the first layer finds their experts itself.
+  const int64_t units = T * top_k * (I / 8);  // (at most: a group for every choice)
+  const bool own = T <= mmk::kMoeFew && units > 0 && H > 0;
+  const int gb = moe_group_blocks(T, E, top_k);
+  int group = 16 * gb;
+  void* route_args[] = {&p, &group};
+  if (!own && (s = launch(moe_route_kernel(E), dim3(1), 1024, route_args, stream, "moe_ffn route")) != MM_OK) return s;
   if (H == 0) return MM_OK;
   int cus = 0;
   if ((s = device_cus(&cus)) != MM_OK) return s;
-  const int64_t units = std::min(E, T * top_k) * (I / 8);
   if (units > 0) {
-    s = launch(moe_gate_up_kernel(T), dim3((unsigned)std::min<int64_t>(units, 4 * (int64_t)cus)), mmk::kMoeWaves * 64, args,
-               stream, "moe_ffn gate and up");
+    s = launch(own ? moe_gate_up_kernel(E) : gb == 1 ? fn(&mmk::moe_gate_up<0, 1>) : fn(&mmk::moe_gate_up<0, 2>),
+               dim3((unsigned)std::min<int64_t>(units, 4 * (int64_t)cus)), mmk::kMoeWaves * 64, args, stream,
+               "moe_ffn gate and up");
     if (s != MM_OK) return s;
   }
-  return launch(moe_down_kernel(T), dim3((unsigned)cdiv(H, 16)), mmk::kMoeWaves * 64, args, stream, "moe_ffn down");
+  s = launch(T <= 16   ? fn(&mmk::moe_down<1, 1>)
+             : gb == 1 ? fn(&mmk::moe_down<4, 1>)
+                       : fn(&mmk::moe_down<4, 2>),
+             dim3((unsigned)cdiv(H, 16), (unsigned)plan.splits), mmk::kMoeWaves * 64, args, stream, "moe_ffn down");
+  if (s != MM_OK || plan.splits == 1) return s;
+  return launch(fn(&mmk::moe_join), dim3((unsigned)cdiv(T * H, 1024)), 256, args, stream, "moe_ffn join");
 }
 
 }  // extern "C"
