@@ -6,10 +6,13 @@
 //
 // lora_shrink leaves A_a x[m] in fp32, in slices of K.  Few rows (a decode step): bound by
 // reading W once; lora_rows streams it and adds B (s_a A_a x[m]) to the same sums.
-// Many rows: the library's tile kernels leave W x in fp32, and lora_join adds the rest.
+// Many rows: lora_tile takes the adapters' terms as further steps of K; where K is
+// cut into slices, lora_join adds them.
 // v = s_a A_a x enters the products with B as two bf16 numbers, high and low part, 16
 // bits of significand: as one, its rounding would be as large as the output's own.
 #pragma once
+
+#include <type_traits>
 
 #include "moe_ffn.hpp"
 #include "rms_norm.hpp"
@@ -35,6 +38,17 @@ struct LoraParams {
   int low_slices, low_k;  // slices of K of low_k (a multiple of 64)
   int slices;             // of acc
   int epi;
+  int tiles_m, tiles_n;   // lora_tile: tiles, K in `slices` pieces of slice_steps super-steps
+  int slice_steps;
+  const struct LoraTileRows* tiles;  // [tiles_m]
+};
+
+// The adapters that a tile's rows (at most 256) have, in the order of their first rows,
+// and which rows.
+struct LoraTileRows {
+  int count;
+  int adapter[256];
+  uint64_t rows[256][4];
 };
 
 // The adapter of row `row`, -1 for none (past the last row, or an index that names none).
@@ -76,31 +90,30 @@ __device__ __forceinline__ u32x4 step_chunk(__amdgpu_buffer_rsrc_t buf, uint32_t
   return load_chunk(buf, off, 128u * (uint32_t)min(st, steps - 1));
 }
 
-// A x of the rows 16 MB y .. + 16 MB - 1 over slice x of K, for ranks 16 z .. + 15 (z the
-// first part of blockIdx.z); of the adapters among the rows, every turns-th.  The waves
-// take every eighth step of 64 k, each step's loads one step ahead, and meet in LDS, added in
-// wave order.  A CU by itself reads some 25 bytes per ns, so the slices, adapters
-// and ranks of few rows go to many (one token, rank 16, K 8192: 4.5 us in 16 slices, 12
-// in one).
-template <int MB>
+// A x of the rows 16 MB y .. + 16 MB - 1 over slice x of K, for 16 RB ranks; of the
+// adapters among the rows, every turns-th (blockIdx.z: ranks and turn).  The waves take every
+// eighth step of 64 k, each step's loads one step ahead, and meet in LDS, added in wave
+// order.  A CU by itself reads some 25 bytes per ns, so the slices, adapters and ranks
+// of few rows go to many (one token, rank 16, K 8192: 4.5 us in 16 slices, 12 in one).
+template <int MB, int RB>
 __global__ void __launch_bounds__(kLoraShrinkWaves * 64) lora_shrink(LoraParams p, int turns) {
-  __shared__ f32x4 red[kLoraShrinkWaves][MB][64];
+  __shared__ f32x4 red[kLoraShrinkWaves][MB * RB][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lx = lane & 15, lg = lane >> 4;
   const int m0 = blockIdx.y * (16 * MB), rows = min(16 * MB, p.M - m0);
-  const int r0 = (int)(blockIdx.z / turns) * 16, my_turn = blockIdx.z % turns;
+  const int r0 = (int)(blockIdx.z / turns) * (16 * RB), my_turn = blockIdx.z % turns;
   const int K = p.K, kbeg = blockIdx.x * p.low_k, klen = min(p.low_k, K - kbeg), steps = (klen + 63) >> 6;
   // (of a slice of a row the buffer ends where the last row's does)
   const __amdgpu_buffer_rsrc_t rx = slice_buffer(p.x + (int64_t)m0 * K + kbeg, rows, K, kbeg);
   struct Step {
-    u32x4 w[2], x[MB][2];
+    u32x4 w[RB][2], x[MB][2];
   };
   int turn = 0;
   each_adapter(lane < rows ? lora_adapter(p, m0 + lane) : -1, [&](int a, uint64_t same) {
     if (turn++ % turns != my_turn) return;
-    const __amdgpu_buffer_rsrc_t rw = slice_buffer(p.A + ((int64_t)a * p.R + r0) * K + kbeg, min(16, p.R - r0), K, kbeg);
-    const uint32_t row = (uint32_t)lx * (uint32_t)K * 2u;
+    const __amdgpu_buffer_rsrc_t rw =
+        slice_buffer(p.A + ((int64_t)a * p.R + r0) * K + kbeg, min(16 * RB, p.R - r0), K, kbeg);
     uint32_t xrow[MB];  // (rows of other adapters are not loaded)
 #pragma unroll
     for (int b = 0; b < MB; ++b)
@@ -108,20 +121,26 @@ __global__ void __launch_bounds__(kLoraShrinkWaves * 64) lora_shrink(LoraParams 
     auto load = [&](int st, Step& t) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        t.w[j] = step_chunk(rw, row, st, j, klen, steps, lg);
+#pragma unroll
+        for (int c = 0; c < RB; ++c)
+          t.w[c][j] = step_chunk(rw, (uint32_t)(16 * c + lx) * (uint32_t)K * 2u, st, j, klen, steps, lg);
 #pragma unroll
         for (int b = 0; b < MB; ++b) t.x[b][j] = step_chunk(rx, xrow[b], st, j, klen, steps, lg);
       }
     };
-    f32x4 acc[MB];
+    f32x4 acc[MB][RB];
 #pragma unroll
-    for (int b = 0; b < MB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+      for (int c = 0; c < RB; ++c) acc[b][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     auto step = [&](int st, Step& t, Step& next) __attribute__((always_inline)) {
       load(st + kLoraShrinkWaves, next);
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int b = 0; b < MB; ++b) acc[b] = mfma_bf16(t.x[b][j], t.w[j], acc[b]);
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+          for (int c = 0; c < RB; ++c) acc[b][c] = mfma_bf16(t.x[b][j], t.w[c][j], acc[b][c]);
     };
     Step s0, s1;
     load(wave, s0);
@@ -131,20 +150,22 @@ __global__ void __launch_bounds__(kLoraShrinkWaves * 64) lora_shrink(LoraParams 
     }
     __syncthreads();  // (what was there before has been read)
 #pragma unroll
-    for (int b = 0; b < MB; ++b) red[wave][b][lane] = acc[b];
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+      for (int c = 0; c < RB; ++c) red[wave][b * RB + c][lane] = acc[b][c];
     __syncthreads();
-    if (wave < MB) {
-      f32x4 s = red[0][wave][lane];
+    for (int i = wave; i < MB * RB; i += kLoraShrinkWaves) {
+      f32x4 s = red[0][i][lane];
 #pragma unroll
       for (int q = 1; q < kLoraShrinkWaves; ++q) {
-        const f32x4 u = red[q][wave][lane];
+        const f32x4 u = red[q][i][lane];
 #pragma unroll
         for (int f = 0; f < 4; ++f) s[f] += u[f];
       }
-      const int r = r0 + lx;
+      const int r = r0 + 16 * (i % RB) + lx;
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
-        const int m = 16 * wave + 4 * lg + f;
+        const int m = 16 * (i / RB) + 4 * lg + f;
         if (r < p.R && ((same >> m) & 1)) p.low[((int64_t)blockIdx.x * p.M + m0 + m) * p.R + r] = s[f];
       }
     }
@@ -189,8 +210,41 @@ __device__ __forceinline__ void lora_fold_all(const LoraParams& p, int64_t threa
     *reinterpret_cast<u32x4*>(v + p.R) = lo;
   }
 }
-__global__ void __launch_bounds__(256) lora_fold(LoraParams p) {
-  lora_fold_all(p, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
+// v of every row, and the adapters of every tile of `bm` rows (0: not needed), which the first
+// workgroups find.
+__global__ void __launch_bounds__(256) lora_fold(LoraParams p, LoraTileRows* tiles, int bm) {
+  const int finders = bm ? p.tiles_m : 0;
+  if ((int)blockIdx.x >= finders) {
+    lora_fold_all(p, (int64_t)(blockIdx.x - finders) * 256 + threadIdx.x, (int64_t)(gridDim.x - finders) * 256);
+    return;
+  }
+  // one wave, four rows to a lane
+  if (threadIdx.x >= 64) return;
+  const int lane = threadIdx.x;
+  LoraTileRows* t = tiles + blockIdx.x;
+  int mine[4];
+  uint64_t left[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    mine[g] = 64 * g < bm ? lora_adapter(p, (int)blockIdx.x * bm + 64 * g + lane) : -1;
+    left[g] = __ballot(mine[g] >= 0);
+  }
+  int count = 0;
+  while (left[0] | left[1] | left[2] | left[3]) {
+    int a = -1;
+#pragma unroll
+    for (int g = 3; g >= 0; --g)
+      if (left[g]) a = __builtin_amdgcn_readlane(mine[g], __builtin_ctzll(left[g]));
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const uint64_t same = __ballot(mine[g] == a);
+      left[g] &= ~same;
+      if (lane == g) t->rows[count][g] = same;
+    }
+    if (lane == 0) t->adapter[count] = a;
+    ++count;
+  }
+  if (lane == 0) t->count = count;
 }
 
 // Up to 16 MB rows.  A workgroup takes a slice y of K, 16 SPW steps of 64 k, and every
@@ -420,6 +474,467 @@ __global__ void __launch_bounds__(256) lora_join(LoraParams p) {
         if (n + f < p.N) o[f] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[f]));
     }
   }
+}
+
+// ---- many rows ---------------------------------------------------------------
+
+// `rows` rows of an operand of `row_bytes` from row `row0` (of `have`) as a buffer.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rows(const void* base, int64_t row0, int64_t have, int rows,
+                                                            uint32_t row_bytes) {
+  const uint32_t n = (uint32_t)min((int64_t)rows, have - row0);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(base)) + row0 * (int64_t)row_bytes,
+                                           (short)0, (int)(n * row_bytes), 0x00020000);
+}
+
+// A lane's 16 sums of the 32 x 32 block at (mb, nb): row mb + lane % 32, columns nb + 8 h + 0..7
+// and + 16 (h = lane / 32).  Epilogue, one rounding.
+__device__ __forceinline__ void lora_block(const LoraParams& p, float (&v)[16], int mb, int nb, int lane, bool has_bias,
+                                           bool gelu) {
+  int first = nb + 8 * (lane >> 5);
+  asm volatile("" : "+v"(first));  // (as in q8_block)
+  uint32_t bs[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+  if (has_bias) {
+    if (nb + 32 <= p.N) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) __builtin_memcpy(&bs[4 * r], p.bias + first + 16 * r, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int n = first + 16 * (i >> 2) + 2 * (i & 3);
+        bs[i] = (uint32_t)p.bias[min(n, p.N - 1)] | (uint32_t)p.bias[min(n + 1, p.N - 1)] << 16;
+      }
+    }
+  }
+  // (without a bias 0 is added: sums that only some paths change spilled)
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] += __builtin_bit_cast(float, i & 1 ? bs[i >> 1] & 0xffff0000u : bs[i >> 1] << 16);
+  if (gelu) gelu_tanh_all(v);
+  if (nb + 32 <= p.N) {
+    // (16-byte stores of 64 consecutive bytes of a row by four lanes, as in q8_block)
+    u32x4 pk[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const auto t = __builtin_amdgcn_permlane16_swap(pack_bf16x2(v[2 * i], v[2 * i + 1]),
+                                                      pack_bf16x2(v[8 + 2 * i], v[9 + 2 * i]), false, false);
+      pk[0][i] = t[0];
+      pk[1][i] = t[1];
+    }
+    int n = nb + 16 * ((lane >> 4) & 1) + 8 * (lane >> 5);
+    asm volatile("" : "+v"(n));
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int m = mb + 16 * r + (lane & 15);
+      if (m < p.M) __builtin_memcpy(p.out + (int64_t)m * p.N + n, &pk[r], 16);
+    }
+  } else if (mb + (lane & 31) < p.M) {
+    uint16_t* o = p.out + (int64_t)(mb + (lane & 31)) * p.N + first;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int n = 16 * (i >> 3) + (i & 7);
+      if (n < p.N - first) o[n] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[i]));
+    }
+  }
+}
+
+// NaN into those outputs of a wave's 32 x 32 block at (mb, nb) whose row of B, of the output
+// row's adapter, is not finite.
+__device__ __forceinline__ void lora_mark(const LoraParams& p, int mb, int nb, int lane) {
+  const int m = mb + (lane & 31), a = lora_adapter(p, m);
+  if (a < 0) return;
+#pragma unroll 1
+  for (int n = nb + 16 * (lane >> 5); n < min(nb + 16 * (lane >> 5) + 16, p.N); ++n) {
+    const uint16_t* b = p.B + ((int64_t)a * p.N + n) * p.R;
+    bool odd = false;
+#pragma unroll 1
+    for (int r = 0; r < p.R; r += 8) {
+      const u32x4 u = *reinterpret_cast<const u32x4*>(b + r);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) odd |= (((u[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0;
+    }
+    if (odd) p.out[(int64_t)m * p.N + n] = 0x7fc0;
+  }
+}
+
+// Tiles of 64 FM rows by 64 FN columns, in the manner of gemm_q8_tile (LDS rows of 128
+// bytes, here 64 k of bf16; the same rings, waits and layout; two v_mfma_f32_32x32x16_bf16 where that
+// has one instruction).
+//
+// The adapters' terms are further super-steps of the same sums: for each adapter among a
+// tile's rows ceil(R / 32) of them, in which x stands for the rows' v, high parts then
+// low parts (rows of other adapters lie past the buffer's end: zeros), and W for the adapter's
+// B, twice.  So a tile of one adapter of rank 32 costs one super-step more.
+// (A zero times an infinity or a NaN of B would be NaN in the other rows: zeros are taken
+// for them, and the adapter's rows get NaN in their columns at the end.)
+// SPLIT: the instance for a K cut into slices; those leave their sums of W x for lora_join.
+template <int FM, int FN, int SX, int SW, bool SPLIT>
+__global__ void __launch_bounds__(256, SX * FM + SW * FN <= 10 ? 2 : 1) lora_tile(LoraParams p) {
+  constexpr int BM = 64 * FM, BN = 64 * FN, XS = BM * 128, WS = BN * 128;
+  constexpr int CX = 2 * FM, CW = 2 * FN;  // copies of 8 rows per wave and super-step
+  // copies that a wait for a super-step may leave in flight: those issued after
+  // the later of its own
+  constexpr int kAhead = SX <= SW ? (SX - 2) * (CX + CW) : CX + (SW - 2) * (CX + CW);
+  constexpr int PER = (CX + CW + 2 * FM * FN - 1) / (2 * FM * FN);  // copies per MFMA of a step
+  __shared__ __attribute__((aligned(1024))) char smem[SX * XS + SW * WS];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l32 = lane & 31, h = lane >> 5;
+  const int wm = (wave >> 1) * (32 * FM), wn = (wave & 1) * (32 * FN);
+  const int G = gridDim.x;
+  const int wg = __builtin_amdgcn_readfirstlane(remap_workgroup(blockIdx.x, G, 1));
+  const int my_units =
+      __builtin_amdgcn_readfirstlane((p.tiles_m * p.tiles_n * (SPLIT ? p.slices : 1) - wg + G - 1) / G);
+  const int KS = (p.K + 63) >> 6;
+  // The arguments as what the compiler does not know to be the same: where they are needed
+  // only from tile to tile they are loaded again, and take no scalar registers in the K loop.
+  auto args = []() __attribute__((always_inline)) {
+    auto* a = (__attribute__((address_space(4))) const LoraParams*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(a));
+    return a;
+  };
+
+  // the lane's place in a copy: row (of 8) and chunk (of even and odd copies); opaque too
+  struct Place {
+    int row;
+    uint32_t chunk[2];
+  };
+  auto place = [&]() __attribute__((always_inline)) {
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    const int row = l >> 3;
+    return Place{row, {16u * (uint32_t)((l & 7) ^ (row >> 1)), 16u * (uint32_t)((l & 7) ^ (4 + (row >> 1)))}};
+  };
+  // the operand row of the lane in copy c
+  auto row_x = [&](int c, int row) __attribute__((always_inline)) { return (uint32_t)(8 * (wave * CX + c) + row); };
+  auto row_w = [&](int c, int row) __attribute__((always_inline)) {
+    const int t = wave * CW + c;
+    return (uint32_t)(32 * (t >> 2) + 16 * ((t >> 1) & 1) + 8 * (row >> 2) + 4 * (t & 1) + (row & 3));
+  };
+  uint32_t vx[CX], vw[CW];
+
+  // Where each operand's copies are: unit (of this workgroup's), super-step and its end.
+  __amdgpu_buffer_rsrc_t rx, rw;
+  uint32_t bx = 0, bw = 0;  // the super-step's part of the offsets
+  int xi = 0, xq = 0, xend = 0, wi = 0, wq = 0, wend = 0;
+  // unit i of this workgroup: its tile and its super-steps [q0, q1)
+  auto unit = [&](int i, int* tm, int* tn, int* q0, int* q1) __attribute__((always_inline)) {
+    const auto* p = args();
+    const int u = wg + i * G, tiles = p->tiles_m * p->tiles_n;
+    const int c = SPLIT ? __builtin_amdgcn_readfirstlane(u / tiles) : 0;
+    tile_coords(u - c * tiles, p->tiles_m, p->tiles_n, 4, tm, tn);
+    *tm = __builtin_amdgcn_readfirstlane(*tm);
+    *tn = __builtin_amdgcn_readfirstlane(*tn);
+    if constexpr (SPLIT) {
+      *q0 = c * p->slice_steps;
+      *q1 = min(*q0 + p->slice_steps, KS);
+    } else {
+      *q0 = 0;
+      *q1 = KS + __builtin_amdgcn_readfirstlane(p->tiles[*tm].count) * ((p->R + 31) >> 5);
+    }
+  };
+  // offsets of super-step q: of K, the ragged last one's chunks past K out of range
+  auto base = [&](int q, uint32_t row, uint32_t chunk, uint32_t K) __attribute__((always_inline)) {
+    return (row * K + chunk) | (128u * (uint32_t)q + chunk < K ? 0u : 0x80000000u);
+  };
+  auto base_x = [&]() __attribute__((always_inline)) {
+    const Place l = place();
+    const uint32_t K = 2u * (uint32_t)args()->K;
+#pragma unroll
+    for (int c = 0; c < CX; ++c) vx[c] = base(xq, row_x(c, l.row), l.chunk[c & 1], K);
+  };
+  auto base_w = [&]() __attribute__((always_inline)) {
+    const Place l = place();
+    const uint32_t K = 2u * (uint32_t)args()->K;
+#pragma unroll
+    for (int c = 0; c < CW; ++c) vw[c] = base(wq, row_w(c, l.row), l.chunk[c & 1], K);
+  };
+  // or of an adapter: piece e of its 2 R values
+  auto extra_x = [&]() __attribute__((always_inline)) {
+    const auto* p = args();
+    const Place l = place();
+    const int ES = (p->R + 31) >> 5, a = (xq - KS) / ES, e = (xq - KS) - a * ES;
+    const uint32_t R4 = 4u * (uint32_t)p->R;
+    int tm, tn, q0, q1;
+    unit(min(xi, my_units - 1), &tm, &tn, &q0, &q1);
+    rx = tile_rows(p->v, (int64_t)tm * BM, p->M, BM, R4);
+    const uint64_t rows = p->tiles[tm].rows[a][(8 * wave * CX) >> 6] >> ((8 * wave * CX) & 63);
+#pragma unroll
+    for (int c = 0; c < CX; ++c) {
+      const uint32_t at = 128u * (uint32_t)e + l.chunk[c & 1];
+      vx[c] = at < R4 && ((rows >> (8 * c + l.row)) & 1) ? row_x(c, l.row) * R4 + at : 0x80000000u;
+    }
+  };
+  auto extra_w = [&]() __attribute__((always_inline)) {
+    const auto* p = args();
+    const Place l = place();
+    const int ES = (p->R + 31) >> 5, a = (wq - KS) / ES, e = (wq - KS) - a * ES;
+    const uint32_t R2 = 2u * (uint32_t)p->R;
+    int tm, tn, q0, q1;
+    unit(min(wi, my_units - 1), &tm, &tn, &q0, &q1);
+    const int64_t first = (int64_t)__builtin_amdgcn_readfirstlane(p->tiles[tm].adapter[a]) * p->N;
+    rw = tile_rows(p->B, first + (int64_t)tn * BN, first + p->N, BN, R2);
+#pragma unroll
+    for (int c = 0; c < CW; ++c) {
+      const uint32_t at = 128u * (uint32_t)e + l.chunk[c & 1];
+      vw[c] = at < 2 * R2 ? row_w(c, l.row) * R2 + (at >= R2 ? at - R2 : at) : 0x80000000u;
+    }
+  };
+  // (past the last unit that one again, never read)
+  auto enter_x = [&]() __attribute__((always_inline)) {
+    int tm, tn;
+    unit(min(xi, my_units - 1), &tm, &tn, &xq, &xend);
+    const auto* p = args();
+    rx = tile_rows(p->x, (int64_t)tm * BM, p->M, BM, 2u * (uint32_t)p->K);
+    base_x();
+    bx = 128u * (uint32_t)xq;
+  };
+  auto enter_w = [&]() __attribute__((always_inline)) {
+    int tm, tn;
+    unit(min(wi, my_units - 1), &tm, &tn, &wq, &wend);
+    const auto* p = args();
+    rw = tile_rows(p->W, (int64_t)tn * BN, p->N, BN, 2u * (uint32_t)p->K);
+    base_w();
+    bw = 128u * (uint32_t)wq;
+  };
+  auto advance_x = [&]() __attribute__((always_inline)) {
+    ++xq;
+    bx += 128u;
+    if (xq >= KS - 1 || xq == xend) {
+      if (xq == xend) {
+        ++xi;
+        enter_x();
+      } else if (xq == KS - 1) {
+        base_x();
+      } else {
+        bx = 0;
+        extra_x();
+      }
+    }
+  };
+  auto advance_w = [&]() __attribute__((always_inline)) {
+    ++wq;
+    bw += 128u;
+    if (wq >= KS - 1 || wq == wend) {
+      if (wq == wend) {
+        ++wi;
+        enter_w();
+      } else if (wq == KS - 1) {
+        base_w();
+      } else {
+        bw = 0;
+        extra_w();
+      }
+    }
+  };
+  auto copy_x = [&](int c, int slot) __attribute__((always_inline)) {
+    copy_to_lds(rx, smem + slot * XS + (wave * CX + c) * 1024, vx[c], bx);
+  };
+  auto copy_w = [&](int c, int slot) __attribute__((always_inline)) {
+    copy_to_lds(rw, smem + SX * XS + slot * WS + (wave * CW + c) * 1024, vw[c], bw);
+  };
+
+  // fragments: chunks 4 s + 2 j + h of a row, j = 0, 1
+  const int f0 = l32 * 128 + ((h ^ ((l32 >> 1) & 7)) << 4);
+  struct Frag {
+    u32x4 j[2];
+  };
+  auto frag = [&](int base, int s) __attribute__((always_inline)) {
+    return Frag{{lds_chunk(smem + base + (f0 ^ (64 * s))), lds_chunk(smem + base + (f0 ^ (64 * s + 32)))}};
+  };
+  f32x16 acc[FM][FN];
+  Frag x[2][FM], w[2][FN];
+
+  auto frag_x = [&](int a, int slot, int s) __attribute__((always_inline)) {
+    return frag(slot * XS + (wm + 32 * a) * 128, s);
+  };
+  auto frag_w = [&](int b, int slot, int s) __attribute__((always_inline)) {
+    return frag(SX * XS + slot * WS + (wn + 32 * b) * 128, s);
+  };
+  auto multiply = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int a = 0; a < FM; ++a)
+#pragma unroll
+        for (int b = 0; b < FN; ++b)
+          acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w[s][b].j[j]),
+                                                              __builtin_bit_cast(bf16x8, x[s][a].j[j]), acc[a][b], 0, 0, 0);
+  };
+
+  enter_x();
+  enter_w();
+#pragma unroll
+  for (int q = 0; q < max(SX, SW); ++q) {
+    if (q > 0 && q < SW) advance_w();
+    if (q > 0 && q < SX) advance_x();
+    if (q < SW) {
+#pragma unroll
+      for (int c = 0; c < CW; ++c) copy_w(c, q);
+    }
+    if (q < SX) {
+#pragma unroll
+      for (int c = 0; c < CX; ++c) copy_x(c, q);
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((SX - 1) * CX + (SW - 1) * CW));
+  order();
+  __builtin_amdgcn_s_barrier();
+  order();
+  int xb = 0, wb = 0;  // slots of super-step q
+  for (int ui = 0; ui < my_units; ++ui) {
+    int tm, tn, q0, q1;
+    unit(ui, &tm, &tn, &q0, &q1);
+#pragma unroll
+    for (int a = 0; a < FM; ++a)
+#pragma unroll
+      for (int b = 0; b < FN; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
+    // (read here and not carried over from the unit before, whose epilogue needs the registers)
+#pragma unroll
+    for (int a = 0; a < FM; ++a) x[0][a] = frag_x(a, xb, 0);
+#pragma unroll
+    for (int b = 0; b < FN; ++b) w[0][b] = frag_w(b, wb, 0);
+    int left_out = 0;  // whether an adapter's B held what is not finite
+    auto clean = [&](int s) __attribute__((always_inline)) {
+      uint32_t any = 0;
+#pragma unroll
+      for (int b = 0; b < FN; ++b) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          // (an exponent of ones carries into the sign's place)
+          const uint32_t u = w[s][b].j[i >> 2][i & 3], odd = ((u & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+          w[s][b].j[i >> 2][i & 3] = u & ~((odd >> 15) * 0xffffu);
+          any |= odd;
+        }
+      }
+      left_out |= __any(any != 0);
+    };
+    // EXTRA: an adapter's super-step
+    auto super_step = [&](auto extra) __attribute__((always_inline)) {
+      constexpr bool EXTRA = decltype(extra)::value;
+#ifdef MM_DEBUG_FULL_SYNC
+      race_check_drain();  // every copy issued so far has landed, for every wave
+      __builtin_amdgcn_s_barrier();
+      order();
+#endif
+      if constexpr (EXTRA) clean(0);
+      // step 0
+#pragma unroll
+      for (int a = 0; a < FM; ++a) x[1][a] = frag_x(a, xb, 1);
+#pragma unroll
+      for (int b = 0; b < FN; ++b) w[1][b] = frag_w(b, wb, 1);
+      multiply(0);
+#pragma unroll
+      for (int i = 0; i < 2 * FM * FN; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);    // an MFMA
+        __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);  // LDS reads
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(kAhead));
+      order();
+      __builtin_amdgcn_s_barrier();
+      order();
+      // (their branches stand here so that each step is a block of its own to
+      // the scheduler, whose groups otherwise mix the two)
+      advance_w();
+      advance_x();
+      if constexpr (EXTRA) clean(1);
+      const int xn = xb == SX - 1 ? 0 : xb + 1, wnext = wb == SW - 1 ? 0 : wb + 1;
+      // step 1.  The compiler keeps the order of copies and reads: a copy after
+      // each fragment, the others after those.
+      auto copy = [&](int c) __attribute__((always_inline)) {
+        if (c < CW)
+          copy_w(c, wb);
+        else
+          copy_x(c - CW, xb);
+      };
+#pragma unroll
+      for (int i = 0; i < FM + FN; ++i) {
+        if (i < FM)
+          x[0][i] = frag_x(i, xn, 0);
+        else
+          w[0][i - FM] = frag_w(i - FM, wnext, 0);
+        copy(i);
+      }
+#pragma unroll
+      for (int i = FM + FN; i < CX + CW; ++i) copy(i);
+      multiply(1);
+#pragma unroll
+      for (int i = 0; i < FM + FN; ++i) {
+        if (i < FM * FN) __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);  // two MFMAs
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);                   // a fragment
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);                   // a copy
+      }
+#pragma unroll
+      for (int i = FM + FN; i < CX + CW; ++i) {
+        if (i < FM * FN) __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      }
+      xb = xn;
+      wb = wnext;
+    };
+    for (int q = q0; q < min(q1, KS); ++q) super_step(std::false_type{});
+    if constexpr (!SPLIT) {
+      for (int q = KS; q < q1; ++q) super_step(std::true_type{});
+    }
+
+    const int m0 = tm * BM + wm, n0 = tn * BN + wn;
+    if constexpr (SPLIT) {
+      const int c = (wg + ui * G) / (p.tiles_m * p.tiles_n);
+#pragma unroll
+      for (int b = 0; b < FN; ++b)
+#pragma unroll
+        for (int a = 0; a < FM; ++a) {
+          const int m = m0 + 32 * a + l32;
+          int n = n0 + 32 * b + 8 * h;
+          asm volatile("" : "+v"(n));
+          if (m >= p.M) continue;
+          float* o = p.acc + ((int64_t)c * p.M + m) * p.N + n;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            if (n + 16 * r + 8 <= p.N) {
+#pragma unroll
+              for (int f = 0; f < 2; ++f) {
+                const f32x4 u = {acc[a][b][8 * r + 4 * f], acc[a][b][8 * r + 4 * f + 1], acc[a][b][8 * r + 4 * f + 2],
+                                 acc[a][b][8 * r + 4 * f + 3]};
+                __builtin_memcpy(o + 16 * r + 4 * f, &u, 16);
+              }
+            } else {
+#pragma unroll
+              for (int f = 0; f < 8; ++f)
+                if (n + 16 * r + f < p.N) o[16 * r + f] = acc[a][b][8 * r + f];
+            }
+          }
+        }
+      continue;
+    }
+    // (the last MFMAs' results are there: the compiler does not see the reads below for what
+    // they are)
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+    int el = lane;  // (opaque, as in place())
+    asm volatile("" : "+v"(el));
+    const int epi = args()->epi;
+    const bool has_bias = epi == EPI_BIAS || epi == EPI_BIAS_GELU, gelu = epi == EPI_GELU || epi == EPI_BIAS_GELU;
+#pragma unroll
+    for (int b = 0; b < FN; ++b)
+#pragma unroll
+      for (int a = 0; a < FM; ++a) {
+        // (each block's sums are moved when it is their turn: taken ahead, they spilled)
+        order();
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v[i]) : "a"(acc[a][b][i]));
+        lora_block(p, v, m0 + 32 * a, n0 + 32 * b, el, has_bias, gelu);
+      }
+    if (left_out) {
+      __builtin_amdgcn_s_waitcnt(0);  // (after the stores above, some of the same places)
+      order();
+#pragma unroll 1
+      for (int i = 0; i < FM * FN; ++i) lora_mark(p, m0 + 32 * (i / FN), n0 + 32 * (i % FN), el);
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0);  // (the copies past the last unit land before the workgroup ends)
 }
 
 }  // namespace mmk

@@ -387,19 +387,25 @@ struct LoraPlan {
   int spw = 0;  // its steps of 64 k per wave
   int64_t slices = 1;  // of K
   bool finish = false;  // the rows' kernel writes the output
-  int low_mb = 0, turns = 0;  // the adapters' first product: blocks of 16 rows, adapters at once
+  int low_mb = 0, low_rb = 0, turns = 0;  // the adapters' first product: blocks of 16 rows, of ranks, adapters at once
   int64_t low_slices = 1, low_k = 0;  // of K there
-  int64_t low = 0, v = 0, acc = 0, split = 0;  // workspace bytes
-  int64_t bytes() const { return low + v + acc + split; }
+  Q8Plan tiles;  // (mb == 0)
+  int64_t low = 0, v = 0, acc = 0, tile_rows = 0;  // workspace bytes
+  int64_t bytes() const { return low + v + acc + tile_rows; }
 };
+
+// The tiles of many rows: as of the 8-bit product of the same bytes, whose super-steps
+// these equal.
+Q8Plan lora_tile_plan(int64_t M, int64_t N, int64_t K) { return q8_plan(M, N, 2 * K, kQ8MaxChunks); }
 
 mm_status lora_plan(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, LoraPlan* p) {
   // A x: enough workgroups to draw on every CU, K in slices of 512 or more.  Decode rows
   // may each have an adapter of their own; of prompts a block of rows has one or two.
   p->low_mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+  p->low_rb = M > 64 && R > 16 ? 2 : 1;
   p->turns = M <= 64 ? (int)std::min(M, L) : (int)std::min<int64_t>(2, L);
-  const int64_t at_once = cdiv(M, 16 * p->low_mb) * cdiv(R, 16) * (M <= 64 ? p->turns : 1);
-  const int64_t want = std::min<int64_t>(16, cdiv(512, at_once));
+  const int64_t at_once = cdiv(M, 16 * p->low_mb) * cdiv(R, 16 * p->low_rb) * (M <= 64 ? p->turns : 1);
+  const int64_t want = std::min<int64_t>(16, M <= 64 ? cdiv(512, at_once) : std::max<int64_t>(1, 256 / at_once));
   p->low_k = std::max<int64_t>(512, cdiv(cdiv(K, want), 64) * 64);
   p->low_slices = cdiv(K, p->low_k);
   p->low = round256(p->low_slices * M * R * 4);
@@ -414,11 +420,24 @@ mm_status lora_plan(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, LoraP
     if (!p->finish) p->acc = round256(p->slices * M * N * 4);
     return MM_OK;
   }
-  p->acc = round256(M * N * 4);
-  int64_t split = 0;
-  const mm_status s = mm_workspace_size(0, M, N, K, MM_NT, &split);
-  p->split = round256(split);
-  return s;
+  p->tiles = lora_tile_plan(M, N, K);
+  p->tile_rows = p->tiles.chunks == 1 ? round256(p->tiles.tiles_m * (int64_t)sizeof(mmk::LoraTileRows)) : 0;
+  if (p->tiles.chunks > 1) p->acc = round256(p->tiles.chunks * M * N * 4);
+  return MM_OK;
+}
+
+template <int FM, int FN, int SX, int SW>
+const void* lora_tile_kernel(bool split) {
+  return split ? fn(&mmk::lora_tile<FM, FN, SX, SW, true>) : fn(&mmk::lora_tile<FM, FN, SX, SW, false>);
+}
+const void* lora_tile_kernel(int kind, bool split) {
+  switch (kind) {
+    case 0: return lora_tile_kernel<4, 4, 3, 2>(split);
+    case 1: return lora_tile_kernel<4, 2, 3, 4>(split);
+    case 2: return lora_tile_kernel<2, 2, 3, 2>(split);
+    case 3: return lora_tile_kernel<2, 2, 5, 5>(split);
+  }
+  return lora_tile_kernel<2, 1, 6, 6>(split);
 }
 
 template <bool FINISH>
@@ -436,7 +455,7 @@ mm_status check_lora(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
   if (R > mmk::kLoraMaxRank) return fail(MM_ERR_UNSUPPORTED, "rank must be at most 256");
   if (R % 8 != 0) return fail(MM_ERR_MISALIGNED, "rank must be a multiple of 8");
   if (K % 8 != 0) return fail(MM_ERR_MISALIGNED, "K must be a multiple of 8 elements");
-  if (K > (int64_t(1) << 22)) return fail(MM_ERR_UNSUPPORTED, "K must be at most 2^22");
+  if (K >= (int64_t(1) << 22)) return fail(MM_ERR_UNSUPPORTED, "K must be below 2^22");
   if (N > (int64_t(1) << 27) - 16) return fail(MM_ERR_UNSUPPORTED, "N must be at most 2^27 - 16");
   const int64_t room = int64_t(1) << 60;
   if (M > 0 && (N > room / M || K > room / M)) return fail(MM_ERR_UNSUPPORTED, "an operand spans 2^60 elements or more");
@@ -968,10 +987,11 @@ mm_status mm_linear_lora(const void* x, const void* W, const void* A, const void
   const int64_t row_blocks = cdiv(M, 16 * plan.low_mb);
   if (row_blocks > kMaxGridY) return fail(MM_ERR_UNSUPPORTED, "M must be below 2^22");
   void* shrink_args[] = {&p, &plan.turns};
-  s = launch(plan.low_mb == 1   ? fn(&mmk::lora_shrink<1>)
-             : plan.low_mb == 2 ? fn(&mmk::lora_shrink<2>)
-                                : fn(&mmk::lora_shrink<4>),
-             dim3((unsigned)plan.low_slices, (unsigned)row_blocks, (unsigned)(cdiv(rank, 16) * plan.turns)),
+  s = launch(plan.low_mb == 1   ? fn(&mmk::lora_shrink<1, 1>)
+             : plan.low_mb == 2 ? fn(&mmk::lora_shrink<2, 1>)
+             : plan.low_rb == 1 ? fn(&mmk::lora_shrink<4, 1>)
+                                : fn(&mmk::lora_shrink<4, 2>),
+             dim3((unsigned)plan.low_slices, (unsigned)row_blocks, (unsigned)(cdiv(rank, 16 * plan.low_rb) * plan.turns)),
              mmk::kLoraShrinkWaves * 64, shrink_args, stream, "linear_lora shrink");
   if (s != MM_OK) return s;
   if (plan.mb) {
@@ -985,12 +1005,27 @@ mm_status mm_linear_lora(const void* x, const void* W, const void* A, const void
                mmk::kLoraWaves * 64, args, stream, "linear_lora rows");
     if (s != MM_OK || plan.finish) return s;
   } else {
-    s = launch(fn(&mmk::lora_fold), dim3((unsigned)std::min<int64_t>(cdiv(M * rank / 8, 256), 1024)), 256, args, stream,
-               "linear_lora fold");
+    const Q8Plan& t = plan.tiles;
+    const bool split = t.chunks > 1;
+    p.tiles_m = (int)t.tiles_m;
+    p.tiles_n = (int)t.tiles_n;
+    p.slices = (int)t.chunks;
+    p.slice_steps = (int)t.chunk_steps;
+    mmk::LoraTileRows* rows = reinterpret_cast<mmk::LoraTileRows*>(ws + plan.low + plan.v + plan.acc);
+    p.tiles = rows;
+    int bm = split ? 0 : 64 * kQ8Kinds[t.kind].fm;
+    void* fold_args[] = {&p, &rows, &bm};
+    s = launch(fn(&mmk::lora_fold),
+               dim3((unsigned)((split ? 0 : t.tiles_m) + std::min<int64_t>(cdiv(M * rank / 8, 256), 1024))), 256, fold_args,
+               stream, "linear_lora fold");
     if (s != MM_OK) return s;
-    void* split = plan.split ? ws + plan.low + plan.v + plan.acc : nullptr;
-    s = mm_matmul_ws(x, W, p.acc, M, N, K, MM_NT, MM_OUT_F32, split, plan.split, stream);
-    if (s != MM_OK) return s;
+    int cus = 0;
+    if ((s = device_cus(&cus)) != MM_OK) return s;
+    const int64_t units = t.tiles_m * t.tiles_n * t.chunks;
+    s = launch(lora_tile_kernel(t.kind, split),
+               dim3((unsigned)std::min<int64_t>(units, (int64_t)cus * kQ8Kinds[t.kind].resident)), 256, args, stream,
+               "linear_lora tiles");
+    if (s != MM_OK || !split) return s;
   }
   return launch(fn(&mmk::lora_join), dim3((unsigned)cdiv(N, 64), (unsigned)cdiv(M, 64)), 256, args, stream,
                 "linear_lora join");

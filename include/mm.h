@@ -344,10 +344,11 @@ mm_status mm_layer_norm_backward(const void* dy, const void* h, const void* weig
  *   index   [M]: the row's adapter; a value that names none (below 0, or at least
  *           `adapters`) leaves the row without one
  *   scale   [adapters] fp32
- *   rank    a multiple of 8, at most 256;  K a multiple of 8, at most 2^22;
+ *   rank    a multiple of 8, at most 256;  K a multiple of 8, below 2^22;
  *           N at most 2^27 - 16;  M below 2^22
  * Sums are fp32; scale * (A x) enters the second product with 16 bits of
- * significand.  rank == 0, adapters == 0 or K == 0 is mm_linear.
+ * significand (in two parts: of an infinity in B the sum may be NaN).  What an adapter
+ * holds reaches the rows that name it and no others.  rank == 0, adapters == 0 or K == 0 is mm_linear.
  * The workspace (size from the function below, a device query; 256-byte aligned, any
  * contents) is needed by every other call of M > 0 and N > 0; two calls in flight at
  * once must not share it.  Other arguments, the epilogue and errors as for mm_linear. */
@@ -372,7 +373,7 @@ mm_status mm_linear_lora(const void* x, const void* W, const void* A, const void
  * token's weights and output NaN.
  * tokens <= 64, n_experts <= 512, top_k <= 16 and <= n_experts; H and I multiples of 8, at
  * most 2^18.  Sums are fp32; the products between the two layers are kept with 16 bits of
- * significand.  Three kernels.  tokens == 0 is a no-op.
+ * significand (in two parts: of an infinity in W_down the sum may be NaN).  tokens == 0 is a no-op.
  * The workspace (size from the function below, host arithmetic only; 256-byte
  * aligned, any contents) is needed by every other call; two calls in flight at once
  * must not share it. */

@@ -117,6 +117,27 @@ def test_linear_lora_rows_do_not_touch_each_other(dev, M):  # noqa: F811
     assert torch.equal(mm.linear_lora(d[0], d[1], A2, B2, index3, s2), mm.linear_lora(*d[:4], index3, d[5]))
 
 
+@pytest.mark.parametrize("M,N,K,R", [(5, 130, 520, 16), (30, 130, 2056, 8), (50, 200, 520, 40), (150, 130, 520, 16),
+                                     (300, 2100, 264, 72), (700, 3000, 1032, 16), (2100, 2100, 328, 8)])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+def test_linear_lora_broken_adapter(dev, M, N, K, R, value):  # noqa: F811
+    """An infinity or a NaN in an adapter's B: its rows lose that column (NaN, or an
+    infinity), all other outputs keep their bits."""
+    (x, W, A, B, index, scale), _ = inputs(M, N, K, R, 5, "mixed", M)
+    index[:3] = torch.tensor([2, 0, -1])
+    d = on(dev, x, W, A, B, index, scale)
+    want = mm.linear_lora(*d, epilogue="gelu_tanh").cpu()
+    assert want.isfinite().all()
+    broken = torch.zeros((5, N), dtype=torch.bool)
+    for a, n, r in ((2, 0, 0), (2, 77, R - 1), (0, N - 1, R // 2), (0, 64, 1)):
+        d[3][a, n, r] = value
+        broken[a, n] = True
+    got = mm.linear_lora(*d, epilogue="gelu_tanh").cpu()
+    bad = torch.where(index[:, None] >= 0, broken[index.clamp(min=0).long()], False)
+    assert torch.equal(got[~bad], want[~bad])
+    assert not got[bad].isfinite().any()  # (gelu(-inf) is NaN)
+
+
 @pytest.mark.parametrize("M", [4, 30, 50, 150])
 def test_linear_lora_not_finite(dev, M):  # noqa: F811
     """Infinite and NaN operands give each output the class of the definition's sums."""
