@@ -10,6 +10,7 @@
 #pragma once
 
 #include "rms_norm.hpp"
+#include "wave_ops.hpp"
 
 namespace mmk {
 
@@ -39,6 +40,33 @@ struct LayerNormGradParams {
   int64_t rows;
   int hidden;
 };
+
+// Sums over a workgroup, the same in every thread: the waves' parts meet in LDS and are
+// added in wave order.  `slot` holds one value per wave and is not reused within a row.
+__device__ __forceinline__ float row_block_sum(float v, float* slot) {
+  v = wave_sum(v);
+  const int waves = blockDim.x >> 6;
+  if (waves == 1) return v;
+  if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = 0.f;
+  for (int w = 0; w < waves; ++w) v += slot[w];
+  return v;
+}
+// Two at once.
+__device__ __forceinline__ float2 row_block_sum(float2 v, float2* slot) {
+  v = float2{wave_sum(v.x), wave_sum(v.y)};
+  const int waves = blockDim.x >> 6;
+  if (waves == 1) return v;
+  if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = float2{0.f, 0.f};
+  for (int w = 0; w < waves; ++w) {
+    v.x += slot[w].x;
+    v.y += slot[w].y;
+  }
+  return v;
+}
 
 // One row per workgroup; thread t holds vectors t, t + T, ... (VPT of them)
 // of 8 values.
@@ -72,7 +100,7 @@ __global__ void __launch_bounds__(1024) layer_norm(LayerNormParams p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum += v[i][j];
   }
-  const float mean = block_sum(sum, slot[0]) / (float)p.hidden;
+  const float mean = row_block_sum(sum, slot[0]) / (float)p.hidden;
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -83,7 +111,7 @@ __global__ void __launch_bounds__(1024) layer_norm(LayerNormParams p) {
       ss = __builtin_fmaf(v[i][j], v[i][j], ss);
     }
   }
-  const float rstd = rsqrtf(block_sum(ss, slot[1]) / (float)p.hidden + p.eps);
+  const float rstd = rsqrtf(row_block_sum(ss, slot[1]) / (float)p.hidden + p.eps);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = threadIdx.x + i * T;
@@ -104,25 +132,6 @@ __global__ void __launch_bounds__(1024) layer_norm(LayerNormParams p) {
     p.mean[row] = mean;
     p.rstd[row] = rstd;
   }
-}
-
-// Two sums over a workgroup at once, as block_sum.
-__device__ __forceinline__ float2 block_sum2(float2 v, float2* slot) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    v.x += __shfl_xor(v.x, d);
-    v.y += __shfl_xor(v.y, d);
-  }
-  const int waves = blockDim.x >> 6;
-  if (waves == 1) return v;
-  if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = float2{0.f, 0.f};
-  for (int w = 0; w < waves; ++w) {
-    v.x += slot[w].x;
-    v.y += slot[w].y;
-  }
-  return v;
 }
 
 // The gradient.  With n = (h - m) r and g = dy w:
@@ -197,7 +206,7 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) layer_norm_grad(LayerNormG
     }
     // two slot rows in turn: a wave may start the next row's sum while
     // another still reads this one's
-    dot = block_sum2(dot, slot[turn]);
+    dot = row_block_sum(dot, slot[turn]);
     const float a = dot.x * inv_n, b = dot.y * inv_n;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -249,15 +258,20 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) layer_norm_grad(LayerNormG
   }
 }
 
-// The gradient of few rows in one launch: the first workgroups sum 8 LANES columns
+// Vectors of 8 columns that a workgroup of the kernel below sums side by side.  Measured (us,
+// 2 / 4 / 8): 2048 x 1024 bf16 12.9 / 12.9 / -, 300 x 4096 bf16 8.0 / 4.7 / 4.6, 2048 x 128
+// bf16 7.1 / 6.6 / -, 2048 x 8192 bf16 61.6 / 38.9 / 28.8, 2048 x 5000 fp32 - / 37.8 / 36.0,
+// 2048 x 16384 bf16 - / 85 / 66.
+__host__ __device__ constexpr int grad_few_lanes(int vpt) { return vpt == 1 ? 4 : 8; }
+
+// The gradient of few rows in one launch: the first workgroups sum 8 `lanes` columns
 // of dw and db each, reading dy and h for it once more, the others take one row
-// each, as above.  T / LANES interleaved runs of rows per column: narrow rows
-// take few lanes, so that enough workgroups sum columns.
+// each, as above.  T / lanes interleaved runs of rows per column.
 template <bool F32, int VPT>
-__global__ void __launch_bounds__(1024) layer_norm_grad_few(LayerNormGradParams p, float* dweight, float* dbias,
-                                                            int lanes) {
+__global__ void __launch_bounds__(1024) layer_norm_grad_few(LayerNormGradParams p, float* dweight, float* dbias) {
+  constexpr int lanes = grad_few_lanes(VPT);
   __shared__ float2 slot[16];
-  __shared__ float sums[2][16][64];
+  __shared__ float sums[2][64][8 * lanes];
   const int T = blockDim.x;
   const int vectors = p.hidden >> 3;
   const int wide = (vectors + lanes - 1) / lanes;  // workgroups of columns
@@ -282,20 +296,18 @@ __global__ void __launch_bounds__(1024) layer_norm_grad_few(LayerNormGradParams 
         }
       }
     }
-    // the runs of a wave, then the waves, in a fixed order
+    // the runs of 16 lanes, then those sums, in a fixed order
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      for (int d = 32; d >= lanes; d >>= 1) {
-        dw[j] += __shfl_xor(dw[j], d);
-        db[j] += __shfl_xor(db[j], d);
-      }
+      dw[j] = row_sum<lanes>(dw[j]);
+      db[j] = row_sum<lanes>(db[j]);
     }
-    const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
+    const int part = threadIdx.x >> 4, l = threadIdx.x & 15;
     if (l < lanes) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        sums[0][wave][8 * l + j] = dw[j];
-        sums[1][wave][8 * l + j] = db[j];
+        sums[0][part][8 * l + j] = dw[j];
+        sums[1][part][8 * l + j] = db[j];
       }
     }
     __syncthreads();
@@ -303,7 +315,8 @@ __global__ void __launch_bounds__(1024) layer_norm_grad_few(LayerNormGradParams 
     const int col = blockIdx.x * 8 * lanes + at;
     if (what < 2 && at < 8 * lanes && col < p.hidden) {
       float s = 0.f;
-      for (int q = 0; q < (T >> 6); ++q) s += sums[what][q][at];
+#pragma unroll 8
+      for (int q = 0; q < (T >> 4); ++q) s += sums[what][q][at];
       (what ? dbias : dweight)[col] = s;
     }
     return;
@@ -335,7 +348,7 @@ __global__ void __launch_bounds__(1024) layer_norm_grad_few(LayerNormGradParams 
       dot.y = __builtin_fmaf(g, (h[i][j] - m) * r, dot.y);
     }
   }
-  dot = block_sum2(dot, slot);
+  dot = row_block_sum(dot, slot);
   const float a = dot.x * (1.0f / (float)p.hidden), b = dot.y * (1.0f / (float)p.hidden);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {

@@ -172,44 +172,47 @@ __global__ void __launch_bounds__(kLoraShrinkWaves * 64) lora_shrink(LoraParams 
   });
 }
 
-// v of row m (adapter a), ranks r .. r + 7: the slices added in order, the scale, two parts.
-__device__ __forceinline__ void lora_v(const LoraParams& p, int m, int a, int r, u32x4* hi, u32x4* lo) {
-  f32x4 v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-  const float* at = p.low + (int64_t)m * p.R + r;
-#pragma unroll 4
-  for (int s = 0; s < p.low_slices; ++s, at += (int64_t)p.M * p.R) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const f32x4 u = *reinterpret_cast<const f32x4*>(at + 4 * h);
-#pragma unroll
-      for (int f = 0; f < 4; ++f) v[h][f] += u[f];
+// v of every row, 8 ranks (a chunk) to 16 threads: each loads the sums of one slice, and their sum
+// times the scale goes as two parts to put(row, chunk, high, low).  Rows without an
+// adapter are left out.
+template <typename F>
+__device__ __forceinline__ void lora_fold_all(const LoraParams& p, int64_t thread, int64_t threads, F put) {
+  const int chunks = p.R >> 3, s = (int)(thread & 15);
+  for (int64_t i = thread; i < (int64_t)p.M * chunks * 16; i += threads) {
+    const int m = (int)((i >> 4) / chunks), c = (int)((i >> 4) - (int64_t)m * chunks);
+    const int a = lora_adapter(p, m);
+    f32x4 v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    if (s < p.low_slices) {
+      const float* at = p.low + ((int64_t)s * p.M + m) * p.R + 8 * c;
+      v[0] = *reinterpret_cast<const f32x4*>(at);
+      v[1] = *reinterpret_cast<const f32x4*>(at + 4);
     }
-  }
-  const float scale = p.scale[a];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint16_t h[2], l[2];
-    split_bf16(v[j >> 1][2 * (j & 1)] * scale, &h[0], &l[0]);
-    split_bf16(v[j >> 1][2 * (j & 1) + 1] * scale, &h[1], &l[1]);
-    (*hi)[j] = (uint32_t)h[0] | (uint32_t)h[1] << 16;
-    (*lo)[j] = (uint32_t)l[0] | (uint32_t)l[1] << 16;
+    for (int d = 1; d < 16; d <<= 1)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j >> 2][j & 3] += __shfl_xor(v[j >> 2][j & 3], d);
+    if (a < 0 || s > 0) continue;
+    const float scale = p.scale[a];
+    u32x4 hi, lo;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint16_t h[2], l[2];
+      split_bf16(v[j >> 1][2 * (j & 1)] * scale, &h[0], &l[0]);
+      split_bf16(v[j >> 1][2 * (j & 1) + 1] * scale, &h[1], &l[1]);
+      hi[j] = (uint32_t)h[0] | (uint32_t)h[1] << 16;
+      lo[j] = (uint32_t)l[0] | (uint32_t)l[1] << 16;
+    }
+    put(m, c, hi, lo);
   }
 }
-
-// v of every row, 8 ranks per thread; rows without an adapter are left out.
 __device__ __forceinline__ void lora_fold_all(const LoraParams& p, int64_t thread, int64_t threads) {
-  const int chunks = p.R >> 3;
-  for (int64_t i = thread; i < (int64_t)p.M * chunks; i += threads) {
-    const int m = (int)(i / chunks), r = 8 * (int)(i - (int64_t)m * chunks);
-    const int a = lora_adapter(p, m);
-    if (a < 0) continue;
-    u32x4 hi, lo;
-    lora_v(p, m, a, r, &hi, &lo);
-    uint16_t* v = p.v + (int64_t)m * 2 * p.R + r;
+  lora_fold_all(p, thread, threads, [&](int m, int c, u32x4 hi, u32x4 lo) {
+    uint16_t* v = p.v + (int64_t)m * 2 * p.R + 8 * c;
     *reinterpret_cast<u32x4*>(v) = hi;
     *reinterpret_cast<u32x4*>(v + p.R) = lo;
-  }
+  });
 }
+
 // v of every row, and the adapters of every tile of `bm` rows (0: not needed), which the first
 // workgroups find.
 __global__ void __launch_bounds__(256) lora_fold(LoraParams p, LoraTileRows* tiles, int bm) {
@@ -313,12 +316,10 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
       }
       ++turn;
     });
-    const int chunks = p.R >> 3;
-    for (int i = threadIdx.x; i < p.M * chunks; i += kLoraWaves * 64) {
-      const int m = i / chunks, c = i - m * chunks, a = lora_adapter(p, m);
-      if (a >= 0) lora_v(p, m, a, 8 * c, &v[m][0][c], &v[m][1][c]);
-    }
-    __syncthreads();
+    lora_fold_all(p, threadIdx.x, kLoraWaves * 64, [&](int m, int c, u32x4 hi, u32x4 lo) {
+      v[m][0][c] = hi;
+      v[m][1][c] = lo;
+    });
   } else {
     lora_fold_all(p, (int64_t)(blockIdx.y * gridDim.x + blockIdx.x) * (kLoraWaves * 64) + threadIdx.x,
                   (int64_t)gridDim.x * gridDim.y * (kLoraWaves * 64));
@@ -341,6 +342,7 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
 #pragma unroll
         for (int b = 0; b < MB; ++b) acc[b] = mfma_bf16(x[b][i][j], t[i & 1].w[j], acc[b]);
     }
+    if (FINISH && round == 0) __syncthreads();  // (v is there)
 #pragma unroll
     for (int q = 0; q < MB; ++q) {
       if (!FINISH || mine[q] < 0) continue;
@@ -472,6 +474,96 @@ __global__ void __launch_bounds__(256) lora_join(LoraParams p) {
 #pragma unroll
       for (int f = 0; f < 8; ++f)
         if (n + f < p.N) o[f] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[f]));
+    }
+  }
+}
+
+// The same for 16 MB rows by 64 columns of decode rows, which may have as many adapters as there
+// are rows: the eight waves share these, and meet in LDS, where each finishes some
+// blocks of 16 by 16.
+template <int MB>
+__global__ void __launch_bounds__(512) lora_join_few(LoraParams p) {
+  __shared__ f32x4 red[8][MB * 4][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lx = lane & 15, lg = lane >> 4;
+  const int m0 = blockIdx.y * (16 * MB), n0 = blockIdx.x * 64;
+  f32x4 acc[MB][4];
+#pragma unroll
+  for (int b = 0; b < MB; ++b)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[b][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+  int turn = 0;
+  each_adapter(lane < 16 * MB ? lora_adapter(p, m0 + lane) : -1, [&](int a, uint64_t same) {
+    if ((turn++ & 7) != wave) return;
+#pragma unroll 2
+    for (int r0 = 0; r0 < p.R; r0 += 32) {
+      const int r = r0 + 8 * lg;
+      u32x4 wf[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int row = min(n0 + 32 * (q >> 1) + 8 * (lx >> 2) + 4 * (q & 1) + (lx & 3), p.N - 1);
+        wf[q] = u32x4{0u, 0u, 0u, 0u};
+        if (r < p.R) wf[q] = *reinterpret_cast<const u32x4*>(p.B + ((int64_t)a * p.N + row) * p.R + r);
+      }
+#pragma unroll
+      for (int b = 0; b < MB; ++b) {
+        if (!((same >> (16 * b)) & 0xffff)) continue;
+        const bool mine = (same >> (16 * b + lx)) & 1;
+        u32x4 hi = {0u, 0u, 0u, 0u}, lo = {0u, 0u, 0u, 0u};
+        if (r < p.R && mine) {
+          const uint16_t* v = p.v + (int64_t)(m0 + 16 * b + lx) * 2 * p.R + r;
+          hi = *reinterpret_cast<const u32x4*>(v);
+          lo = *reinterpret_cast<const u32x4*>(v + p.R);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          f32x4 d = mfma_bf16(wf[q], hi, f32x4{0.f, 0.f, 0.f, 0.f});
+          d = mfma_bf16(wf[q], lo, d);
+#pragma unroll
+          for (int f = 0; f < 4; ++f) acc[b][q][f] += mine ? d[f] : 0.f;
+        }
+      }
+    }
+  });
+#pragma unroll
+  for (int b = 0; b < MB; ++b)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) red[wave][4 * b + q][lane] = acc[b][q];
+  __syncthreads();
+  for (int i = wave; i < 4 * MB; i += 8) {
+    // columns 32 (q / 2) + 8 lg + 4 (q % 2) + 0..3 of a lane
+    const int q = i & 3, m = m0 + 16 * (i >> 2) + lx, n = n0 + 32 * (q >> 1) + 8 * lg + 4 * (q & 1);
+    if (m >= p.M) continue;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    const float* at = p.acc + (int64_t)m * p.N;
+    for (int s = 0; s < p.slices; ++s, at += (int64_t)p.M * p.N) {
+      f32x4 u;
+      if (n + 4 <= p.N) {
+        __builtin_memcpy(&u, at + n, 16);
+      } else {
+#pragma unroll
+        for (int f = 0; f < 4; ++f) u[f] = at[min(n + f, p.N - 1)];
+      }
+#pragma unroll
+      for (int f = 0; f < 4; ++f) sum[f] += u[f];
+    }
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      const f32x4 u = red[w][i][lane];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) sum[f] += u[f];
+    }
+    uint16_t o[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) o[f] = decoder_epilogue(sum[f], p.bias, p.epi, min(n + f, p.N - 1));
+    uint16_t* to = p.out + (int64_t)m * p.N + n;
+    if (n + 4 <= p.N) {
+      __builtin_memcpy(to, o, 8);
+    } else {
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+        if (n + f < p.N) to[f] = o[f];
     }
   }
 }

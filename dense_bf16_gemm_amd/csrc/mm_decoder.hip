@@ -372,7 +372,9 @@ const void* layer_norm_grad_few_kernel(int vpt) {
                     : fn(&mmk::layer_norm_grad_few<F32, 4>);
 }
 
-// Rows whose gradient is one launch (as of the RMS norm).
+// Rows whose gradient is one launch, as of the RMS norm.  Measured (us, one launch / two,
+// bf16): 256 x 4096 4.5 / 12.3, 1024 x 4096 11.9 / 18.5, 2048 x 1024 12.9 / 16.4, 2048 x 4096
+// 20.1 / 21.3, 2048 x 8192 28.8 / 37.1, 4096 x 4096 37.2 / 31.6.
 bool layer_norm_few(int64_t rows, int64_t hidden) { return rows <= kFewRows || hidden > kLongRow; }
 
 // ----------------------------------------------------------------------------
@@ -488,11 +490,16 @@ const void* moe_route_kernel(int64_t E) {
                     : fn(&mmk::moe_route<8>);
 }
 const void* moe_gate_up_kernel(int64_t E) {
-  return E <= 64    ? fn(&mmk::moe_gate_up<1, 1>)
-         : E <= 128 ? fn(&mmk::moe_gate_up<2, 1>)
-         : E <= 256 ? fn(&mmk::moe_gate_up<4, 1>)
-                    : fn(&mmk::moe_gate_up<8, 1>);
+  return E <= 64    ? fn(&mmk::moe_gate_up<1>)
+         : E <= 128 ? fn(&mmk::moe_gate_up<2>)
+         : E <= 256 ? fn(&mmk::moe_gate_up<4>)
+                    : fn(&mmk::moe_gate_up<8>);
 }
+
+// Blocks of 16 tokens to a group there: two where an expert has 12 on the average and the
+// registers hold two.  Measured (us a call, one / two): 64 tokens, 2 of 8 experts of 4096 x 4096
+// 232 / 188, 32, 8 of 20 of 4040 x 3144 404 / 377, 64, 1 of 8 of 4096 x 4096 171 / 180.
+int moe_group_blocks(int64_t T, int64_t E, int64_t H, int64_t k) { return T * k >= 12 * E && H <= 4096 ? 2 : 1; }
 
 // Workgroups that share 16 columns of the second layer: the number that spreads the
 // columns' workgroups most evenly over the CUs, a further one for a twentieth.
@@ -507,22 +514,55 @@ int64_t moe_splits(int64_t H) {
   return best;
 }
 
-// Blocks of 16 tokens to a group: two where an expert has 16 on the average.  Measured (us
-// a call, one / two): 64 tokens, 2 of 8 experts of 4096 x 4096 302 / 288, 1 of 8 200 / 217,
-// 6 of 32 of 2048 x 4096 456 / 486.
-int moe_group_blocks(int64_t T, int64_t E, int64_t k) { return T > 16 && T * k >= 16 * E ? 2 : 1; }
+// Whether experts of several tokens go to the kernels that hold the tokens' rows.  Measured
+// (us a call, without / with): 61 tokens, 4 of 60 experts of 2056 x 1416 276 / 256, 40, 8 of
+// 64 of 2048 x 1408 273 / 265, 64, 6 of 32 of 4096 x 2048 457 / 350, 64, 2 of 8 of 4096 x 4096
+// 304 / 188; but 16, 8 of 128 of 4096 x 1536 608 / 650, and 20, 4 of 60 of 1024 x 512 52 / 68.
+bool moe_many(int64_t T, int64_t E, int64_t H, int64_t I, int64_t k) {
+  return T > mmk::kMoeFew && T * k >= 4 * E && H <= 8192 && H * I >= (int64_t(1) << 21);
+}
 
 struct MoePlan {
-  int64_t splits, mid, part;  // (the last two: workspace bytes, after the tables)
+  bool many = false;
+  int gb = 1;  // blocks of 16 tokens to a group
+  int up_spw = 0, down_spw = 0;  // steps per wave
+  int64_t splits = 1, slices = 1;
+  int64_t mid = 0, part = 0;  // workspace bytes, after the tables
   int64_t bytes() const { return kMoeTableBytes + mid + part; }
 };
 
-MoePlan moe_plan(int64_t T, int64_t H, int64_t I, int64_t k) {
+int moe_steps(int64_t n, int most) {
+  int spw = 2;
+  while (spw < most && mmk::kMoeManyWaves * 64 * spw < n) spw *= 2;
+  return spw;
+}
+
+MoePlan moe_plan(int64_t T, int64_t E, int64_t H, int64_t I, int64_t k) {
   MoePlan p;
-  p.splits = H > 0 ? moe_splits(H) : 1;
   p.mid = round256(T * k * I * 4);
-  p.part = p.splits > 1 ? round256(p.splits * T * H * 4) : 0;
+  p.many = moe_many(T, E, H, I, k);
+  if (p.many) {
+    p.gb = moe_group_blocks(T, E, H, k);
+    p.up_spw = moe_steps(H, 8 / p.gb);
+    p.down_spw = moe_steps(I, 4 / p.gb);
+    p.slices = cdiv(I, mmk::kMoeManyWaves * 64 * p.down_spw);
+    p.part = round256(p.slices * T * k * H * 4);
+  } else {
+    p.splits = H > 0 ? moe_splits(H) : 1;
+    p.part = p.splits > 1 ? round256(p.splits * T * H * 4) : 0;
+  }
   return p;
+}
+
+const void* moe_gate_up_many_kernel(int gb, int spw) {
+  if (gb == 2) return spw == 2 ? fn(&mmk::moe_gate_up_many<2, 2>) : fn(&mmk::moe_gate_up_many<2, 4>);
+  return spw == 2   ? fn(&mmk::moe_gate_up_many<1, 2>)
+         : spw == 4 ? fn(&mmk::moe_gate_up_many<1, 4>)
+                    : fn(&mmk::moe_gate_up_many<1, 8>);
+}
+const void* moe_down_many_kernel(int gb, int spw) {
+  if (gb == 2) return fn(&mmk::moe_down_many<2, 2>);
+  return spw == 2 ? fn(&mmk::moe_down_many<1, 2>) : fn(&mmk::moe_down_many<1, 4>);
 }
 
 }  // namespace
@@ -906,11 +946,10 @@ mm_status mm_layer_norm_backward(const void* dy, const void* h, const void* weig
     norm_shape(hidden, 512, &threads, &vpt);
     if (few) {
       threads = std::max(threads, 512);  // (for the columns' sums)
-      int lanes = 8;
-      while (lanes > 1 && cdiv(hidden, 8 * lanes) < 128) lanes /= 2;
-      void* args[] = {&p, &dweight, &dbias, &lanes};
+      void* args[] = {&p, &dweight, &dbias};
       return launch(stream_dtype == MM_OUT_F32 ? layer_norm_grad_few_kernel<true>(vpt) : layer_norm_grad_few_kernel<false>(vpt),
-                    dim3((unsigned)(rows + cdiv(hidden, 8 * lanes))), threads, args, stream, "layer_norm gradient");
+                    dim3((unsigned)(rows + cdiv(hidden, 8 * mmk::grad_few_lanes(vpt)))), threads, args, stream,
+                    "layer_norm gradient");
     }
     if (vpt == 4) norm_shape(hidden, 1024, &threads, &vpt);
     void* args[] = {&p};
@@ -1004,6 +1043,14 @@ mm_status mm_linear_lora(const void* x, const void* W, const void* A, const void
     s = launch(k, dim3((unsigned)cdiv(blocks, each), (unsigned)plan.slices),
                mmk::kLoraWaves * 64, args, stream, "linear_lora rows");
     if (s != MM_OK || plan.finish) return s;
+    // All rows to a workgroup where the columns' workgroups are enough, which reads B
+    // once: 64 x 14336, rank 64, 8 adapters 10.4 us (12.8 in blocks of 16 rows), but 49 x 1473
+    // 9.1 us (4.6).
+    const int jb = N >= 8192 ? plan.mb : 1;
+    return launch(jb == 1   ? fn(&mmk::lora_join_few<1>)
+                  : jb == 2 ? fn(&mmk::lora_join_few<2>)
+                            : fn(&mmk::lora_join_few<4>),
+                  dim3((unsigned)cdiv(N, 64), (unsigned)cdiv(M, 16 * jb)), 512, args, stream, "linear_lora join");
   } else {
     const Q8Plan& t = plan.tiles;
     const bool split = t.chunks > 1;
@@ -1016,7 +1063,7 @@ mm_status mm_linear_lora(const void* x, const void* W, const void* A, const void
     int bm = split ? 0 : 64 * kQ8Kinds[t.kind].fm;
     void* fold_args[] = {&p, &rows, &bm};
     s = launch(fn(&mmk::lora_fold),
-               dim3((unsigned)((split ? 0 : t.tiles_m) + std::min<int64_t>(cdiv(M * rank / 8, 256), 1024))), 256, fold_args,
+               dim3((unsigned)((split ? 0 : t.tiles_m) + std::min<int64_t>(cdiv(M * rank * 2, 256), 1024))), 256, fold_args,
                stream, "linear_lora fold");
     if (s != MM_OK) return s;
     int cus = 0;
@@ -1036,7 +1083,7 @@ mm_status mm_moe_ffn_workspace_size(int64_t tokens, int64_t experts, int64_t H, 
   *bytes = 0;
   const mm_status s = check_moe(tokens, experts, H, I, top_k);
   if (s != MM_OK || tokens == 0) return s;
-  *bytes = moe_plan(tokens, H, I, top_k).bytes();
+  *bytes = moe_plan(tokens, experts, H, I, top_k).bytes();
   return MM_OK;
 }
 
@@ -1059,7 +1106,7 @@ mm_status mm_moe_ffn(const void* x, const float* logits, const void* W_gate, con
                      {W_down, E * I * H * 2}};
   const Span outs[] = {{out, T * H * 2}, {experts, T * top_k * 4}, {weights, T * top_k * 4}, {workspace, workspace_bytes}};
   if (any_overlap(in, outs)) return fail(MM_ERR_INVALID_VALUE, "an output or the workspace overlaps an input or another output");
-  const MoePlan plan = moe_plan(T, H, I, top_k);
+  const MoePlan plan = moe_plan(T, E, H, I, top_k);
   if (!workspace || workspace_bytes < plan.bytes())
     return fail(MM_ERR_INVALID_VALUE, "workspace smaller than mm_moe_ffn_workspace_size reports");
   if (!aligned(workspace, 256)) return fail(MM_ERR_MISALIGNED, "workspace must be 256-byte aligned");
@@ -1083,26 +1130,33 @@ mm_status mm_moe_ffn(const void* x, const float* logits, const void* W_gate, con
   p.k = (int)top_k;
   p.renormalize = renormalize != 0;
   p.splits = (int)plan.splits;
+  p.slices = (int)plan.slices;
   void* args[] = {&p};
   // Few tokens: every workgroup of the first layer finds their experts itself.
   const int64_t units = T * top_k * (I / 8);  // (at most: a group for every choice)
   const bool own = T <= mmk::kMoeFew && units > 0 && H > 0;
-  const int gb = moe_group_blocks(T, E, top_k);
-  int group = 16 * gb;
+  int group = 16 * plan.gb;
   void* route_args[] = {&p, &group};
   if (!own && (s = launch(moe_route_kernel(E), dim3(1), 1024, route_args, stream, "moe_ffn route")) != MM_OK) return s;
   if (H == 0) return MM_OK;
   int cus = 0;
   if ((s = device_cus(&cus)) != MM_OK) return s;
+  if (plan.many && units > 0) {
+    s = launch(moe_gate_up_many_kernel(plan.gb, plan.up_spw), dim3((unsigned)cus), mmk::kMoeManyWaves * 64, args, stream,
+               "moe_ffn gate and up");
+    if (s != MM_OK) return s;
+    s = launch(moe_down_many_kernel(plan.gb, plan.down_spw), dim3((unsigned)cus), mmk::kMoeManyWaves * 64, args, stream,
+               "moe_ffn down");
+    if (s != MM_OK) return s;
+    return launch(fn(&mmk::moe_combine), dim3((unsigned)cdiv(H, 1024), (unsigned)T), 256, args, stream, "moe_ffn combine");
+  }
   if (units > 0) {
-    s = launch(own ? moe_gate_up_kernel(E) : gb == 1 ? fn(&mmk::moe_gate_up<0, 1>) : fn(&mmk::moe_gate_up<0, 2>),
+    s = launch(own ? moe_gate_up_kernel(E) : fn(&mmk::moe_gate_up<0>),
                dim3((unsigned)std::min<int64_t>(units, 4 * (int64_t)cus)), mmk::kMoeWaves * 64, args, stream,
                "moe_ffn gate and up");
     if (s != MM_OK) return s;
   }
-  s = launch(T <= 16   ? fn(&mmk::moe_down<1, 1>)
-             : gb == 1 ? fn(&mmk::moe_down<4, 1>)
-                       : fn(&mmk::moe_down<4, 2>),
+  s = launch(T <= 16 ? fn(&mmk::moe_down<1>) : fn(&mmk::moe_down<4>),
              dim3((unsigned)cdiv(H, 16), (unsigned)plan.splits), mmk::kMoeWaves * 64, args, stream, "moe_ffn down");
   if (s != MM_OK || plan.splits == 1) return s;
   return launch(fn(&mmk::moe_join), dim3((unsigned)cdiv(T * H, 1024)), 256, args, stream, "moe_ffn join");

@@ -14,6 +14,7 @@
 #pragma once
 
 #include "gemm_q8.hpp"
+#include "wave_ops.hpp"
 
 namespace mmk {
 
@@ -30,6 +31,7 @@ struct MoeGroups {
   int act[N], start[N], rows[N];
   int tok[N];
   float wt[N];
+  int row[N];  // of choice t k + j, -1 for none
 };
 typedef MoeGroups<kMoeTokens * kMoeTopK> MoeTables;
 
@@ -44,10 +46,10 @@ struct MoeParams {
   float* weights;         // [T][k]
   MoeTables* tab;
   uint16_t* mid;          // [T k][2][I]: high and low parts of the intermediate
-  float* part;            // [splits][T][H]: parts of the output
+  float* part;            // parts of the output: [splits][T][H], or [slices][T k][H] of each row's
   int T, E, H, I, k;
   int renormalize;
-  int splits;
+  int splits, slices;
 };
 
 // Floats as unsigned numbers of the same order; NaN above all, both zeros alike,
@@ -105,9 +107,7 @@ __device__ __forceinline__ void moe_choose(const MoeParams& p, MoeGroups<N>* tab
       for (int r = 1; r < VPL; ++r) m[i] = max(m[i], key[i][r]);
     }
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1)
-#pragma unroll
-      for (int i = 0; i < TPW; ++i) m[i] = max(m[i], (uint32_t)__shfl_xor((int)m[i], d));
+    for (int i = 0; i < TPW; ++i) m[i] = wave_max(m[i]);
 #pragma unroll
     for (int i = 0; i < TPW; ++i) {
       if (m[i] == 0u) continue;  // (none is left)
@@ -140,8 +140,7 @@ __device__ __forceinline__ void moe_choose(const MoeParams& p, MoeGroups<N>* tab
 #pragma unroll
       for (int r = 0; r < VPL; ++r) sum += all[i][r] ? expf(key_value(all[i][r]) - peak) : 0.f;
     }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+    sum = wave_sum(sum);
     if (lane < p.k) {
       const int s = t * p.k + lane;
       const float w = mine[i] ? part / sum : 0.f;
@@ -190,11 +189,15 @@ __device__ __forceinline__ void moe_choose(const MoeParams& p, MoeGroups<N>* tab
   __syncthreads();
   for (int s = threadIdx.x; s < p.T * p.k; s += NW * 64) {
     const int x = id[s], t = s / p.k;
-    if (x < 0) continue;
+    if (x < 0) {
+      tab->row[s] = -1;
+      continue;
+    }
     const uint32_t lo = mask[x][0], hi = mask[x][1];
     const int before = t < 32 ? __popc(lo & ((1u << t) - 1u)) : __popc(lo) + __popc(hi & ((1u << (t - 32)) - 1u));
     tab->tok[first[x] + before] = t;
     tab->wt[first[x] + before] = share[s];
+    tab->row[s] = first[x] + before;
   }
 }
 
@@ -228,12 +231,12 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 // A unit of work: 8 columns of I of one group, gate and up rows together as the 16
 // columns of an MFMA block.  The eight waves take every eighth step of 64 k, each
 // step's loads one step ahead, and meet in LDS, added in wave order.  Of an expert with
-// more tokens than a group takes (16 GB) the weights are read again for each group.
+// more tokens than a group of 16 takes the weights are read again for each group.
 // VPL > 0: up to eight tokens, each workgroup chooses their experts itself.
-template <int VPL, int GB>
+template <int VPL>
 __global__ void __launch_bounds__(kMoeWaves * 64) moe_gate_up(MoeParams p) {
   constexpr bool kOwn = VPL > 0;
-  __shared__ float red[kMoeWaves][GB][64][4];
+  __shared__ float red[kMoeWaves][64][4];
   __shared__ MoeGroups<kOwn ? kMoeFew * kMoeTopK : 1> own;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -273,7 +276,7 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_gate_up(MoeParams p) {
     tail[j] = out[j] ? 0x80000000u : 0u;
   }
   struct Step {
-    u32x4 w[2], x[GB][2];
+    u32x4 w[2], x[2];
   };
   for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int q = __builtin_amdgcn_readfirstlane(unit / cols), c0 = 8 * (unit - q * cols);
@@ -281,35 +284,24 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_gate_up(MoeParams p) {
     const int s = __builtin_amdgcn_readfirstlane(pick([&](auto& t) { return t.start[q]; }));
     const int n = __builtin_amdgcn_readfirstlane(pick([&](auto& t) { return t.rows[q]; }));
     const uint16_t* w = (lx < 8 ? p.wg : p.wu) + ((int64_t)e * p.I + c0 + (lx & 7)) * H + 8 * lg;
-    uint32_t xo[GB];
-#pragma unroll
-    for (int a = 0; a < GB; ++a) {
-      const int m = 16 * a + lx;
-      xo[a] = 0x80000000u;
-      if (m < n) xo[a] = (uint32_t)pick([&](auto& t) { return t.tok[s + m]; }) * (uint32_t)H * 2u + 16u * (uint32_t)lg;
-    }
+    uint32_t xo = 0x80000000u;
+    if (lx < n) xo = (uint32_t)pick([&](auto& t) { return t.tok[s + lx]; }) * (uint32_t)H * 2u + 16u * (uint32_t)lg;
     auto load = [&](int st, Step& t) __attribute__((always_inline)) {
       const bool last = st == steps - 1;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         t.w[j] = *reinterpret_cast<const u32x4*>(w + (last && out[j] ? -8 * lg : 64 * st + 32 * j));
-#pragma unroll
-        for (int a = 0; a < GB; ++a)
-          if (a == 0 || 16 * a < n) t.x[a][j] = load_chunk(rx, (xo[a] + 64u * j) | (last ? tail[j] : 0u), 128u * (uint32_t)st);
+        t.x[j] = load_chunk(rx, (xo + 64u * j) | (last ? tail[j] : 0u), 128u * (uint32_t)st);
       }
     };
-    f32x4 acc[GB];
-#pragma unroll
-    for (int a = 0; a < GB; ++a) acc[a] = f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     auto step = [&](int st, Step& t, Step& next) __attribute__((always_inline)) {
       load(min(st + kMoeWaves, steps - 1), next);
       const bool last = st == steps - 1;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if (last && out[j]) t.w[j] = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int a = 0; a < GB; ++a)
-          if (a == 0 || 16 * a < n) acc[a] = mfma_bf16(t.x[a][j], t.w[j], acc[a]);
+        acc = mfma_bf16(t.x[j], t.w[j], acc);
       }
     };
     if (wave < steps) {
@@ -321,17 +313,16 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_gate_up(MoeParams p) {
       }
     }
     __syncthreads();  // (the unit before has been read)
-#pragma unroll
-    for (int a = 0; a < GB; ++a) *reinterpret_cast<f32x4*>(red[wave][a][lane]) = acc[a];
+    *reinterpret_cast<f32x4*>(red[wave][lane]) = acc;
     __syncthreads();
     const int m = threadIdx.x >> 3, c = threadIdx.x & 7;
     if (m < n) {
-      const int a = m >> 4, l = 16 * ((m >> 2) & 3) + c, f = m & 3;
+      const int l = 16 * (m >> 2) + c, f = m & 3;
       float g = 0.f, u = 0.f;
 #pragma unroll
       for (int v = 0; v < kMoeWaves; ++v) {
-        g += red[v][a][l][f];
-        u += red[v][a][l + 8][f];
+        g += red[v][l][f];
+        u += red[v][l + 8][f];
       }
       uint16_t hi, lo;
       split_bf16(pick([&](auto& t) { return t.wt[s + m]; }) * swiglu(g, u), &hi, &lo);
@@ -349,8 +340,8 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_gate_up(MoeParams p) {
 // adds their parts.  (The last workgroup to arrive could; but the fences that order
 // its reads after the others' writes took 230 us, since each writes back and
 // invalidates an XCD's L2.)
-// TB, GB: blocks of 16 tokens in all and in a group.
-template <int TB, int GB>
+// TB: blocks of 16 tokens.
+template <int TB>
 __global__ void __launch_bounds__(kMoeWaves * 64) moe_down(MoeParams p) {
   __shared__ float sums[kMoeWaves][16 * TB][16];
   const int lane = threadIdx.x & 63;
@@ -375,13 +366,13 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_down(MoeParams p) {
     tail[j] = out[j] ? 0x80000000u : 0u;
   }
   struct Step {
-    u32x4 w[2], x[GB][2][2];
+    u32x4 w[2], x[2][2];
   };
   // a group and a step of its I
   struct At {
     int q, st, s, n;
     const uint16_t* w;
-    uint32_t xo[GB];
+    uint32_t xo;
   };
   auto enter = [&](At& at, int q) __attribute__((always_inline)) {
     at.q = q;
@@ -389,9 +380,7 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_down(MoeParams p) {
     at.s = __builtin_amdgcn_readfirstlane(tab->start[q]);
     at.n = __builtin_amdgcn_readfirstlane(tab->rows[q]);
     at.w = p.wd + ((int64_t)e * p.H + row) * I + 8 * lg;
-#pragma unroll
-    for (int a = 0; a < GB; ++a)
-      at.xo[a] = 16 * a + lx < at.n ? (uint32_t)(at.s + 16 * a + lx) * (uint32_t)I * 4u + 16u * (uint32_t)lg : 0x80000000u;
+    at.xo = lx < at.n ? (uint32_t)(at.s + lx) * (uint32_t)I * 4u + 16u * (uint32_t)lg : 0x80000000u;
   };
   auto load = [&](const At& at, Step& t) __attribute__((always_inline)) {
     const bool last = at.st == steps - 1;
@@ -399,18 +388,11 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_down(MoeParams p) {
     for (int j = 0; j < 2; ++j) {
       t.w[j] = *reinterpret_cast<const u32x4*>(at.w + (last && out[j] ? -8 * lg : 64 * at.st + 32 * j));
 #pragma unroll
-      for (int a = 0; a < GB; ++a) {
-        if (a > 0 && 16 * a >= at.n) continue;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          t.x[a][j][h] =
-              load_chunk(rx, (at.xo[a] + 64u * j + (uint32_t)(2 * I) * h) | (last ? tail[j] : 0u), 128u * (uint32_t)at.st);
-      }
+      for (int h = 0; h < 2; ++h)
+        t.x[j][h] = load_chunk(rx, (at.xo + 64u * j + (uint32_t)(2 * I) * h) | (last ? tail[j] : 0u), 128u * (uint32_t)at.st);
     }
   };
-  f32x4 acc[GB];
-#pragma unroll
-  for (int a = 0; a < GB; ++a) acc[a] = f32x4{0.f, 0.f, 0.f, 0.f};
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   if (lo < hi) {
     At now, ahead;
     enter(now, lo / steps);
@@ -428,25 +410,18 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_down(MoeParams p) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if (last && out[j]) t.w[j] = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int a = 0; a < GB; ++a) {
-          if (a > 0 && 16 * a >= now.n) continue;
-          acc[a] = mfma_bf16(t.x[a][j][0], t.w[j], acc[a]);
-          acc[a] = mfma_bf16(t.x[a][j][1], t.w[j], acc[a]);
-        }
+        acc = mfma_bf16(t.x[j][0], t.w[j], acc);
+        acc = mfma_bf16(t.x[j][1], t.w[j], acc);
       }
     };
     auto leave = [&](int i) __attribute__((always_inline)) {
       if (now.st == steps - 1 || i == hi - 1) {
 #pragma unroll
-        for (int a = 0; a < GB; ++a) {
-#pragma unroll
-          for (int f = 0; f < 4; ++f) {
-            const int m = 16 * a + 4 * lg + f;
-            if (m < now.n) sums[wave][tab->tok[now.s + m]][lx] += acc[a][f];
-          }
-          acc[a] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int f = 0; f < 4; ++f) {
+          const int m = 4 * lg + f;
+          if (m < now.n) sums[wave][tab->tok[now.s + m]][lx] += acc[f];
         }
+        acc = f32x4{0.f, 0.f, 0.f, 0.f};
       }
       advance(now);
     };
@@ -495,6 +470,266 @@ __global__ void __launch_bounds__(256) moe_join(MoeParams p) {
   uint16_t* o = p.out + i;
   const uint32_t pk[2] = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
   __builtin_memcpy(o, pk, 8);
+}
+
+// ---- experts of several tokens -------------------------------------------------
+//
+// Read from L2 for every unit, the tokens' rows are as many bytes as the weights at 16
+// tokens to an expert (two times as many in the second layer), which halves the rate (64
+// tokens, 2 of 8 experts of 4096 x 4096: 2.8 TB/s of weights).  So here a workgroup of 16
+// waves takes a run of neighbouring units, and each wave holds its part of a group's
+// rows in registers until the group changes: the steps 16 i + w of 64 values, i < SPW.
+// Each step's weights are loaded one step ahead, across units; the waves' sums of a unit
+// meet in LDS (two sets in turn: one barrier per unit), and are added in wave order by
+// another wave for each unit.
+
+constexpr int kMoeManyWaves = 16;
+
+// A lane's piece j of step st of 64 values from a row at byte `row` of a buffer of rows of n values;
+// zeros past them, and past the last step.
+__device__ __forceinline__ u32x4 moe_chunk(__amdgpu_buffer_rsrc_t buf, uint32_t row, int st, int j, int n, int steps, int lg) {
+  const uint32_t off = 64 * st + 32 * j + 8 * lg < n ? row + 64u * j + 16u * (uint32_t)lg : 0x80000000u;
+  return load_chunk(buf, off, 128u * (uint32_t)min(st, steps - 1));
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t moe_rows(const uint16_t* base, int rows, int n) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), (short)0, rows * n * 2, 0x00020000);
+}
+
+// The first layer: a unit is 16 columns of I of one group, gate and up.
+template <int GB, int SPW>
+__global__ void __launch_bounds__(kMoeManyWaves * 64) moe_gate_up_many(MoeParams p) {
+  static_assert(SPW % 2 == 0 && GB * SPW <= 8, "x in 64 registers, two steps in turn");
+  __shared__ f32x4 red[2][kMoeManyWaves][2][GB][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lx = lane & 15, lg = lane >> 4;
+  const MoeTables* tab = p.tab;
+  const int H = p.H, steps = (H + 63) >> 6, cols = (p.I + 15) >> 4;
+  const int64_t units = (int64_t)__builtin_amdgcn_readfirstlane(tab->count) * cols;
+  const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
+  if (u0 >= u1) return;
+  struct Step {
+    u32x4 w[2][2];
+  };
+  // where the loads are: group, column block, and the two weights' rows there
+  int lq = u0 / cols, lc = u0 - lq * cols;
+  __amdgpu_buffer_rsrc_t rg, ru;
+  auto enter = [&]() __attribute__((always_inline)) {
+    const int64_t first = (int64_t)__builtin_amdgcn_readfirstlane(tab->act[lq]) * p.I + 16 * lc;
+    const int rows = min(16, p.I - 16 * lc);
+    rg = moe_rows(p.wg + first * H, rows, H);
+    ru = moe_rows(p.wu + first * H, rows, H);
+  };
+  uint32_t row = (uint32_t)lx * (uint32_t)H * 2u;
+  auto load = [&](int i, Step& t) __attribute__((always_inline)) {
+    asm volatile("" : "+v"(row));  // (opaque: the steps' offsets are not all kept in registers)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      t.w[0][j] = moe_chunk(rg, row, wave + kMoeManyWaves * i, j, H, steps, lg);
+      t.w[1][j] = moe_chunk(ru, row, wave + kMoeManyWaves * i, j, H, steps, lg);
+    }
+  };
+  Step t[2];
+  enter();
+  load(0, t[0]);
+  u32x4 x[GB][SPW][2];
+  int q = -1, c = lc, s = 0, n = 0;
+  for (int unit = u0; unit < u1; ++unit) {
+    if (q < 0 || c == cols) {  // the next group's rows
+      q = q < 0 ? lq : q + 1;
+      c = unit == u0 ? c : 0;
+      s = __builtin_amdgcn_readfirstlane(tab->start[q]);
+      n = __builtin_amdgcn_readfirstlane(tab->rows[q]);
+      const __amdgpu_buffer_rsrc_t rx = moe_rows(p.x, p.T, H);
+#pragma unroll
+      for (int a = 0; a < GB; ++a) {
+        uint32_t xo = 0x80000000u;
+        if (16 * a + lx < n) xo = (uint32_t)tab->tok[s + 16 * a + lx] * (uint32_t)H * 2u;
+#pragma unroll
+        for (int i = 0; i < SPW; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) x[a][i][j] = moe_chunk(rx, xo, wave + kMoeManyWaves * i, j, H, steps, lg);
+      }
+    }
+    f32x4 acc[2][GB];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int a = 0; a < GB; ++a) acc[h][a] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < SPW; ++i) {
+      if (i + 1 < SPW) {
+        load(i + 1, t[(i + 1) & 1]);
+      } else {
+        // (past the last unit, that one again, unused)
+        if (unit + 1 < u1 && ++lc == cols) {
+          lc = 0;
+          ++lq;
+        }
+        enter();
+        load(0, t[0]);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int a = 0; a < GB; ++a) acc[h][a] = mfma_bf16(x[a][i][j], t[i & 1].w[h][j], acc[h][a]);
+    }
+    auto set = red[(unit - u0) & 1];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int a = 0; a < GB; ++a) set[wave][h][a][lane] = acc[h][a];
+    __syncthreads();
+    const int c0 = 16 * c;
+    ++c;
+    const int a = (wave - (unit - u0) * GB) & (kMoeManyWaves - 1);
+    if (a >= GB || 16 * a >= n) continue;
+    f32x4 v[2] = {set[0][0][a][lane], set[0][1][a][lane]};
+#pragma unroll 3
+    for (int w = 1; w < kMoeManyWaves; ++w)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4 u = set[w][h][a][lane];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) v[h][f] += u[f];
+      }
+    if (c0 + lx >= p.I) continue;
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const int m = 16 * a + 4 * lg + f;
+      if (m >= n) continue;
+      uint16_t* o = p.mid + (int64_t)(s + m) * 2 * p.I + c0 + lx;
+      split_bf16(tab->wt[s + m] * swiglu(v[0][f], v[1][f]), o, o + p.I);
+    }
+  }
+}
+
+// The second layer: a unit is 16 columns of H of one group and slice of I (16 SPW steps), and
+// leaves its sums for each of the group's rows; moe_combine adds a token's.
+template <int GB, int SPW>
+__global__ void __launch_bounds__(kMoeManyWaves * 64) moe_down_many(MoeParams p) {
+  static_assert(SPW % 2 == 0 && GB * SPW <= 4, "x in 64 registers, two steps in turn");
+  __shared__ f32x4 red[2][kMoeManyWaves][GB][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lx = lane & 15, lg = lane >> 4;
+  const MoeTables* tab = p.tab;
+  const int I = p.I, steps = (I + 63) >> 6, cols = (p.H + 15) >> 4;
+  const int64_t units = (int64_t)__builtin_amdgcn_readfirstlane(tab->count) * p.slices * cols;
+  const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
+  if (u0 >= u1) return;
+  struct Step {
+    u32x4 w[2];
+  };
+  int lq = u0 / cols, lc = u0 - lq * cols;  // (lq, q: group and slice together)
+  __amdgpu_buffer_rsrc_t rw;
+  int lfirst = 0;
+  auto enter = [&]() __attribute__((always_inline)) {
+    const int g = lq / p.slices;
+    lfirst = (lq - g * p.slices) * (kMoeManyWaves * SPW) + wave;
+    const int64_t first = (int64_t)__builtin_amdgcn_readfirstlane(tab->act[g]) * p.H + 16 * lc;
+    rw = moe_rows(p.wd + first * I, min(16, p.H - 16 * lc), I);
+  };
+  uint32_t row = (uint32_t)lx * (uint32_t)I * 2u;
+  auto load = [&](int i, Step& t) __attribute__((always_inline)) {
+    asm volatile("" : "+v"(row));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) t.w[j] = moe_chunk(rw, row, lfirst + kMoeManyWaves * i, j, I, steps, lg);
+  };
+  Step t[2];
+  enter();
+  load(0, t[0]);
+  u32x4 x[GB][SPW][2][2];
+  int q = -1, c = lc, s = 0, n = 0, slice = 0;
+  for (int unit = u0; unit < u1; ++unit) {
+    if (q < 0 || c == cols) {
+      q = q < 0 ? lq : q + 1;
+      c = unit == u0 ? c : 0;
+      const int g = q / p.slices;
+      slice = q - g * p.slices;
+      s = __builtin_amdgcn_readfirstlane(tab->start[g]);
+      n = __builtin_amdgcn_readfirstlane(tab->rows[g]);
+      const __amdgpu_buffer_rsrc_t rx = moe_rows(p.mid + (int64_t)s * 2 * I, 2 * n, I);
+      const int first = slice * (kMoeManyWaves * SPW) + wave;
+#pragma unroll
+      for (int a = 0; a < GB; ++a) {
+        const uint32_t xo = 16 * a + lx < n ? (uint32_t)(16 * a + lx) * (uint32_t)I * 4u : 0x80000000u;
+#pragma unroll
+        for (int i = 0; i < SPW; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              x[a][i][j][h] = moe_chunk(rx, xo + (uint32_t)(2 * I) * h, first + kMoeManyWaves * i, j, I, steps, lg);
+      }
+    }
+    f32x4 acc[GB];
+#pragma unroll
+    for (int a = 0; a < GB; ++a) acc[a] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < SPW; ++i) {
+      if (i + 1 < SPW) {
+        load(i + 1, t[(i + 1) & 1]);
+      } else {
+        if (unit + 1 < u1 && ++lc == cols) {
+          lc = 0;
+          ++lq;
+        }
+        enter();
+        load(0, t[0]);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int a = 0; a < GB; ++a) {
+          acc[a] = mfma_bf16(x[a][i][j][0], t[i & 1].w[j], acc[a]);
+          acc[a] = mfma_bf16(x[a][i][j][1], t[i & 1].w[j], acc[a]);
+        }
+    }
+    auto set = red[(unit - u0) & 1];
+#pragma unroll
+    for (int a = 0; a < GB; ++a) set[wave][a][lane] = acc[a];
+    __syncthreads();
+    const int n0 = 16 * c;
+    ++c;
+    const int a = (wave - (unit - u0) * GB) & (kMoeManyWaves - 1);
+    if (a >= GB || 16 * a >= n) continue;
+    f32x4 v = set[0][a][lane];
+#pragma unroll 5
+    for (int w = 1; w < kMoeManyWaves; ++w) {
+      const f32x4 u = set[w][a][lane];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) v[f] += u[f];
+    }
+    if (n0 + lx >= p.H) continue;
+    float* o = p.part + ((int64_t)slice * p.T * p.k + s) * p.H + n0 + lx;
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const int m = 16 * a + 4 * lg + f;
+      if (m < n) o[(int64_t)m * p.H] = v[f];
+    }
+  }
+}
+
+// out[t] from the rows of its choices, in their order and in that of the slices: four columns per
+// thread.
+__global__ void __launch_bounds__(256) moe_combine(MoeParams p) {
+  const int t = blockIdx.y, n = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (n >= p.H) return;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < p.k; ++j) {
+    const int row = p.tab->row[t * p.k + j];
+    if (row < 0) break;
+    for (int s = 0; s < p.slices; ++s) {
+      const f32x4 u = *reinterpret_cast<const f32x4*>(p.part + ((int64_t)s * p.T * p.k + row) * p.H + n);
+#pragma unroll
+      for (int f = 0; f < 4; ++f) v[f] += u[f];
+    }
+  }
+  const uint32_t pk[2] = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  __builtin_memcpy(p.out + (int64_t)t * p.H + n, pk, 8);
 }
 
 }  // namespace mmk

@@ -66,6 +66,13 @@ def test_linear_lora_exact(dev, M, N, K, R, L, how):  # noqa: F811
     assert torch.equal(got.cpu(), want.float().bfloat16())
 
 
+# K in slices and many columns: the parts of one, two and four blocks of 16 rows joined
+@pytest.mark.parametrize("M,N,K,R,L", [(5, 8193, 8264, 24, 2), (20, 8200, 4200, 16, 3), (40, 8208, 136, 8, 4), (32, 70, 4104, 40, 9),
+                                       (64, 8192, 2056, 256, 2)])
+def test_linear_lora_exact_joined(dev, M, N, K, R, L):  # noqa: F811
+    test_linear_lora_exact(dev, M, N, K, R, L, "mixed")
+
+
 @pytest.mark.parametrize("M,N,K,R,L,how,epi", [
     (1, 1001, 4096, 16, 8, "mixed", "none"), (4, 1024, 2056, 64, 3, "mixed", "bias"),
     (16, 512, 8192, 16, 16, "mixed", "gelu_tanh"), (30, 300, 2000, 128, 5, "mixed", "bias_gelu_tanh"),

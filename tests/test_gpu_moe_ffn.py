@@ -190,6 +190,119 @@ def test_moe_ffn_past_32_bits(dev):  # noqa: F811
     assert torch.equal(out, mm.moe_ffn(x, logits[:, -1:].contiguous(), g1, u1, d1, 1)[0])
 
 
+# ---- experts of several tokens and many weights ---------------------------------
+
+# One and two blocks of 16 tokens to a group, steps per wave 2, 4 and 8, slices of I 1, 2 and 3, ragged
+# H and I, an expert of more tokens than a group
+LARGE = [(9, 2, 2056, 1032, 1), (33, 3, 1416, 2056, 2), (64, 8, 4088, 520, 1), (40, 5, 8192, 264, 1), (64, 4, 520, 4104, 3),
+         (17, 4, 512, 8200, 1), (64, 1, 2600, 840, 1), (12, 3, 8184, 264, 2), (61, 16, 1032, 2040, 4), (64, 2, 4096, 512, 2)]
+
+
+@pytest.mark.parametrize("T,E,H,I,k", LARGE)
+def test_moe_ffn_large(dev, T, E, H, I, k):  # noqa: F811
+    args = inputs(T, E, H, I, T + E + H)
+    out, intact = guarded((T, H), torch.bfloat16, dev)
+    d = on(dev, *args)
+    got = mm.moe_ffn(*d, k, out=out)
+    intact()
+    check(got, *args, k, True)
+    for a, b in zip(got, mm.moe_ffn(*d, k)):
+        assert torch.equal(a, b), "not reproducible"
+    # padded rows, tokens of one expert, and one that all others have
+    logits = args[1]
+    logits[0] = logits[T // 2] = -math.inf
+    logits[1, 1:] = -math.inf
+    logits[2:T // 2, 0] = 16.0
+    got = mm.moe_ffn(*on(dev, *args), k, False)
+    check(got, *args, k, False)
+    assert (got[0][[0, T // 2]] == 0).all() and (got[1][[0, T // 2]] == -1).all()
+    assert int(got[1][1, 0]) == 0 and (got[1][1, 1:] == -1).all()
+    logits[:] = -math.inf
+    got = mm.moe_ffn(*on(dev, *args), k)
+    assert (got[0] == 0).all() and (got[1] == -1).all() and (got[2] == 0).all()
+
+
+@pytest.mark.parametrize("T,E,H,I", [(20, 5, 1032, 2056), (64, 4, 2056, 1032), (33, 6, 520, 4104)])
+def test_moe_ffn_large_sums_that_are_exact(dev, T, E, H, I):  # noqa: F811
+    """As above, with two thirds of the terms of the second layer zero so that the sums stay exact."""
+    g = gen(T)
+    x = torch.randint(0, 2, (T, H), generator=g).bfloat16()
+    x[:, 0] = 1
+    gate = torch.zeros((E, I, H)).bfloat16()
+    gate[:, :, 0] = torch.randint(1, 3, (E, I), generator=g).bfloat16() * 64
+    up = torch.zeros((E, I, H)).bfloat16()
+    up[:, torch.arange(I), torch.arange(I) % H] = torch.randint(-1, 2, (E, I), generator=g).bfloat16()
+    up[:, :, H - 1] += 1
+    down = torch.randint(-1, 2, (E, H, I), generator=g).bfloat16()
+    down[:, :, ::3] = 0
+    logits = torch.randn((T, E), generator=g)
+    out, experts, _ = mm.moe_ffn(*on(dev, x, logits, gate, up, down), 1)
+    assert len(set(experts.flatten().tolist())) == E
+    for t in range(T):
+        e = int(experts[t, 0])
+        mid = (gate[e].double() @ x[t].double()) * (up[e].double() @ x[t].double())
+        assert float(down[e].double().abs().max()) * float(mid.abs().sum()) < 2 ** 24 * 64
+        want = down[e].double() @ mid
+        assert torch.equal(out[t].cpu(), want.float().bfloat16()), t
+
+
+def test_moe_ffn_large_not_finite(dev):  # noqa: F811
+    """A token's NaN, and weights that are not finite, reach the tokens that have them and no other;
+    idle experts' weights are not in the sums."""
+    T, E, H, I, k = 40, 7, 1032, 2056, 1
+    x, logits, gate, up, down = inputs(T, E, H, I, 4)
+    logits[:, 6] = -math.inf
+    clean, experts, _ = (t.cpu() for t in mm.moe_ffn(*on(dev, x, logits, gate, up, down), k))
+    x[4, 100] = math.nan
+    gate[6], up[6], down[6] = math.nan, math.inf, math.nan
+    e = int(experts[5, 0])
+    down[e, 7, 3] = math.inf
+    down[e, 9, I - 1] = math.nan
+    gate[e, I - 1, H - 1] = math.nan
+    out = mm.moe_ffn(*on(dev, x, logits, gate, up, down), k)[0].cpu()
+    hit = experts[:, 0] == e
+    assert out[hit].isnan().all() and out[4].isnan().all()
+    hit[4] = True
+    assert torch.equal(out[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("T,E,H,I,k", [(20, 3, 1032, 2056, 2), (20, 5, 520, 8200, 1)])
+def test_moe_ffn_large_keeps_inside_its_workspace(dev, T, E, H, I, k):  # noqa: F811
+    x, logits, gate, up, down = on(dev, *inputs(T, E, H, I, 12))
+    want = mm.moe_ffn(x, logits, gate, up, down, k)
+    nbytes = binding.moe_ffn_workspace_size(T, E, H, I, k)
+    ws = torch.full((nbytes + 256,), 0xFF, dtype=torch.uint8, device=dev)
+    out, experts, weights = (torch.empty_like(t) for t in want)
+    binding.check(binding.load().mm_moe_ffn(
+        x.data_ptr(), logits.data_ptr(), gate.data_ptr(), up.data_ptr(), down.data_ptr(), out.data_ptr(),
+        experts.data_ptr(), weights.data_ptr(), T, E, H, I, k, 1, ws.data_ptr(), nbytes,
+        torch.cuda.current_stream().cuda_stream), "mm_moe_ffn")
+    assert all(torch.equal(a, b) for a, b in zip((out, experts, weights), want)) and bool((ws[nbytes:] == 0xFF).all())
+
+
+def test_moe_ffn_large_replays_from_a_graph(dev):  # noqa: F811
+    """The experts of a replay are those of its own logits."""
+    T, E, H, I, k = 24, 4, 1032, 2056, 2
+    x, logits, gate, up, down = on(dev, *inputs(T, E, H, I, 31))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        mm.moe_ffn(x, logits, gate, up, down, k)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = mm.moe_ffn(x, logits, gate, up, down, k)
+    for i in range(4):
+        logits.copy_(randn(gen(100 + i), (T, E)))
+        if i == 2:
+            logits[3:] = -math.inf
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, mm.moe_ffn(x, logits, gate, up, down, k)):
+            assert torch.equal(a, b), i
+        torch.cuda.synchronize()
+
+
 # ---- a decoder layer's step ----------------------------------------------------
 
 def layer_inputs(dev, M, H, I, E):  # noqa: F811
@@ -270,14 +383,14 @@ def test_two_graphs_at_once_have_their_own_workspaces(dev):  # noqa: F811
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             outs = layer(p)
-        steps.append((side, graph, outs, want))
+        steps.append((side, graph, outs, want, p))  # (a graph reads its inputs' memory: they stay)
     torch.cuda.synchronize()
     for _ in range(3):
-        for side, graph, _, _ in steps:
+        for side, graph, _, _, _ in steps:
             with torch.cuda.stream(side):
                 for _ in range(5):
                     graph.replay()
     torch.cuda.synchronize()
-    for _, _, outs, want in steps:
+    for _, _, outs, want, _ in steps:
         for a, b in zip(outs, want):
             assert torch.equal(a, b)
