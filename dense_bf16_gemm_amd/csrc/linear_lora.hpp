@@ -478,8 +478,7 @@ __global__ void __launch_bounds__(256) lora_join(LoraParams p) {
   }
 }
 
-// The same for 16 MB rows by 64 columns of decode rows, which may have as many adapters as there
-// are rows: the eight waves share these, and meet in LDS, where each finishes some
+// The same for 16 MB rows by 64 columns, which may have as many adapters as there are rows: the eight waves share these, and meet in LDS, where each finishes some
 // blocks of 16 by 16.
 template <int MB>
 __global__ void __launch_bounds__(512) lora_join_few(LoraParams p) {

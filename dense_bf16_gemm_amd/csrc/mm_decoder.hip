@@ -403,11 +403,14 @@ Q8Plan lora_tile_plan(int64_t M, int64_t N, int64_t K) { return q8_plan(M, N, 2 
 mm_status lora_plan(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, LoraPlan* p) {
   // A x: enough workgroups to draw on every CU, K in slices of 512 or more.  Decode rows
   // may each have an adapter of their own; of prompts a block of rows has one or two.
-  p->low_mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+  // Measured (us, prompts, blocks of 32 rows in 4 slices / of 64 in 256 workgroups): 2047 x 4104,
+  // rank 32 10.8 / 13.0, 8192 x 8192, rank 16 42 / 44.
+  p->low_mb = M <= 16 ? 1 : M <= 32 || M > 64 ? 2 : 4;
   p->low_rb = M > 64 && R > 16 ? 2 : 1;
   p->turns = M <= 64 ? (int)std::min(M, L) : (int)std::min<int64_t>(2, L);
   const int64_t at_once = cdiv(M, 16 * p->low_mb) * cdiv(R, 16 * p->low_rb) * (M <= 64 ? p->turns : 1);
-  const int64_t want = std::min<int64_t>(16, M <= 64 ? cdiv(512, at_once) : std::max<int64_t>(1, 256 / at_once));
+  const int64_t want = M <= 64 ? std::min<int64_t>(16, cdiv(512, at_once))
+                               : std::max<int64_t>({1, std::min<int64_t>(4, 1024 / at_once), std::min<int64_t>(16, 256 / at_once)});
   p->low_k = std::max<int64_t>(512, cdiv(cdiv(K, want), 64) * 64);
   p->low_slices = cdiv(K, p->low_k);
   p->low = round256(p->low_slices * M * R * 4);
@@ -1024,12 +1027,12 @@ mm_status mm_linear_lora(const void* x, const void* W, const void* A, const void
   p.low_k = (int)plan.low_k;
   void* args[] = {&p};
   const int64_t row_blocks = cdiv(M, 16 * plan.low_mb);
-  if (row_blocks > kMaxGridY) return fail(MM_ERR_UNSUPPORTED, "M must be below 2^22");
+  if (row_blocks > kMaxGridY) return fail(MM_ERR_UNSUPPORTED, "M must be at most 2^21 - 32");
   void* shrink_args[] = {&p, &plan.turns};
   s = launch(plan.low_mb == 1   ? fn(&mmk::lora_shrink<1, 1>)
-             : plan.low_mb == 2 ? fn(&mmk::lora_shrink<2, 1>)
-             : plan.low_rb == 1 ? fn(&mmk::lora_shrink<4, 1>)
-                                : fn(&mmk::lora_shrink<4, 2>),
+             : plan.low_mb == 4 ? fn(&mmk::lora_shrink<4, 1>)
+             : plan.low_rb == 1 ? fn(&mmk::lora_shrink<2, 1>)
+                                : fn(&mmk::lora_shrink<2, 2>),
              dim3((unsigned)plan.low_slices, (unsigned)row_blocks, (unsigned)(cdiv(rank, 16 * plan.low_rb) * plan.turns)),
              mmk::kLoraShrinkWaves * 64, shrink_args, stream, "linear_lora shrink");
   if (s != MM_OK) return s;
@@ -1043,14 +1046,6 @@ mm_status mm_linear_lora(const void* x, const void* W, const void* A, const void
     s = launch(k, dim3((unsigned)cdiv(blocks, each), (unsigned)plan.slices),
                mmk::kLoraWaves * 64, args, stream, "linear_lora rows");
     if (s != MM_OK || plan.finish) return s;
-    // All rows to a workgroup where the columns' workgroups are enough, which reads B
-    // once: 64 x 14336, rank 64, 8 adapters 10.4 us (12.8 in blocks of 16 rows), but 49 x 1473
-    // 9.1 us (4.6).
-    const int jb = N >= 8192 ? plan.mb : 1;
-    return launch(jb == 1   ? fn(&mmk::lora_join_few<1>)
-                  : jb == 2 ? fn(&mmk::lora_join_few<2>)
-                            : fn(&mmk::lora_join_few<4>),
-                  dim3((unsigned)cdiv(N, 64), (unsigned)cdiv(M, 16 * jb)), 512, args, stream, "linear_lora join");
   } else {
     const Q8Plan& t = plan.tiles;
     const bool split = t.chunks > 1;
@@ -1074,8 +1069,18 @@ mm_status mm_linear_lora(const void* x, const void* W, const void* A, const void
                "linear_lora tiles");
     if (s != MM_OK || !split) return s;
   }
-  return launch(fn(&mmk::lora_join), dim3((unsigned)cdiv(N, 64), (unsigned)cdiv(M, 64)), 256, args, stream,
-                "linear_lora join");
+  // Few rows: all to a workgroup where the columns' workgroups are enough, which reads B once
+  // (64 x 14336, rank 64, 8 adapters 10.4 us, 12.8 in blocks of 16 rows; but 49 x 1473 9.1, 4.6).
+  // More: 64 by 64 where that makes a workgroup for every CU (us, so / in blocks of 16 rows:
+  // 1000 x 1024 6.9 / 8.0, 512 x 4096 6.2 / 9.8; but 300 x 2000 11.1 / 8.2, 100 x 4096 10.4 / 6.2).
+  const int64_t groups = cdiv(N, 64);
+  if (!plan.mb && groups * cdiv(M, 64) >= 256)
+    return launch(fn(&mmk::lora_join), dim3((unsigned)groups, (unsigned)cdiv(M, 64)), 256, args, stream, "linear_lora join");
+  const int jb = plan.mb && N >= 8192 ? plan.mb : 1;
+  return launch(jb == 1   ? fn(&mmk::lora_join_few<1>)
+                : jb == 2 ? fn(&mmk::lora_join_few<2>)
+                          : fn(&mmk::lora_join_few<4>),
+                dim3((unsigned)groups, (unsigned)cdiv(M, 16 * jb)), 512, args, stream, "linear_lora join");
 }
 
 mm_status mm_moe_ffn_workspace_size(int64_t tokens, int64_t experts, int64_t H, int64_t I, int64_t top_k, int64_t* bytes) {
