@@ -69,7 +69,8 @@ __device__ __forceinline__ float2 row_block_sum(float2 v, float2* slot) {
 }
 
 // One row per workgroup; thread t holds vectors t, t + T, ... (VPT of them)
-// of 8 values.
+// of 8 values, so that the row is read once and both sums run over registers.  Bound by
+// HBM: 2047 x 5000 fp32 with a residual 28 us (143 MB, 5.1 TB/s); one row of 8192 3.3 us, the latency of a load and two sums.
 template <bool F32, int VPT>
 __global__ void __launch_bounds__(1024) layer_norm(LayerNormParams p) {
   __shared__ float slot[2][16];
@@ -141,6 +142,7 @@ __global__ void __launch_bounds__(1024) layer_norm(LayerNormParams p) {
 // columns for every row, so its parts of dw and db stay in registers (fp32) and are
 // written once; layer_norm_dparams adds the workgroups' parts in order.  AHEAD
 // (up to 512 threads): a row's loads are issued before the row before is summed.
+// Bound by HBM: 8192 x 4096 bf16 with dres 59 us with the parts' sum, 4.5 TB/s.
 template <bool F32, int VPT, bool AHEAD>
 __global__ void __launch_bounds__(AHEAD ? 512 : 1024) layer_norm_grad(LayerNormGradParams p) {
   __shared__ float2 slot[2][16];
@@ -266,7 +268,9 @@ __host__ __device__ constexpr int grad_few_lanes(int vpt) { return vpt == 1 ? 4 
 
 // The gradient of few rows in one launch: the first workgroups sum 8 `lanes` columns
 // of dw and db each, reading dy and h for it once more, the others take one row
-// each, as above.  T / lanes interleaved runs of rows per column.
+// each, as above.  T / lanes interleaved runs of rows per column.  A launch less and no parts
+// in memory, for dy and h twice (the second time out of L2 in part): 300 x 5000 fp32 7.4 us
+// (2.0 TB/s of what is needed once), 2048 x 8192 bf16 28.8 (4.7).
 template <bool F32, int VPT>
 __global__ void __launch_bounds__(1024) layer_norm_grad_few(LayerNormGradParams p, float* dweight, float* dbias) {
   constexpr int lanes = grad_few_lanes(VPT);

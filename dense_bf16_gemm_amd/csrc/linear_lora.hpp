@@ -81,26 +81,28 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t slice_buffer(const uint16_t* b
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), (short)0, (rows * K - from) * 2, 0x00020000);
 }
 
-// A lane's piece j (0, 1) of step st of 64 k from a row at byte `row` of a buffer: chunk
-// lane / 16 of 8 values.  Zeros past K; past the last step too (its base, a
-// scalar, has to stay inside the buffer).
-__device__ __forceinline__ u32x4 step_chunk(__amdgpu_buffer_rsrc_t buf, uint32_t row, int st, int j, int K, int steps,
-                                            int lg) {
-  const uint32_t off = 64 * st + 32 * j + 8 * lg < K ? row + 64u * j + 16u * (uint32_t)lg : 0x80000000u;
-  return load_chunk(buf, off, 128u * (uint32_t)min(st, steps - 1));
-}
-
 // A x of the rows 16 MB y .. + 16 MB - 1 over slice x of K, for 16 RB ranks; of the
 // adapters among the rows, every turns-th (blockIdx.z: ranks and turn).  The waves take every
 // eighth step of 64 k, each step's loads one step ahead, and meet in LDS, added in wave
 // order.  A CU by itself reads some 25 bytes per ns, so the slices, adapters and ranks
-// of few rows go to many (one token, rank 16, K 8192: 4.5 us in 16 slices, 12 in one).
-template <int MB, int RB>
+// of few rows go to many (one token, rank 16, K 8192: 4.0 us in 16 slices, 12 in one).
+// Few rows: latency (16 rows of as many adapters 5.1 us, 3 MB).  Prompts: a read of x, 8192 x
+// 8192 for rank 16 37 us, 3.6 TB/s.
+// TURN: loaded eight lanes to a row (to_fragments): 8192 x 8192 for rank 16 43 us without, 37 with it;
+// but rows of other adapters are left out, and where those are most, the MFMA's order touches few
+// lines: 64 rows of 64 adapters 9.0 us without, 13.8 with it.
+template <int MB, int RB, bool TURN>
 __global__ void __launch_bounds__(kLoraShrinkWaves * 64) lora_shrink(LoraParams p, int turns) {
   __shared__ f32x4 red[kLoraShrinkWaves][MB * RB][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lx = lane & 15, lg = lane >> 4;
+  // row and chunk of a block's load j, and its two as fragments
+  auto row = [&](int j) __attribute__((always_inline)) { return TURN ? 8 * j + (lane >> 3) : lx; };
+  auto chunk = [&](int j) __attribute__((always_inline)) { return TURN ? lane & 7 : 4 * j + lg; };
+  auto turn = [&](u32x4(&v)[2]) __attribute__((always_inline)) {
+    if constexpr (TURN) to_fragments(v, red[wave][0], lane);  // (free during the products)
+  };
   const int m0 = blockIdx.y * (16 * MB), rows = min(16 * MB, p.M - m0);
   const int r0 = (int)(blockIdx.z / turns) * (16 * RB), my_turn = blockIdx.z % turns;
   const int K = p.K, kbeg = blockIdx.x * p.low_k, klen = min(p.low_k, K - kbeg), steps = (klen + 63) >> 6;
@@ -109,23 +111,27 @@ __global__ void __launch_bounds__(kLoraShrinkWaves * 64) lora_shrink(LoraParams 
   struct Step {
     u32x4 w[RB][2], x[MB][2];
   };
-  int turn = 0;
+  int nth = 0;
   each_adapter(lane < rows ? lora_adapter(p, m0 + lane) : -1, [&](int a, uint64_t same) {
-    if (turn++ % turns != my_turn) return;
+    if (nth++ % turns != my_turn) return;
     const __amdgpu_buffer_rsrc_t rw =
         slice_buffer(p.A + ((int64_t)a * p.R + r0) * K + kbeg, min(16 * RB, p.R - r0), K, kbeg);
-    uint32_t xrow[MB];  // (rows of other adapters are not loaded)
+    uint32_t xrow[MB][2];  // (rows of other adapters are not loaded)
 #pragma unroll
     for (int b = 0; b < MB; ++b)
-      xrow[b] = (same >> (16 * b + lx)) & 1 ? (uint32_t)(16 * b + lx) * (uint32_t)K * 2u : 0x80000000u;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int m = 16 * b + row(j);
+        xrow[b][j] = (same >> m) & 1 ? (uint32_t)m * (uint32_t)K * 2u : 0x80000000u;
+      }
     auto load = [&](int st, Step& t) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
         for (int c = 0; c < RB; ++c)
-          t.w[c][j] = step_chunk(rw, (uint32_t)(16 * c + lx) * (uint32_t)K * 2u, st, j, klen, steps, lg);
+          t.w[c][j] = step_chunk(rw, (uint32_t)(16 * c + row(j)) * (uint32_t)K * 2u, st, chunk(j), klen, steps);
 #pragma unroll
-        for (int b = 0; b < MB; ++b) t.x[b][j] = step_chunk(rx, xrow[b], st, j, klen, steps, lg);
+        for (int b = 0; b < MB; ++b) t.x[b][j] = step_chunk(rx, xrow[b][j], st, chunk(j), klen, steps);
       }
     };
     f32x4 acc[MB][RB];
@@ -136,19 +142,23 @@ __global__ void __launch_bounds__(kLoraShrinkWaves * 64) lora_shrink(LoraParams 
     auto step = [&](int st, Step& t, Step& next) __attribute__((always_inline)) {
       load(st + kLoraShrinkWaves, next);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int c = 0; c < RB; ++c) turn(t.w[c]);
 #pragma unroll
-        for (int b = 0; b < MB; ++b)
+      for (int b = 0; b < MB; ++b) {
+        turn(t.x[b]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int c = 0; c < RB; ++c) acc[b][c] = mfma_bf16(t.x[b][j], t.w[c][j], acc[b][c]);
+      }
     };
+    __syncthreads();  // (what was in LDS before has been read)
     Step s0, s1;
     load(wave, s0);
     for (int st = wave; st < steps; st += 2 * kLoraShrinkWaves) {
       step(st, s0, s1);
       step(st + kLoraShrinkWaves, s1, s0);
     }
-    __syncthreads();  // (what was there before has been read)
 #pragma unroll
     for (int b = 0; b < MB; ++b)
 #pragma unroll
@@ -257,23 +267,28 @@ __global__ void __launch_bounds__(256) lora_fold(LoraParams p, LoraTileRows* til
 // in LDS (two sets in turn: one barrier per block) and are added in wave order, by
 // another wave for each block.
 // FINISH (K in one slice): v comes into LDS first, the adapters' terms join the sums
-// here, each adapter on a wave, and the output is written.  Else lora_join does both,
+// here, each adapter on a wave, and the output is written.  Else lora_join_few does both,
 // and v is left in memory for it.
+// Bound by reading W: 16 x 28672 x 8192 95 us (5.0 TB/s), 1 x 8192 x 8192 25 (5.4), 64 x 14336 x
+// 4096 27 (4.3, and 7 MB of parts).  With x read from L2 for every block the first took 150; with x
+// and W loaded in the MFMA's order (see to_fragments) 99, 25 and 32.
 template <int MB, int SPW, bool FINISH>
 __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
   static_assert(SPW % 2 == 0 && MB * SPW <= 8, "x in 64 registers, two steps in turn");
   __shared__ f32x4 red[2][kLoraWaves][MB][64];
+  __shared__ f32x4 turn[kLoraWaves][128];
   __shared__ u32x4 v[FINISH ? 16 * MB : 1][2][kLoraMaxRank / 8];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lx = lane & 15, lg = lane >> 4;
+  const int lr = lane >> 3, lk = lane & 7;  // of what is loaded (to_fragments)
   const int K = p.K, steps = (K + 63) >> 6, blocks = (p.N + 15) >> 4;
   const int first = blockIdx.y * (kLoraWaves * SPW) + wave;
 
   struct Step {
     u32x4 w[2];
   };
-  uint32_t row = (uint32_t)lx * (uint32_t)K * 2u;
+  uint32_t row = (uint32_t)lr * (uint32_t)K * 2u;
   auto load = [&](int block, int i, Step& t) __attribute__((always_inline)) {
     // (opaque: the steps' offsets are not all kept in registers)
     asm volatile("" : "+v"(row));
@@ -281,7 +296,8 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
     const int n0 = 16 * min(block, blocks - 1);
     const __amdgpu_buffer_rsrc_t rw = rows_buffer(p.W + (int64_t)n0 * K, min(16, p.N - n0), K);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) t.w[j] = step_chunk(rw, row, first + kLoraWaves * i, j, K, steps, lg);
+    for (int j = 0; j < 2; ++j)
+      t.w[j] = step_chunk(rw, row + (uint32_t)(16 * j) * (uint32_t)K, first + kLoraWaves * i, lk, K, steps);
   };
   Step t[2];
   load(blockIdx.x, 0, t[0]);
@@ -294,7 +310,11 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
       for (int b = 0; b < MB; ++b)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          x[b][i][j] = step_chunk(rx, (uint32_t)(16 * b + lx) * (uint32_t)K * 2u, first + kLoraWaves * i, j, K, steps, lg);
+          x[b][i][j] = step_chunk(rx, (uint32_t)(16 * b + 8 * j + lr) * (uint32_t)K * 2u, first + kLoraWaves * i, lk, K, steps);
+#pragma unroll
+    for (int i = 0; i < SPW; ++i)
+#pragma unroll
+      for (int b = 0; b < MB; ++b) to_fragments(x[b][i], turn[wave], lane);
   }
   // this wave's adapters (of at most 16 MB) and their rows
   int mine[MB];
@@ -305,16 +325,16 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
     same[q] = 0;
   }
   if constexpr (FINISH) {
-    int turn = 0;
+    int nth = 0;
     each_adapter(lora_adapter(p, lane), [&](int a, uint64_t s) {
 #pragma unroll
       for (int q = 0; q < MB; ++q) {
-        if (turn == kLoraWaves * q + wave) {
+        if (nth == kLoraWaves * q + wave) {
           mine[q] = a;
           same[q] = s;
         }
       }
-      ++turn;
+      ++nth;
     });
     lora_fold_all(p, threadIdx.x, kLoraWaves * 64, [&](int m, int c, u32x4 hi, u32x4 lo) {
       v[m][0][c] = hi;
@@ -337,10 +357,12 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
         load(block, i + 1, t[(i + 1) & 1]);
       else
         load(block + gridDim.x, 0, t[0]);
+      u32x4(&w)[2] = t[i & 1].w;
+      to_fragments(w, turn[wave], lane);
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int b = 0; b < MB; ++b) acc[b] = mfma_bf16(x[b][i][j], t[i & 1].w[j], acc[b]);
+        for (int b = 0; b < MB; ++b) acc[b] = mfma_bf16(x[b][i][j], w[j], acc[b]);
     }
     if (FINISH && round == 0) __syncthreads();  // (v is there)
 #pragma unroll
@@ -398,6 +420,7 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
 // out = epi(sum of acc's slices + bias + B v): 64 rows by 64 columns per workgroup, 16
 // rows per wave.  B is the MFMA's first operand, so a lane's sums are of one row;
 // the block pair's rows of B are taken in the order that makes them 8 consecutive columns.
+// Bound by the parts' bytes: 512 x 4096 in 2 slices 6.2 us.
 __global__ void __launch_bounds__(256) lora_join(LoraParams p) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -479,7 +502,8 @@ __global__ void __launch_bounds__(256) lora_join(LoraParams p) {
 }
 
 // The same for 16 MB rows by 64 columns, which may have as many adapters as there are rows: the eight waves share these, and meet in LDS, where each finishes some
-// blocks of 16 by 16.
+// blocks of 16 by 16.  64 x 14336, rank 64, 8 adapters 10.5 us, 24 MB (2.3 TB/s): one chain of
+// index, v and B, sums and parts per workgroup.
 template <int MB>
 __global__ void __launch_bounds__(512) lora_join_few(LoraParams p) {
   __shared__ f32x4 red[8][MB * 4][64];
@@ -654,6 +678,9 @@ __device__ __forceinline__ void lora_mark(const LoraParams& p, int mb, int nb, i
 // tile's rows ceil(R / 32) of them, in which x stands for the rows' v, high parts then
 // low parts (rows of other adapters lie past the buffer's end: zeros), and W for the adapter's
 // B, twice.  So a tile of one adapter of rank 32 costs one super-step more.
+// Bound by issuing MFMAs and by L2: 8192^3, rank 16 815 us (1350 TFLOP/s; MFMAs in 75 % of a working
+// CU's cycles, 11 TB/s out of L2).  Where rows start inside a 128-byte line (K not a
+// multiple of 64) each copy touches two: 2047 x 3001 x 4104 65 us, 1.26 GB out of L2.
 // (A zero times an infinity or a NaN of B would be NaN in the other rows: zeros are taken
 // for them, and the adapter's rows get NaN in their columns at the end.)
 // SPLIT: the instance for a K cut into slices; those leave their sums of W x for lora_join.

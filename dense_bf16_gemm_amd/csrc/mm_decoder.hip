@@ -501,7 +501,7 @@ const void* moe_gate_up_kernel(int64_t E) {
 
 // Blocks of 16 tokens to a group there: two where an expert has 12 on the average and the
 // registers hold two.  Measured (us a call, one / two): 64 tokens, 2 of 8 experts of 4096 x 4096
-// 232 / 188, 32, 8 of 20 of 4040 x 3144 404 / 377, 64, 1 of 8 of 4096 x 4096 171 / 180.
+// 204 / 167, 64, 6 of 32 of 4096 x 2048 327 / 311, but 64, 1 of 8 of 4096 x 4096 154 / 160.
 int moe_group_blocks(int64_t T, int64_t E, int64_t H, int64_t k) { return T * k >= 12 * E && H <= 4096 ? 2 : 1; }
 
 // Workgroups that share 16 columns of the second layer: the number that spreads the
@@ -517,12 +517,17 @@ int64_t moe_splits(int64_t H) {
   return best;
 }
 
-// Whether experts of several tokens go to the kernels that hold the tokens' rows.  Measured
-// (us a call, without / with): 61 tokens, 4 of 60 experts of 2056 x 1416 276 / 256, 40, 8 of
-// 64 of 2048 x 1408 273 / 265, 64, 6 of 32 of 4096 x 2048 457 / 350, 64, 2 of 8 of 4096 x 4096
-// 304 / 188; but 16, 8 of 128 of 4096 x 1536 608 / 650, and 20, 4 of 60 of 1024 x 512 52 / 68.
+// Whether experts of several tokens go to the kernels that hold the tokens' rows: they cost a
+// launch's worth of rows per expert, which wide experts, or many tokens to one, are worth, and lose less
+// where rows start inside a line.  Measured (us a call, without / with): wide, 16 tokens, 2 of 8
+// experts of 4104 x 14344 616 / 550, 48, 4 of 32 of 4096 x 2048 313 / 295, but 64, 6 of 64 of
+// 4096 x 1536 446 / 467; many tokens, 64, 2 of 8 of 4096 x 4096 225 / 167, 64, 4 of 16 of 1024 x 2048
+// 76 / 71, but 48, 8 of 64 of 2048 x 1408 229 / 240; ragged, 61, 4 of 60 of 2056 x 1416
+// 263 / 248, but 64, 8 of 128 of 4104 x 776 548 / 576, and 64, 2 of 48 of 2056 x 1416 197 / 199.
 bool moe_many(int64_t T, int64_t E, int64_t H, int64_t I, int64_t k) {
-  return T > mmk::kMoeFew && T * k >= 4 * E && H <= 8192 && H * I >= (int64_t(1) << 21);
+  if (T <= mmk::kMoeFew || H > 8192 || T * k < 4 * E) return false;
+  if (H * I >= (int64_t(1) << 23)) return true;
+  return H * I >= (int64_t(1) << 21) && (T * k >= 12 * E || ((H % 64 != 0 || I % 64 != 0) && I >= 1024));
 }
 
 struct MoePlan {
@@ -1029,10 +1034,11 @@ mm_status mm_linear_lora(const void* x, const void* W, const void* A, const void
   const int64_t row_blocks = cdiv(M, 16 * plan.low_mb);
   if (row_blocks > kMaxGridY) return fail(MM_ERR_UNSUPPORTED, "M must be at most 2^21 - 32");
   void* shrink_args[] = {&p, &plan.turns};
-  s = launch(plan.low_mb == 1   ? fn(&mmk::lora_shrink<1, 1>)
-             : plan.low_mb == 4 ? fn(&mmk::lora_shrink<4, 1>)
-             : plan.low_rb == 1 ? fn(&mmk::lora_shrink<2, 1>)
-                                : fn(&mmk::lora_shrink<2, 2>),
+  s = launch(plan.low_mb == 1   ? fn(&mmk::lora_shrink<1, 1, false>)
+             : plan.low_mb == 4 ? fn(&mmk::lora_shrink<4, 1, false>)
+             : M <= 64          ? fn(&mmk::lora_shrink<2, 1, false>)
+             : plan.low_rb == 1 ? fn(&mmk::lora_shrink<2, 1, true>)
+                                : fn(&mmk::lora_shrink<2, 2, true>),
              dim3((unsigned)plan.low_slices, (unsigned)row_blocks, (unsigned)(cdiv(rank, 16 * plan.low_rb) * plan.turns)),
              mmk::kLoraShrinkWaves * 64, shrink_args, stream, "linear_lora shrink");
   if (s != MM_OK) return s;

@@ -8,7 +8,8 @@
 // Bound by reading the weights of the experts in use, 6 H I bytes each, once.
 // moe_gate_up leaves w SiLU(g) u, moe_down sums over experts; what tokens an expert has
 // is found by moe_route before them, or for few tokens by every workgroup of
-// moe_gate_up for itself.  The intermediate is kept as two bf16 numbers, high and
+// moe_gate_up for itself.  Experts of several tokens go to moe_gate_up_many, moe_down_many and
+// moe_combine.  The intermediate is kept as two bf16 numbers, high and
 // low part, 16 bits of significand: as one, its rounding would add as much error to
 // an output as the output's own.
 #pragma once
@@ -201,6 +202,7 @@ __device__ __forceinline__ void moe_choose(const MoeParams& p, MoeGroups<N>* tab
   }
 }
 
+// (latency, k dependent steps: 16 tokens, 8 of 128 experts 8.3 us, 64, 8 of 128 14.3)
 template <int VPL>
 __global__ void __launch_bounds__(1024) moe_route(MoeParams p, int group) {
   moe_choose<VPL, 16, kMoeTokens / 16>(p, p.tab, group, true);
@@ -228,19 +230,43 @@ __device__ __forceinline__ float swiglu(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
+// A step's 16 rows of 128 bytes are loaded with eight lanes to a row, rows lane / 8 and
+// 8 + lane / 8, chunk lane % 8, and brought to the places of the MFMA's two fragments (row
+// lane % 16, chunks lane / 16 and 4 + lane / 16) through 2 KiB of LDS of the wave's own.
+// Loaded in those places at once, 16 neighbouring lanes touch 16 lines, which holds a CU to
+// some 16 bytes a clock and the reading of weights to 5.2 TB/s.
+// KEEP: the places stay in registers; else they are taken anew each time, which leaves room for more
+// waves (8 tokens, 4 of 32 experts of 1024 x 512 25.1 us kept, 21.7 anew; but 61, 4 of 60 of
+// 2056 x 1416, whose waves a CU holds either way, 245, 250).
+template <bool KEEP = false>
+__device__ __forceinline__ void to_fragments(u32x4 (&v)[2], f32x4* slot, int lane) {
+  if constexpr (!KEEP) asm volatile("" : "+v"(lane));
+  // (chunks of rows 2 i and 2 i + 1 keyed by i: no bank twice)
+  const int at = lane ^ (lane >> 4);
+  slot[at] = __builtin_bit_cast(f32x4, v[0]);
+  slot[64 + (at ^ 4)] = __builtin_bit_cast(f32x4, v[1]);
+  __builtin_amdgcn_wave_barrier();
+  const int row = lane & 15, from = 8 * row + ((lane >> 4) ^ (row >> 1));
+  v[0] = __builtin_bit_cast(u32x4, slot[from]);
+  v[1] = __builtin_bit_cast(u32x4, slot[from ^ 4]);
+}
+
 // A unit of work: 8 columns of I of one group, gate and up rows together as the 16
 // columns of an MFMA block.  The eight waves take every eighth step of 64 k, each
 // step's loads one step ahead, and meet in LDS, added in wave order.  Of an expert with
 // more tokens than a group of 16 takes the weights are read again for each group.
 // VPL > 0: up to eight tokens, each workgroup chooses their experts itself.
+// Bound by the weights: one token, 2 of 8 experts of 4096 x 14336, both layers 124 us (5.7 TB/s); 16
+// tokens, 8 of 128 of 4096 x 1536 551 (5.6).  With w and x loaded in the MFMA's order 134 and 601.
 template <int VPL>
 __global__ void __launch_bounds__(kMoeWaves * 64) moe_gate_up(MoeParams p) {
   constexpr bool kOwn = VPL > 0;
   __shared__ float red[kMoeWaves][64][4];
+  __shared__ f32x4 turn[kMoeWaves][128];
   __shared__ MoeGroups<kOwn ? kMoeFew * kMoeTopK : 1> own;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lx = lane & 15, lg = lane >> 4;
+  const int lr = lane >> 3, lk = lane & 7;  // of what is loaded (to_fragments)
   if constexpr (kOwn) {
     moe_choose<VPL, kMoeWaves, 1>(p, &own, 16, blockIdx.x == 0);
     __syncthreads();
@@ -268,13 +294,8 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_gate_up(MoeParams p) {
   const __amdgpu_buffer_rsrc_t rx =
       __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p.x), (short)0, p.T * H * 2, 0x00020000);
   // chunks of the last step past H: zeros on both sides
-  bool out[2];
-  uint32_t tail[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    out[j] = 64 * (steps - 1) + 32 * j + 8 * lg >= H;
-    tail[j] = out[j] ? 0x80000000u : 0u;
-  }
+  const bool out = 64 * (steps - 1) + 8 * lk >= H;
+  const uint32_t tail = out ? 0x80000000u : 0u;
   struct Step {
     u32x4 w[2], x[2];
   };
@@ -283,26 +304,31 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_gate_up(MoeParams p) {
     const int e = __builtin_amdgcn_readfirstlane(pick([&](auto& t) { return t.act[q]; }));
     const int s = __builtin_amdgcn_readfirstlane(pick([&](auto& t) { return t.start[q]; }));
     const int n = __builtin_amdgcn_readfirstlane(pick([&](auto& t) { return t.rows[q]; }));
-    const uint16_t* w = (lx < 8 ? p.wg : p.wu) + ((int64_t)e * p.I + c0 + (lx & 7)) * H + 8 * lg;
-    uint32_t xo = 0x80000000u;
-    if (lx < n) xo = (uint32_t)pick([&](auto& t) { return t.tok[s + lx]; }) * (uint32_t)H * 2u + 16u * (uint32_t)lg;
+    const int64_t wrow = ((int64_t)e * p.I + c0 + lr) * H + 8 * lk;
+    const uint16_t *wg = p.wg + wrow, *wu = p.wu + wrow;
+    uint32_t xo[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int m = 8 * j + lr;
+      xo[j] = 0x80000000u;
+      if (m < n) xo[j] = (uint32_t)pick([&](auto& t) { return t.tok[s + m]; }) * (uint32_t)H * 2u + 16u * (uint32_t)lk;
+    }
     auto load = [&](int st, Step& t) __attribute__((always_inline)) {
       const bool last = st == steps - 1;
+      const int at = last && out ? -8 * lk : 64 * st;
+      t.w[0] = *reinterpret_cast<const u32x4*>(wg + at);
+      t.w[1] = *reinterpret_cast<const u32x4*>(wu + at);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        t.w[j] = *reinterpret_cast<const u32x4*>(w + (last && out[j] ? -8 * lg : 64 * st + 32 * j));
-        t.x[j] = load_chunk(rx, (xo + 64u * j) | (last ? tail[j] : 0u), 128u * (uint32_t)st);
-      }
+      for (int j = 0; j < 2; ++j) t.x[j] = load_chunk(rx, xo[j] | (last ? tail : 0u), 128u * (uint32_t)st);
     };
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     auto step = [&](int st, Step& t, Step& next) __attribute__((always_inline)) {
       load(min(st + kMoeWaves, steps - 1), next);
-      const bool last = st == steps - 1;
+      if (st == steps - 1 && out) t.w[0] = t.w[1] = u32x4{0u, 0u, 0u, 0u};
+      to_fragments(t.x, turn[wave], lane);
+      to_fragments(t.w, turn[wave], lane);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (last && out[j]) t.w[j] = u32x4{0u, 0u, 0u, 0u};
-        acc = mfma_bf16(t.x[j], t.w[j], acc);
-      }
+      for (int j = 0; j < 2; ++j) acc = mfma_bf16(t.x[j], t.w[j], acc);
     };
     if (wave < steps) {
       Step s0, s1;
@@ -339,14 +365,18 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_gate_up(MoeParams p) {
 // order.  With more than one workgroup (few columns would leave CUs idle) moe_join
 // adds their parts.  (The last workgroup to arrive could; but the fences that order
 // its reads after the others' writes took 230 us, since each writes back and
-// invalidates an XCD's L2.)
+// invalidates an XCD's L2.)  Bound by the weights, as above.  Waves that take
+// every eighth step, as there, read no faster and add up more often (20, 4 of 60 experts of 1024 x 512
+// 18 us, 14 in runs), and twice the waves were no faster either.
 // TB: blocks of 16 tokens.
 template <int TB>
 __global__ void __launch_bounds__(kMoeWaves * 64) moe_down(MoeParams p) {
   __shared__ float sums[kMoeWaves][16 * TB][16];
+  __shared__ f32x4 turn[kMoeWaves][128];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lx = lane & 15, lg = lane >> 4;
+  const int lr = lane >> 3, lk = lane & 7;  // of what is loaded (to_fragments)
   const MoeTables* tab = p.tab;
   const int I = p.I, steps = (I + 63) >> 6;
   const int count = __builtin_amdgcn_readfirstlane(tab->count);
@@ -357,39 +387,37 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_down(MoeParams p) {
   for (int i = lane; i < 16 * TB * 16; i += 64) (&sums[wave][0][0])[i] = 0.f;
   const __amdgpu_buffer_rsrc_t rx =
       __builtin_amdgcn_make_buffer_rsrc(p.mid, (short)0, p.T * p.k * I * 4, 0x00020000);
-  const int64_t row = min(n0 + lx, p.H - 1);
-  bool out[2];
-  uint32_t tail[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    out[j] = 64 * (steps - 1) + 32 * j + 8 * lg >= I;
-    tail[j] = out[j] ? 0x80000000u : 0u;
-  }
+  const bool out = 64 * (steps - 1) + 8 * lk >= I;
+  const uint32_t tail = out ? 0x80000000u : 0u;
   struct Step {
-    u32x4 w[2], x[2][2];
+    u32x4 w[2], x[2][2];  // (x: high and low parts)
   };
   // a group and a step of its I
   struct At {
     int q, st, s, n;
-    const uint16_t* w;
-    uint32_t xo;
+    const uint16_t* w[2];
+    uint32_t xo[2];
   };
   auto enter = [&](At& at, int q) __attribute__((always_inline)) {
     at.q = q;
     const int e = __builtin_amdgcn_readfirstlane(tab->act[q]);
     at.s = __builtin_amdgcn_readfirstlane(tab->start[q]);
     at.n = __builtin_amdgcn_readfirstlane(tab->rows[q]);
-    at.w = p.wd + ((int64_t)e * p.H + row) * I + 8 * lg;
-    at.xo = lx < at.n ? (uint32_t)(at.s + lx) * (uint32_t)I * 4u + 16u * (uint32_t)lg : 0x80000000u;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int m = 8 * j + lr;
+      at.w[j] = p.wd + ((int64_t)e * p.H + min(n0 + m, p.H - 1)) * I + 8 * lk;
+      at.xo[j] = m < at.n ? (uint32_t)(at.s + m) * (uint32_t)I * 4u + 16u * (uint32_t)lk : 0x80000000u;
+    }
   };
   auto load = [&](const At& at, Step& t) __attribute__((always_inline)) {
     const bool last = at.st == steps - 1;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      t.w[j] = *reinterpret_cast<const u32x4*>(at.w + (last && out[j] ? -8 * lg : 64 * at.st + 32 * j));
+      t.w[j] = *reinterpret_cast<const u32x4*>(at.w[j] + (last && out ? -8 * lk : 64 * at.st));
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        t.x[j][h] = load_chunk(rx, (at.xo + 64u * j + (uint32_t)(2 * I) * h) | (last ? tail[j] : 0u), 128u * (uint32_t)at.st);
+        t.x[h][j] = load_chunk(rx, (at.xo[j] + (uint32_t)(2 * I) * h) | (last ? tail : 0u), 128u * (uint32_t)at.st);
     }
   };
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -406,12 +434,13 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_down(MoeParams p) {
     auto step = [&](Step& t, Step& next) __attribute__((always_inline)) {
       advance(ahead);  // (past the last step, that of another wave or the last again: unused)
       load(ahead, next);
-      const bool last = now.st == steps - 1;
+      if (now.st == steps - 1 && out) t.w[0] = t.w[1] = u32x4{0u, 0u, 0u, 0u};
+      to_fragments(t.w, turn[wave], lane);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (last && out[j]) t.w[j] = u32x4{0u, 0u, 0u, 0u};
-        acc = mfma_bf16(t.x[j][0], t.w[j], acc);
-        acc = mfma_bf16(t.x[j][1], t.w[j], acc);
+      for (int h = 0; h < 2; ++h) {
+        to_fragments(t.x[h], turn[wave], lane);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc = mfma_bf16(t.x[h][j], t.w[j], acc);
       }
     };
     auto leave = [&](int i) __attribute__((always_inline)) {
@@ -481,14 +510,16 @@ __global__ void __launch_bounds__(256) moe_join(MoeParams p) {
 // rows in registers until the group changes: the steps 16 i + w of 64 values, i < SPW.
 // Each step's weights are loaded one step ahead, across units; the waves' sums of a unit
 // meet in LDS (two sets in turn: one barrier per unit), and are added in wave order by
-// another wave for each unit.
+// another wave for each unit.  61 tokens, 4 of 60 experts of 2056 x 1416: 248 us
+// in all (4.2 TB/s of rows that start inside a line); 64, 6 of 32 of 4096 x 2048 311 (5.2), 343 with x
+// out of L2.
 
 constexpr int kMoeManyWaves = 16;
 
-// A lane's piece j of step st of 64 values from a row at byte `row` of a buffer of rows of n values;
-// zeros past them, and past the last step.
-__device__ __forceinline__ u32x4 moe_chunk(__amdgpu_buffer_rsrc_t buf, uint32_t row, int st, int j, int n, int steps, int lg) {
-  const uint32_t off = 64 * st + 32 * j + 8 * lg < n ? row + 64u * j + 16u * (uint32_t)lg : 0x80000000u;
+// A lane's chunk of step st of 64 values from a row at byte `row` of a buffer of rows of n values;
+// zeros past them, and past the last step (its base, a scalar, has to stay inside the buffer).
+__device__ __forceinline__ u32x4 step_chunk(__amdgpu_buffer_rsrc_t buf, uint32_t row, int st, int chunk, int n, int steps) {
+  const uint32_t off = 64 * st + 8 * chunk < n ? row + 16u * (uint32_t)chunk : 0x80000000u;
   return load_chunk(buf, off, 128u * (uint32_t)min(st, steps - 1));
 }
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t moe_rows(const uint16_t* base, int rows, int n) {
@@ -500,9 +531,11 @@ template <int GB, int SPW>
 __global__ void __launch_bounds__(kMoeManyWaves * 64) moe_gate_up_many(MoeParams p) {
   static_assert(SPW % 2 == 0 && GB * SPW <= 8, "x in 64 registers, two steps in turn");
   __shared__ f32x4 red[2][kMoeManyWaves][2][GB][64];
+  __shared__ f32x4 turn[kMoeManyWaves][128];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lx = lane & 15, lg = lane >> 4;
+  const int lr = lane >> 3, lk = lane & 7;  // of what is loaded (to_fragments)
   const MoeTables* tab = p.tab;
   const int H = p.H, steps = (H + 63) >> 6, cols = (p.I + 15) >> 4;
   const int64_t units = (int64_t)__builtin_amdgcn_readfirstlane(tab->count) * cols;
@@ -520,13 +553,22 @@ __global__ void __launch_bounds__(kMoeManyWaves * 64) moe_gate_up_many(MoeParams
     rg = moe_rows(p.wg + first * H, rows, H);
     ru = moe_rows(p.wu + first * H, rows, H);
   };
-  uint32_t row = (uint32_t)lx * (uint32_t)H * 2u;
+  uint32_t row = (uint32_t)lr * (uint32_t)H * 2u;
   auto load = [&](int i, Step& t) __attribute__((always_inline)) {
-    asm volatile("" : "+v"(row));  // (opaque: the steps' offsets are not all kept in registers)
+    // opaque: the steps' offsets are not all kept in registers; the row neither, where x leaves none
+    // (6 spilled)
+    int l = lane;
+    if constexpr (GB * SPW == 8) {
+      asm volatile("" : "+v"(l));
+      row = (uint32_t)(l >> 3) * (uint32_t)H * 2u;
+    } else {
+      asm volatile("" : "+v"(row));
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      t.w[0][j] = moe_chunk(rg, row, wave + kMoeManyWaves * i, j, H, steps, lg);
-      t.w[1][j] = moe_chunk(ru, row, wave + kMoeManyWaves * i, j, H, steps, lg);
+      const uint32_t at = row + (uint32_t)(16 * j) * (uint32_t)H;
+      t.w[0][j] = step_chunk(rg, at, wave + kMoeManyWaves * i, l & 7, H, steps);
+      t.w[1][j] = step_chunk(ru, at, wave + kMoeManyWaves * i, l & 7, H, steps);
     }
   };
   Step t[2];
@@ -543,13 +585,22 @@ __global__ void __launch_bounds__(kMoeManyWaves * 64) moe_gate_up_many(MoeParams
       const __amdgpu_buffer_rsrc_t rx = moe_rows(p.x, p.T, H);
 #pragma unroll
       for (int a = 0; a < GB; ++a) {
-        uint32_t xo = 0x80000000u;
-        if (16 * a + lx < n) xo = (uint32_t)tab->tok[s + 16 * a + lx] * (uint32_t)H * 2u;
+        uint32_t xo[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int m = 16 * a + 8 * j + lr;
+          xo[j] = 0x80000000u;
+          if (m < n) xo[j] = (uint32_t)tab->tok[s + m] * (uint32_t)H * 2u;
+        }
 #pragma unroll
         for (int i = 0; i < SPW; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) x[a][i][j] = moe_chunk(rx, xo, wave + kMoeManyWaves * i, j, H, steps, lg);
+          for (int j = 0; j < 2; ++j) x[a][i][j] = step_chunk(rx, xo[j], wave + kMoeManyWaves * i, lk, H, steps);
       }
+#pragma unroll
+      for (int a = 0; a < GB; ++a)
+#pragma unroll
+        for (int i = 0; i < SPW; ++i) to_fragments<GB == 1>(x[a][i], turn[wave], lane);
     }
     f32x4 acc[2][GB];
 #pragma unroll
@@ -570,11 +621,14 @@ __global__ void __launch_bounds__(kMoeManyWaves * 64) moe_gate_up_many(MoeParams
         load(0, t[0]);
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int h = 0; h < 2; ++h) {
+        u32x4(&w)[2] = t[i & 1].w[h];
+        to_fragments<GB == 1>(w, turn[wave], lane);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int a = 0; a < GB; ++a) acc[h][a] = mfma_bf16(x[a][i][j], t[i & 1].w[h][j], acc[h][a]);
+          for (int a = 0; a < GB; ++a) acc[h][a] = mfma_bf16(x[a][i][j], w[j], acc[h][a]);
+      }
     }
     auto set = red[(unit - u0) & 1];
 #pragma unroll
@@ -612,9 +666,11 @@ template <int GB, int SPW>
 __global__ void __launch_bounds__(kMoeManyWaves * 64) moe_down_many(MoeParams p) {
   static_assert(SPW % 2 == 0 && GB * SPW <= 4, "x in 64 registers, two steps in turn");
   __shared__ f32x4 red[2][kMoeManyWaves][GB][64];
+  __shared__ f32x4 turn[kMoeManyWaves][128];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lx = lane & 15, lg = lane >> 4;
+  const int lr = lane >> 3, lk = lane & 7;  // of what is loaded (to_fragments)
   const MoeTables* tab = p.tab;
   const int I = p.I, steps = (I + 63) >> 6, cols = (p.H + 15) >> 4;
   const int64_t units = (int64_t)__builtin_amdgcn_readfirstlane(tab->count) * p.slices * cols;
@@ -632,16 +688,17 @@ __global__ void __launch_bounds__(kMoeManyWaves * 64) moe_down_many(MoeParams p)
     const int64_t first = (int64_t)__builtin_amdgcn_readfirstlane(tab->act[g]) * p.H + 16 * lc;
     rw = moe_rows(p.wd + first * I, min(16, p.H - 16 * lc), I);
   };
-  uint32_t row = (uint32_t)lx * (uint32_t)I * 2u;
+  uint32_t row = (uint32_t)lr * (uint32_t)I * 2u;
   auto load = [&](int i, Step& t) __attribute__((always_inline)) {
     asm volatile("" : "+v"(row));
 #pragma unroll
-    for (int j = 0; j < 2; ++j) t.w[j] = moe_chunk(rw, row, lfirst + kMoeManyWaves * i, j, I, steps, lg);
+    for (int j = 0; j < 2; ++j)
+      t.w[j] = step_chunk(rw, row + (uint32_t)(16 * j) * (uint32_t)I, lfirst + kMoeManyWaves * i, lk, I, steps);
   };
   Step t[2];
   enter();
   load(0, t[0]);
-  u32x4 x[GB][SPW][2][2];
+  u32x4 x[GB][SPW][2][2];  // (high and low parts)
   int q = -1, c = lc, s = 0, n = 0, slice = 0;
   for (int unit = u0; unit < u1; ++unit) {
     if (q < 0 || c == cols) {
@@ -655,15 +712,26 @@ __global__ void __launch_bounds__(kMoeManyWaves * 64) moe_down_many(MoeParams p)
       const int first = slice * (kMoeManyWaves * SPW) + wave;
 #pragma unroll
       for (int a = 0; a < GB; ++a) {
-        const uint32_t xo = 16 * a + lx < n ? (uint32_t)(16 * a + lx) * (uint32_t)I * 4u : 0x80000000u;
+        uint32_t xo[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int m = 16 * a + 8 * j + lr;
+          xo[j] = m < n ? (uint32_t)m * (uint32_t)I * 4u : 0x80000000u;
+        }
 #pragma unroll
         for (int i = 0; i < SPW; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              x[a][i][j][h] = moe_chunk(rx, xo + (uint32_t)(2 * I) * h, first + kMoeManyWaves * i, j, I, steps, lg);
+            for (int j = 0; j < 2; ++j)
+              x[a][i][h][j] = step_chunk(rx, xo[j] + (uint32_t)(2 * I) * h, first + kMoeManyWaves * i, lk, I, steps);
       }
+#pragma unroll
+      for (int a = 0; a < GB; ++a)
+#pragma unroll
+        for (int i = 0; i < SPW; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) to_fragments<GB == 1>(x[a][i][h], turn[wave], lane);
     }
     f32x4 acc[GB];
 #pragma unroll
@@ -680,13 +748,14 @@ __global__ void __launch_bounds__(kMoeManyWaves * 64) moe_down_many(MoeParams p)
         enter();
         load(0, t[0]);
       }
+      u32x4(&w)[2] = t[i & 1].w;
+      to_fragments<GB == 1>(w, turn[wave], lane);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int a = 0; a < GB; ++a)
 #pragma unroll
-        for (int a = 0; a < GB; ++a) {
-          acc[a] = mfma_bf16(x[a][i][j][0], t[i & 1].w[j], acc[a]);
-          acc[a] = mfma_bf16(x[a][i][j][1], t[i & 1].w[j], acc[a]);
-        }
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[a] = mfma_bf16(x[a][i][h][j], w[j], acc[a]);
     }
     auto set = red[(unit - u0) & 1];
 #pragma unroll

@@ -1,7 +1,8 @@
-"""Times of the decoder-layer operators: the cases of perf/operators.py, and
-any others of the same kinds.
+"""Times of the decoder-layer operators: the cases of perf/operators.py, or with
+--more those of perf/more_operators.py, and any others of the same kinds.
 
     python examples/operator_times.py [name ...] [--case op=q8,M=512,N=8192,K=8192,epilogue=none ...] [--calls N]
+    python examples/operator_times.py --more [name ...] [--case op=moe,T=16,E=8,H=4096,I=14336,top_k=2 ...] [--calls N]
 
 Names select among the listed cases (none: all, or only those given with
 --case).  For each case two times are printed, in
@@ -26,10 +27,13 @@ sys.path.insert(0, ROOT)
 DEFAULTS = {"norm": dict(stream="bf16", residual=True), "norm_q8": dict(stream="bf16", residual=True),
             "norm_backward": dict(stream="bf16", residual=True),
             "w4": dict(group=128, zeros=False, epilogue="none"), "q8": dict(epilogue="none")}
+MORE_DEFAULTS = {"norm": DEFAULTS["norm"], "norm_backward": DEFAULTS["norm_backward"],
+                 "lora": dict(rank=16, adapters=8, requests=8, epilogue="none"),
+                 "moe": dict(renormalize=True, padded=0)}
 
 
-def operators():
-    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+def operators(file):
+    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", file))
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
     module.own = True
@@ -41,9 +45,7 @@ def parse_case(text):
     for part in text.split(","):
         key, _, value = part.partition("=")
         values[key] = int(value) if value.isdigit() else {"True": True, "False": False}.get(value, value)
-    if values.get("op") not in DEFAULTS:
-        raise argparse.ArgumentTypeError(f"op must be one of {', '.join(DEFAULTS)}")
-    return dict(name=text, **{**DEFAULTS[values["op"]], **values})
+    return dict(name=text, **values)
 
 
 def median_us(fn, calls):
@@ -89,12 +91,17 @@ def main(argv=None):
     parser.add_argument("names", nargs="*")
     parser.add_argument("--case", action="append", type=parse_case, default=[])
     parser.add_argument("--calls", type=int, default=0)
+    parser.add_argument("--more", action="store_true")
     args = parser.parse_args(argv)
+    defaults = MORE_DEFAULTS if args.more else DEFAULTS
+    for case in args.case:
+        if case.get("op") not in defaults:
+            parser.error(f"op must be one of {', '.join(defaults)}")
     if not torch.cuda.is_available():
         raise SystemExit("these times need a GPU")
-    module = operators()
-    cases = [c for c in module.listed()
-             if c["name"] in args.names or not (args.names or args.case)] + args.case
+    module = operators("more_operators.py" if args.more else "operators.py")
+    cases = [c for c in module.listed() if c["name"] in args.names or not (args.names or args.case)]
+    cases += [{**defaults[c["op"]], **c} for c in args.case]
     for case in cases:
         if args.calls:
             state = module.prepare(case, 0)

@@ -195,7 +195,8 @@ def test_moe_ffn_past_32_bits(dev):  # noqa: F811
 # One and two blocks of 16 tokens to a group, steps per wave 2, 4 and 8, slices of I 1, 2 and 3, ragged
 # H and I, an expert of more tokens than a group
 LARGE = [(9, 2, 2056, 1032, 1), (33, 3, 1416, 2056, 2), (64, 8, 4088, 520, 1), (40, 5, 8192, 264, 1), (64, 4, 520, 4104, 3),
-         (17, 4, 512, 8200, 1), (64, 1, 2600, 840, 1), (12, 3, 8184, 264, 2), (61, 16, 1032, 2040, 4), (64, 2, 4096, 512, 2)]
+         (17, 4, 512, 8200, 1), (64, 1, 2600, 840, 1), (12, 3, 8184, 264, 2), (61, 16, 1032, 2040, 4), (64, 2, 4096, 512, 2),
+         (40, 3, 8192, 264, 1), (12, 1, 8184, 264, 1), (16, 2, 4096, 2056, 1)]
 
 
 @pytest.mark.parametrize("T,E,H,I,k", LARGE)
