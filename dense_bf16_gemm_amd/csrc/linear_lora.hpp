@@ -87,8 +87,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t slice_buffer(const uint16_t* b
 // order.  A CU by itself reads some 25 bytes per ns, so the slices, adapters and ranks
 // of few rows go to many (one token, rank 16, K 8192: 4.0 us in 16 slices, 12 in one).
 // Few rows: latency (16 rows of as many adapters 5.1 us, 3 MB).  Prompts: a read of x, 8192 x
-// 8192 for rank 16 37 us, 3.6 TB/s.
-// TURN: loaded eight lanes to a row (to_fragments): 8192 x 8192 for rank 16 43 us without, 37 with it;
+// 8192 for rank 16 35 us, 3.8 TB/s.
+// TURN: loaded eight lanes to a row (to_fragments): 8192 x 8192 for rank 16 43 us without, 35 with it;
 // but rows of other adapters are left out, and where those are most, the MFMA's order touches few
 // lines: 64 rows of 64 adapters 9.0 us without, 13.8 with it.
 template <int MB, int RB, bool TURN>
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(256) lora_fold(LoraParams p, LoraTileRows* til
 // here, each adapter on a wave, and the output is written.  Else lora_join_few does both,
 // and v is left in memory for it.
 // Bound by reading W: 16 x 28672 x 8192 95 us (5.0 TB/s), 1 x 8192 x 8192 25 (5.4), 64 x 14336 x
-// 4096 27 (4.3, and 7 MB of parts).  With x read from L2 for every block the first took 150; with x
+// 4096 26 (4.5, and 7 MB of parts).  With x read from L2 for every block the first took 150; with x
 // and W loaded in the MFMA's order (see to_fragments) 99, 25 and 32.
 template <int MB, int SPW, bool FINISH>
 __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
@@ -678,9 +678,9 @@ __device__ __forceinline__ void lora_mark(const LoraParams& p, int mb, int nb, i
 // tile's rows ceil(R / 32) of them, in which x stands for the rows' v, high parts then
 // low parts (rows of other adapters lie past the buffer's end: zeros), and W for the adapter's
 // B, twice.  So a tile of one adapter of rank 32 costs one super-step more.
-// Bound by issuing MFMAs and by L2: 8192^3, rank 16 815 us (1350 TFLOP/s; MFMAs in 75 % of a working
+// Bound by issuing MFMAs and by L2: 8192^3, rank 16 850 us (1290 TFLOP/s; MFMAs in 75 % of a working
 // CU's cycles, 11 TB/s out of L2).  Where rows start inside a 128-byte line (K not a
-// multiple of 64) each copy touches two: 2047 x 3001 x 4104 65 us, 1.26 GB out of L2.
+// multiple of 64) each copy touches two: 2047 x 3001 x 4104 75 us, 1.26 GB out of L2 (17 TB/s).
 // (A zero times an infinity or a NaN of B would be NaN in the other rows: zeros are taken
 // for them, and the adapter's rows get NaN in their columns at the end.)
 // SPLIT: the instance for a K cut into slices; those leave their sums of W x for lora_join.

@@ -66,6 +66,12 @@ def test_linear_lora_exact(dev, M, N, K, R, L, how):  # noqa: F811
     assert torch.equal(got.cpu(), want.float().bfloat16())
 
 
+# one column, and fewer than a store's eight, of more rows than the decode kernels take
+@pytest.mark.parametrize("M,N,K,R,L", [(70, 1, 8, 8, 1), (200, 3, 72, 8, 2), (130, 9, 2056, 256, 130), (1030, 7, 4096, 16, 3)])
+def test_linear_lora_exact_narrow(dev, M, N, K, R, L):  # noqa: F811
+    test_linear_lora_exact(dev, M, N, K, R, L, "mixed")
+
+
 # K in slices and many columns: the parts of one, two and four blocks of 16 rows joined
 @pytest.mark.parametrize("M,N,K,R,L", [(5, 8193, 8264, 24, 2), (20, 8200, 4200, 16, 3), (40, 8208, 136, 8, 4), (32, 70, 4104, 40, 9),
                                        (64, 8192, 2056, 256, 2)])

@@ -162,6 +162,21 @@ def test_moe_ffn_without_terms(dev):  # noqa: F811
         mm.moe_ffn(x, logits, gate, up, down, 7)
 
 
+@pytest.mark.parametrize("T", [5, 40])
+def test_moe_ffn_of_empty_sizes(dev, T):  # noqa: F811
+    """No values per token, no experts at all, and experts so wide that only their count says no."""
+    x, logits, gate, up, down = on(dev, *inputs(T, 6, 64, 24, 2))
+    want = mm.moe_ffn(x, logits, gate, up, down, 2)
+    out, experts, weights = mm.moe_ffn(x[:, :0].contiguous(), logits, gate[:, :, :0].contiguous(),
+                                       up[:, :, :0].contiguous(), down[:, :0].contiguous(), 2)
+    assert out.shape == (T, 0) and torch.equal(experts, want[1]) and torch.equal(weights, want[2])
+    for H, I in ((64, 24), (4096, 2048)):
+        wide = torch.ones((T, H), dtype=torch.bfloat16, device=dev)
+        none = torch.empty((0, I, H), dtype=torch.bfloat16, device=dev)
+        out, experts, _ = mm.moe_ffn(wide, logits[:, :0].contiguous(), none, none, none.reshape(0, H, I), 0)
+        assert (out == 0).all() and out.shape == (T, H) and experts.shape == (T, 0)
+
+
 @pytest.mark.parametrize("T", [3, 40])
 def test_moe_ffn_keeps_inside_its_workspace(dev, T):  # noqa: F811
     E, H, I, k = 10, 136, 264, 3
