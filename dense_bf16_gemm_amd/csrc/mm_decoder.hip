@@ -381,7 +381,7 @@ bool layer_norm_few(int64_t rows, int64_t hidden) { return rows <= kFewRows || h
 // Linear layer with an adapter per row
 // ----------------------------------------------------------------------------
 // At most this many rows take the rows' kernel (us a call, so / as tiles: 64 x 14336 x 4096, rank 64
-// 44.7 / 56, 33 x 3001 x 1032 14.9 / 19.6, 48 x 28672 x 8192 with as many adapters 134 / 136; the kernel's
+// 45.6 / 56.3, 33 x 3001 x 1032 16.2 / 20.2, 64 x 8192 x 8192 with as many adapters 53.8 / 56.5; the kernel's
 // registers hold no more).
 constexpr int64_t kLoraRows = 64;
 
@@ -508,7 +508,8 @@ const void* moe_gate_up_kernel(int64_t E) {
 int moe_group_blocks(int64_t T, int64_t E, int64_t H, int64_t k) { return T * k >= 12 * E && H <= 4096 ? 2 : 1; }
 
 // Workgroups that share 16 columns of the second layer: the number that spreads the
-// columns' workgroups most evenly over the CUs, a further one for a twentieth.
+// columns' workgroups most evenly over the CUs, a further one for a twentieth (256 CUs: 516 workgroups
+// of a layer took 66 us, 512 of them 50).
 int64_t moe_splits(int64_t H) {
   const int64_t blocks = cdiv(H, 16);
   int64_t best = 1;
@@ -1147,8 +1148,8 @@ mm_status mm_moe_ffn(const void* x, const float* logits, const void* W_gate, con
   p.slices = (int)plan.slices;
   void* args[] = {&p};
   // Few tokens: every workgroup of the first layer finds their experts itself (us a call, so / by a
-  // launch before: one token, 2 of 8 experts of 4096 x 14336 134.0 / 137.5, 8, 2 of 8 of 512 x 512
-  // 15.1 / 16.5; but 8, 8 of 512 of 1024 x 512 67.8 / 66.1).
+  // launch before: one token, 2 of 8 experts of 4096 x 14336 124.8 / 127.8, 8, 2 of 8 of 512 x 512
+  // 13.2 / 15.8, 8, 8 of 512 of 1024 x 512 53.5 / 58.8); a workgroup of eight waves has one token each.
   const int64_t units = T * top_k * (I / 8);  // (at most: a group for every choice)
   const bool own = T <= mmk::kMoeFew && units > 0 && H > 0;
   int group = 16 * plan.gb;
