@@ -537,7 +537,7 @@ bool moe_many(int64_t T, int64_t E, int64_t H, int64_t I, int64_t k) {
 struct MoePlan {
   bool many = false;
   int gb = 1;  // blocks of 16 tokens to a group
-  int up_spw = 0, down_spw = 0;  // steps per wave
+  int up_spw = 0, down_spw = 0;  // steps per wave (down: the three parts of x in 48 registers)
   int64_t splits = 1, slices = 1;
   int64_t mid = 0, part = 0;  // workspace bytes, after the tables
   int64_t bytes() const { return kMoeTableBytes + mid + part; }
@@ -551,12 +551,12 @@ int moe_steps(int64_t n, int most) {
 
 MoePlan moe_plan(int64_t T, int64_t E, int64_t H, int64_t I, int64_t k) {
   MoePlan p;
-  p.mid = round256(T * k * I * 4);
+  p.mid = round256(T * k * I * 6);
   p.many = moe_many(T, E, H, I, k);
   if (p.many) {
     p.gb = moe_group_blocks(T, E, H, k);
     p.up_spw = moe_steps(H, 8 / p.gb);
-    p.down_spw = moe_steps(I, 4 / p.gb);
+    p.down_spw = 2 / p.gb;
     p.slices = cdiv(I, mmk::kMoeManyWaves * 64 * p.down_spw);
     p.part = round256(p.slices * T * k * H * 4);
   } else {
@@ -572,9 +572,8 @@ const void* moe_gate_up_many_kernel(int gb, int spw) {
          : spw == 4 ? fn(&mmk::moe_gate_up_many<1, 4>)
                     : fn(&mmk::moe_gate_up_many<1, 8>);
 }
-const void* moe_down_many_kernel(int gb, int spw) {
-  if (gb == 2) return fn(&mmk::moe_down_many<2, 2>);
-  return spw == 2 ? fn(&mmk::moe_down_many<1, 2>) : fn(&mmk::moe_down_many<1, 4>);
+const void* moe_down_many_kernel(int gb) {
+  return gb == 2 ? fn(&mmk::moe_down_many<2, 1>) : fn(&mmk::moe_down_many<1, 2>);
 }
 
 }  // namespace
@@ -1162,7 +1161,7 @@ mm_status mm_moe_ffn(const void* x, const float* logits, const void* W_gate, con
     s = launch(moe_gate_up_many_kernel(plan.gb, plan.up_spw), dim3((unsigned)cus), mmk::kMoeManyWaves * 64, args, stream,
                "moe_ffn gate and up");
     if (s != MM_OK) return s;
-    s = launch(moe_down_many_kernel(plan.gb, plan.down_spw), dim3((unsigned)cus), mmk::kMoeManyWaves * 64, args, stream,
+    s = launch(moe_down_many_kernel(plan.gb), dim3((unsigned)cus), mmk::kMoeManyWaves * 64, args, stream,
                "moe_ffn down");
     if (s != MM_OK) return s;
     return launch(fn(&mmk::moe_combine), dim3((unsigned)cdiv(H, 1024), (unsigned)T), 256, args, stream, "moe_ffn combine");

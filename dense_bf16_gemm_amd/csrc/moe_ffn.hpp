@@ -9,9 +9,10 @@
 // moe_gate_up leaves w SiLU(g) u, moe_down sums over experts; what tokens an expert has
 // is found by moe_route before them, or for few tokens by every workgroup of
 // moe_gate_up for itself.  Experts of several tokens go to moe_gate_up_many, moe_down_many and
-// moe_combine.  The intermediate is kept as two bf16 numbers, high and
-// low part, 16 bits of significand: as one, its rounding would add as much error to
-// an output as the output's own.
+// moe_combine.  The intermediate is fp32, kept as three bf16 numbers whose sum it is, and the second
+// layer multiplies each: as one, its rounding would add as much error to an output as the
+// output's own; as two, 16 bits of significand, the outputs of one token of 2 of 8 experts lay 1.4e-4 from
+// those of fp32 (the roundings that it turns), as three 1.1e-5.
 #pragma once
 
 #include "gemm_q8.hpp"
@@ -21,6 +22,7 @@ namespace mmk {
 
 constexpr int kMoeTokens = 64, kMoeExperts = 512, kMoeTopK = 16;
 constexpr int kMoeFew = 8;  // tokens whose experts moe_gate_up chooses itself
+constexpr int kMoePacked = 5;  // tokens of a group whose three parts are one block of 16 rows
 constexpr int kMoeWaves = 8;
 
 // The tokens of the experts in use, grouped: group g is up to 16 or 32 tokens of expert act[g]
@@ -46,7 +48,7 @@ struct MoeParams {
   int* experts;           // [T][k]
   float* weights;         // [T][k]
   MoeTables* tab;
-  uint16_t* mid;          // [T k][2][I]: high and low parts of the intermediate
+  uint16_t* mid;          // [T k][3][I]: the parts of the intermediate
   float* part;            // parts of the output: [splits][T][H], or [slices][T k][H] of each row's
   int T, E, H, I, k;
   int renormalize;
@@ -225,6 +227,31 @@ __device__ __forceinline__ void split_bf16(float v, uint16_t* hi, uint16_t* lo) 
   *lo = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v - __builtin_bit_cast(float, b & 0xffff0000u)));
 }
 
+// A float as the sum of three bf16: 8 bits of the significand each, cut, so that the sum is exact
+// (to 2^-133, the last bit of a bf16).  put(i, part i); what is not finite stays in part 0.
+template <typename F>
+__device__ __forceinline__ void split_bf16(float v, F put) {
+  uint32_t b = __builtin_bit_cast(uint32_t, v);
+  if ((b & 0x7f800000u) == 0x7f800000u) {
+    put(0, __builtin_bit_cast(uint16_t, static_cast<__bf16>(v)));
+    put(1, (uint16_t)0);
+    put(2, (uint16_t)0);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    put(i, (uint16_t)(b >> 16));
+    v -= __builtin_bit_cast(float, b & 0xffff0000u);
+    b = __builtin_bit_cast(uint32_t, v);
+  }
+}
+
+// The intermediate `v` of row `row` and column `col`, in its parts (below 2^30 values in all).
+__device__ __forceinline__ void moe_leave(const MoeParams& p, int row, int col, float v) {
+  const uint32_t at = (uint32_t)row * 3u * (uint32_t)p.I + (uint32_t)col;
+  split_bf16(v, [&](int i, uint16_t part) __attribute__((always_inline)) { p.mid[at + (uint32_t)(i * p.I)] = part; });
+}
+
 // SiLU(g) u, as the fused FFN has it
 __device__ __forceinline__ float swiglu(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
@@ -350,11 +377,7 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_gate_up(MoeParams p) {
         g += red[v][l][f];
         u += red[v][l + 8][f];
       }
-      uint16_t hi, lo;
-      split_bf16(pick([&](auto& t) { return t.wt[s + m]; }) * swiglu(g, u), &hi, &lo);
-      uint16_t* o = p.mid + (int64_t)(s + m) * 2 * p.I + c0 + c;
-      o[0] = hi;
-      o[p.I] = lo;
+      moe_leave(p, s + m, c0 + c, pick([&](auto& t) { return t.wt[s + m]; }) * swiglu(g, u));
     }
   }
 }
@@ -368,6 +391,9 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_gate_up(MoeParams p) {
 // invalidates an XCD's L2.)  Bound by the weights, as above.  Waves that take
 // every eighth step, as there, read no faster and add up more often (20, 4 of 60 experts of 1024 x 512
 // 18 us, 14 in runs), and twice the waves were no faster either.
+// The parts of up to kMoePacked tokens are rows of the same block (row 5 h + m: part h of token m),
+// of more they are three blocks (us a call, three always / so: one token, 2 of 8 experts of 4096 x 14336
+// 134.5 / 124.1, 8 tokens 502 / 457, 16, 8 of 128 of 4096 x 1536 587 / 541).
 // TB: blocks of 16 tokens.
 template <int TB>
 __global__ void __launch_bounds__(kMoeWaves * 64) moe_down(MoeParams p) {
@@ -386,11 +412,11 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_down(MoeParams p) {
   const int n0 = blockIdx.x * 16;
   for (int i = lane; i < 16 * TB * 16; i += 64) (&sums[wave][0][0])[i] = 0.f;
   const __amdgpu_buffer_rsrc_t rx =
-      __builtin_amdgcn_make_buffer_rsrc(p.mid, (short)0, p.T * p.k * I * 4, 0x00020000);
+      __builtin_amdgcn_make_buffer_rsrc(p.mid, (short)0, p.T * p.k * I * 6, 0x00020000);
   const bool out = 64 * (steps - 1) + 8 * lk >= I;
   const uint32_t tail = out ? 0x80000000u : 0u;
   struct Step {
-    u32x4 w[2], x[2][2];  // (x: high and low parts)
+    u32x4 w[2], x[3][2];  // (x: the three parts, or all in the first)
   };
   // a group and a step of its I
   struct At {
@@ -407,17 +433,26 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_down(MoeParams p) {
     for (int j = 0; j < 2; ++j) {
       const int m = 8 * j + lr;
       at.w[j] = p.wd + ((int64_t)e * p.H + min(n0 + m, p.H - 1)) * I + 8 * lk;
-      at.xo[j] = m < at.n ? (uint32_t)(at.s + m) * (uint32_t)I * 4u + 16u * (uint32_t)lk : 0x80000000u;
+      const int h = at.n > kMoePacked ? 0 : m / kMoePacked, r = m - h * kMoePacked;
+      at.xo[j] = r < at.n && h < 3 ? (uint32_t)(3 * (at.s + r) + h) * (uint32_t)I * 2u + 16u * (uint32_t)lk : 0x80000000u;
     }
   };
   auto load = [&](const At& at, Step& t) __attribute__((always_inline)) {
     const bool last = at.st == steps - 1;
+    auto load_x = [&](int h, int j) __attribute__((always_inline)) {
+      t.x[h][j] = load_chunk(rx, (at.xo[j] + (uint32_t)(2 * I) * h) | (last ? tail : 0u), 128u * (uint32_t)at.st);
+    };
+    // (first: a wait that has to do for both leaves the others in flight)
+    if (at.n > kMoePacked) {
+#pragma unroll
+      for (int h = 1; h < 3; ++h)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) load_x(h, j);
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       t.w[j] = *reinterpret_cast<const u32x4*>(at.w[j] + (last && out ? -8 * lk : 64 * at.st));
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        t.x[h][j] = load_chunk(rx, (at.xo[j] + (uint32_t)(2 * I) * h) | (last ? tail : 0u), 128u * (uint32_t)at.st);
+      load_x(0, j);
     }
   };
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -436,19 +471,35 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_down(MoeParams p) {
       load(ahead, next);
       if (now.st == steps - 1 && out) t.w[0] = t.w[1] = u32x4{0u, 0u, 0u, 0u};
       to_fragments(t.w, turn[wave], lane);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      auto multiply = [&](int h) __attribute__((always_inline)) {
         to_fragments(t.x[h], turn[wave], lane);
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc = mfma_bf16(t.x[h][j], t.w[j], acc);
+      };
+      multiply(0);
+      if (now.n > kMoePacked) {
+        multiply(1);
+        multiply(2);
       }
     };
     auto leave = [&](int i) __attribute__((always_inline)) {
       if (now.st == steps - 1 || i == hi - 1) {
+        if (now.n > kMoePacked) {
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          const int m = 4 * lg + f;
-          if (m < now.n) sums[wave][tab->tok[now.s + m]][lx] += acc[f];
+          for (int f = 0; f < 4; ++f) {
+            const int m = 4 * lg + f;
+            if (m < now.n) sums[wave][tab->tok[now.s + m]][lx] += acc[f];
+          }
+        } else {  // the parts' rows meet in the wave's own LDS
+          float* rows = reinterpret_cast<float*>(turn[wave]);
+#pragma unroll
+          for (int f = 0; f < 4; ++f) rows[16 * (4 * lg + f) + lx] = acc[f];
+          __builtin_amdgcn_wave_barrier();
+          for (int i = lane; i < 16 * now.n; i += 64) {
+            const float* r = rows + i;
+            sums[wave][tab->tok[now.s + (i >> 4)]][lx] += r[0] + r[16 * kMoePacked] + r[32 * kMoePacked];
+          }
+          __builtin_amdgcn_wave_barrier();
         }
         acc = f32x4{0.f, 0.f, 0.f, 0.f};
       }
@@ -534,7 +585,6 @@ __global__ void __launch_bounds__(kMoeManyWaves * 64) moe_gate_up_many(MoeParams
   __shared__ f32x4 turn[kMoeManyWaves][128];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lx = lane & 15, lg = lane >> 4;
   const int lr = lane >> 3, lk = lane & 7;  // of what is loaded (to_fragments)
   const MoeTables* tab = p.tab;
   const int H = p.H, steps = (H + 63) >> 6, cols = (p.I + 15) >> 4;
@@ -649,13 +699,15 @@ __global__ void __launch_bounds__(kMoeManyWaves * 64) moe_gate_up_many(MoeParams
 #pragma unroll
         for (int f = 0; f < 4; ++f) v[h][f] += u[f];
       }
-    if (c0 + lx >= p.I) continue;
+    // (opaque, as in load: 2 spilled)
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    if (c0 + (l & 15) >= p.I) continue;
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
-      const int m = 16 * a + 4 * lg + f;
+      const int m = 16 * a + 4 * (l >> 4) + f;
       if (m >= n) continue;
-      uint16_t* o = p.mid + (int64_t)(s + m) * 2 * p.I + c0 + lx;
-      split_bf16(tab->wt[s + m] * swiglu(v[0][f], v[1][f]), o, o + p.I);
+      moe_leave(p, s + m, c0 + (l & 15), tab->wt[s + m] * swiglu(v[0][f], v[1][f]));
     }
   }
 }
@@ -664,7 +716,7 @@ __global__ void __launch_bounds__(kMoeManyWaves * 64) moe_gate_up_many(MoeParams
 // leaves its sums for each of the group's rows; moe_combine adds a token's.
 template <int GB, int SPW>
 __global__ void __launch_bounds__(kMoeManyWaves * 64) moe_down_many(MoeParams p) {
-  static_assert(SPW % 2 == 0 && GB * SPW <= 4, "x in 64 registers, two steps in turn");
+  static_assert(GB * SPW <= 2, "x in 48 registers");
   __shared__ f32x4 red[2][kMoeManyWaves][GB][64];
   __shared__ f32x4 turn[kMoeManyWaves][128];
   const int lane = threadIdx.x & 63;
@@ -698,9 +750,10 @@ __global__ void __launch_bounds__(kMoeManyWaves * 64) moe_down_many(MoeParams p)
   Step t[2];
   enter();
   load(0, t[0]);
-  u32x4 x[GB][SPW][2][2];  // (high and low parts)
+  u32x4 x[GB][SPW][3][2];
   int q = -1, c = lc, s = 0, n = 0, slice = 0;
-  for (int unit = u0; unit < u1; ++unit) {
+  // `now` and `then`: the two steps in turn, now the unit's first
+  auto one = [&](int unit, Step& now, Step& then) __attribute__((always_inline)) {
     if (q < 0 || c == cols) {
       q = q < 0 ? lq : q + 1;
       c = unit == u0 ? c : 0;
@@ -708,7 +761,7 @@ __global__ void __launch_bounds__(kMoeManyWaves * 64) moe_down_many(MoeParams p)
       slice = q - g * p.slices;
       s = __builtin_amdgcn_readfirstlane(tab->start[g]);
       n = __builtin_amdgcn_readfirstlane(tab->rows[g]);
-      const __amdgpu_buffer_rsrc_t rx = moe_rows(p.mid + (int64_t)s * 2 * I, 2 * n, I);
+      const __amdgpu_buffer_rsrc_t rx = moe_rows(p.mid + (int64_t)s * 3 * I, 3 * n, I);
       const int first = slice * (kMoeManyWaves * SPW) + wave;
 #pragma unroll
       for (int a = 0; a < GB; ++a) {
@@ -716,12 +769,12 @@ __global__ void __launch_bounds__(kMoeManyWaves * 64) moe_down_many(MoeParams p)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int m = 16 * a + 8 * j + lr;
-          xo[j] = m < n ? (uint32_t)m * (uint32_t)I * 4u : 0x80000000u;
+          xo[j] = m < n ? (uint32_t)m * (uint32_t)I * 6u : 0x80000000u;
         }
 #pragma unroll
         for (int i = 0; i < SPW; ++i)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < 3; ++h)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
               x[a][i][h][j] = step_chunk(rx, xo[j] + (uint32_t)(2 * I) * h, first + kMoeManyWaves * i, lk, I, steps);
@@ -731,29 +784,30 @@ __global__ void __launch_bounds__(kMoeManyWaves * 64) moe_down_many(MoeParams p)
 #pragma unroll
         for (int i = 0; i < SPW; ++i)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) to_fragments<GB == 1>(x[a][i][h], turn[wave], lane);
+          for (int h = 0; h < 3; ++h) to_fragments<GB == 1>(x[a][i][h], turn[wave], lane);
     }
     f32x4 acc[GB];
 #pragma unroll
     for (int a = 0; a < GB; ++a) acc[a] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < SPW; ++i) {
+      Step &used = i & 1 ? then : now, &next = i & 1 ? now : then;
       if (i + 1 < SPW) {
-        load(i + 1, t[(i + 1) & 1]);
+        load(i + 1, next);
       } else {
         if (unit + 1 < u1 && ++lc == cols) {
           lc = 0;
           ++lq;
         }
         enter();
-        load(0, t[0]);
+        load(0, next);
       }
-      u32x4(&w)[2] = t[i & 1].w;
+      u32x4(&w)[2] = used.w;
       to_fragments<GB == 1>(w, turn[wave], lane);
 #pragma unroll
       for (int a = 0; a < GB; ++a)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 3; ++h)
 #pragma unroll
           for (int j = 0; j < 2; ++j) acc[a] = mfma_bf16(x[a][i][h][j], w[j], acc[a]);
     }
@@ -764,7 +818,7 @@ __global__ void __launch_bounds__(kMoeManyWaves * 64) moe_down_many(MoeParams p)
     const int n0 = 16 * c;
     ++c;
     const int a = (wave - (unit - u0) * GB) & (kMoeManyWaves - 1);
-    if (a >= GB || 16 * a >= n) continue;
+    if (a >= GB || 16 * a >= n) return;
     f32x4 v = set[0][a][lane];
 #pragma unroll 5
     for (int w = 1; w < kMoeManyWaves; ++w) {
@@ -772,12 +826,19 @@ __global__ void __launch_bounds__(kMoeManyWaves * 64) moe_down_many(MoeParams p)
 #pragma unroll
       for (int f = 0; f < 4; ++f) v[f] += u[f];
     }
-    if (n0 + lx >= p.H) continue;
+    if (n0 + lx >= p.H) return;
     float* o = p.part + ((int64_t)slice * p.T * p.k + s) * p.H + n0 + lx;
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
       const int m = 16 * a + 4 * lg + f;
       if (m < n) o[(int64_t)m * p.H] = v[f];
+    }
+  };
+  for (int unit = u0; unit < u1; ++unit) {
+    one(unit, t[0], t[1]);
+    // (an odd number of steps leaves the next unit's first in the other place)
+    if constexpr (SPW & 1) {
+      if (++unit < u1) one(unit, t[1], t[0]);
     }
   }
 }

@@ -372,8 +372,8 @@ mm_status mm_linear_lora(const void* x, const void* W, const void* A, const void
  * zeros.  A logit of NaN counts as the largest; it, or one of plus infinity, makes the
  * token's weights and output NaN.
  * tokens <= 64, n_experts <= 512, top_k <= 16 and <= n_experts; H and I multiples of 8, at
- * most 2^18.  Sums are fp32; the products between the two layers are kept with 16 bits of
- * significand (in two parts: of an infinity in W_down the sum may be NaN).  tokens == 0 is a no-op.
+ * most 2^18.  Sums and what stands between the two layers are fp32 (the latter in three bf16 parts: of an
+ * infinity in W_down the sum may be NaN).  tokens == 0 is a no-op.
  * The workspace (size from the function below, host arithmetic only; 256-byte
  * aligned, any contents) is needed by every other call; two calls in flight at once
  * must not share it. */
