@@ -8,8 +8,8 @@
 // reading W once; lora_rows streams it and adds B (s_a A_a x[m]) to the same sums.
 // Many rows: lora_tile takes the adapters' terms as further steps of K; where K is
 // cut into slices, lora_join adds them.
-// v = s_a A_a x enters the products with B as two bf16 numbers, high and low part, 16
-// bits of significand: as one, its rounding would be as large as the output's own.
+// v = s_a A_a x, fp32, enters the products with B as three bf16 numbers whose sum it is: as one, its
+// rounding would be as large as the output's own, as two (16 bits of significand) up to 2^-16 of v would be lost.
 #pragma once
 
 #include <type_traits>
@@ -32,7 +32,7 @@ struct LoraParams {
   const uint16_t* bias;   // [N] or null
   uint16_t* out;          // [M][N]
   float* low;             // [low_slices][M][R]: parts of A x
-  uint16_t* v;            // [M][2][R]: s A x, high and low parts
+  uint16_t* v;            // [M][3][R]: s A x, its parts
   float* acc;             // [slices][M][N]: parts of W x
   int M, N, K, R, L;
   int low_slices, low_k;  // slices of K of low_k (a multiple of 64)
@@ -50,6 +50,9 @@ struct LoraTileRows {
   int adapter[256];
   uint64_t rows[256][4];
 };
+
+// Super-steps of 64 values of lora_tile that the parts of an adapter of rank R take.
+__device__ __forceinline__ int lora_steps(int R) { return (3 * R + 63) >> 6; }
 
 // The adapter of row `row`, -1 for none (past the last row, or an index that names none).
 __device__ __forceinline__ int lora_adapter(const LoraParams& p, int row) {
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(kLoraShrinkWaves * 64) lora_shrink(LoraParams 
 }
 
 // v of every row, 8 ranks (a chunk) to 16 threads: each loads the sums of one slice, and their sum
-// times the scale goes as two parts to put(row, chunk, high, low).  Rows without an
+// times the scale goes in its parts to put(row, chunk, parts).  Rows without an
 // adapter are left out.
 template <typename F>
 __device__ __forceinline__ void lora_fold_all(const LoraParams& p, int64_t thread, int64_t threads, F put) {
@@ -203,23 +206,19 @@ __device__ __forceinline__ void lora_fold_all(const LoraParams& p, int64_t threa
       for (int j = 0; j < 8; ++j) v[j >> 2][j & 3] += __shfl_xor(v[j >> 2][j & 3], d);
     if (a < 0 || s > 0) continue;
     const float scale = p.scale[a];
-    u32x4 hi, lo;
+    u32x4 part[3];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      uint16_t h[2], l[2];
-      split_bf16(v[j >> 1][2 * (j & 1)] * scale, &h[0], &l[0]);
-      split_bf16(v[j >> 1][2 * (j & 1) + 1] * scale, &h[1], &l[1]);
-      hi[j] = (uint32_t)h[0] | (uint32_t)h[1] << 16;
-      lo[j] = (uint32_t)l[0] | (uint32_t)l[1] << 16;
+      split_bf16(v[j >> 1][2 * (j & 1)] * scale, [&](int h, uint16_t u) { part[h][j] = u; });
+      split_bf16(v[j >> 1][2 * (j & 1) + 1] * scale, [&](int h, uint16_t u) { part[h][j] |= (uint32_t)u << 16; });
     }
-    put(m, c, hi, lo);
+    put(m, c, part);
   }
 }
 __device__ __forceinline__ void lora_fold_all(const LoraParams& p, int64_t thread, int64_t threads) {
-  lora_fold_all(p, thread, threads, [&](int m, int c, u32x4 hi, u32x4 lo) {
-    uint16_t* v = p.v + (int64_t)m * 2 * p.R + 8 * c;
-    *reinterpret_cast<u32x4*>(v) = hi;
-    *reinterpret_cast<u32x4*>(v + p.R) = lo;
+  lora_fold_all(p, thread, threads, [&](int m, int c, const u32x4(&part)[3]) {
+#pragma unroll
+    for (int h = 0; h < 3; ++h) *reinterpret_cast<u32x4*>(p.v + ((int64_t)m * 3 + h) * p.R + 8 * c) = part[h];
   });
 }
 
@@ -277,7 +276,7 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
   static_assert(SPW % 2 == 0 && MB * SPW <= 8, "x in 64 registers, two steps in turn");
   __shared__ f32x4 red[2][kLoraWaves][MB][64];
   __shared__ f32x4 turn[kLoraWaves][128];
-  __shared__ u32x4 v[FINISH ? 16 * MB : 1][2][kLoraMaxRank / 8];
+  __shared__ u32x4 v[FINISH ? 16 * MB : 1][3][kLoraMaxRank / 8];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lx = lane & 15, lg = lane >> 4;
@@ -336,9 +335,9 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
       }
       ++nth;
     });
-    lora_fold_all(p, threadIdx.x, kLoraWaves * 64, [&](int m, int c, u32x4 hi, u32x4 lo) {
-      v[m][0][c] = hi;
-      v[m][1][c] = lo;
+    lora_fold_all(p, threadIdx.x, kLoraWaves * 64, [&](int m, int c, const u32x4(&part)[3]) {
+#pragma unroll
+      for (int h = 0; h < 3; ++h) v[m][h][c] = part[h];
     });
   } else {
     lora_fold_all(p, (int64_t)(blockIdx.y * gridDim.x + blockIdx.x) * (kLoraWaves * 64) + threadIdx.x,
@@ -376,13 +375,14 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
 #pragma unroll
         for (int b = 0; b < MB; ++b) {
           if (!((same[q] >> (16 * b)) & 0xffff)) continue;
-          u32x4 hi = {0u, 0u, 0u, 0u}, lo = {0u, 0u, 0u, 0u};
-          if (r < p.R && ((same[q] >> (16 * b + lx)) & 1)) {
-            hi = v[16 * b + lx][0][r >> 3];
-            lo = v[16 * b + lx][1][r >> 3];
+          const bool mine = r < p.R && ((same[q] >> (16 * b + lx)) & 1);
+          f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < 3; ++h) {
+            u32x4 part = {0u, 0u, 0u, 0u};
+            if (mine) part = v[16 * b + lx][h][r >> 3];
+            d = mfma_bf16(part, wf, d);
           }
-          f32x4 d = mfma_bf16(hi, wf, f32x4{0.f, 0.f, 0.f, 0.f});
-          d = mfma_bf16(lo, wf, d);
           // (0 times what is not finite: other rows' sums are left alone)
 #pragma unroll
           for (int f = 0; f < 4; ++f)
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(256) lora_join(LoraParams p) {
     const bool mine = (same >> lx) & 1;
     for (int r0 = 0; r0 < p.R; r0 += 32) {
       const int r = r0 + 8 * lg;
-      u32x4 wf[2][2], hi = {0u, 0u, 0u, 0u}, lo = {0u, 0u, 0u, 0u};
+      u32x4 wf[2][2], part[3];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -461,17 +461,18 @@ __global__ void __launch_bounds__(256) lora_join(LoraParams p) {
           if (r < p.R) wf[c][h] = *reinterpret_cast<const u32x4*>(p.B + ((int64_t)a * p.N + n) * p.R + r);
         }
       }
-      if (r < p.R && mine) {
-        const uint16_t* v = p.v + (int64_t)m * 2 * p.R + r;
-        hi = *reinterpret_cast<const u32x4*>(v);
-        lo = *reinterpret_cast<const u32x4*>(v + p.R);
+#pragma unroll
+      for (int h = 0; h < 3; ++h) {
+        part[h] = u32x4{0u, 0u, 0u, 0u};
+        if (r < p.R && mine) part[h] = *reinterpret_cast<const u32x4*>(p.v + ((int64_t)m * 3 + h) * p.R + r);
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          f32x4 d = mfma_bf16(wf[c][h], hi, f32x4{0.f, 0.f, 0.f, 0.f});
-          d = mfma_bf16(wf[c][h], lo, d);
+          f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 3; ++i) d = mfma_bf16(wf[c][h], part[i], d);
           // (0 times what is not finite: other rows' sums are left alone)
 #pragma unroll
           for (int f = 0; f < 4; ++f) acc[c][h][f] += mine ? d[f] : 0.f;
@@ -533,16 +534,18 @@ __global__ void __launch_bounds__(512) lora_join_few(LoraParams p) {
       for (int b = 0; b < MB; ++b) {
         if (!((same >> (16 * b)) & 0xffff)) continue;
         const bool mine = (same >> (16 * b + lx)) & 1;
-        u32x4 hi = {0u, 0u, 0u, 0u}, lo = {0u, 0u, 0u, 0u};
-        if (r < p.R && mine) {
-          const uint16_t* v = p.v + (int64_t)(m0 + 16 * b + lx) * 2 * p.R + r;
-          hi = *reinterpret_cast<const u32x4*>(v);
-          lo = *reinterpret_cast<const u32x4*>(v + p.R);
+        u32x4 part[3];
+#pragma unroll
+        for (int h = 0; h < 3; ++h) {
+          part[h] = u32x4{0u, 0u, 0u, 0u};
+          if (r < p.R && mine)
+            part[h] = *reinterpret_cast<const u32x4*>(p.v + ((int64_t)(m0 + 16 * b + lx) * 3 + h) * p.R + r);
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          f32x4 d = mfma_bf16(wf[q], hi, f32x4{0.f, 0.f, 0.f, 0.f});
-          d = mfma_bf16(wf[q], lo, d);
+          f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < 3; ++h) d = mfma_bf16(wf[q], part[h], d);
 #pragma unroll
           for (int f = 0; f < 4; ++f) acc[b][q][f] += mine ? d[f] : 0.f;
         }
@@ -675,9 +678,9 @@ __device__ __forceinline__ void lora_mark(const LoraParams& p, int mb, int nb, i
 // has one instruction).
 //
 // The adapters' terms are further super-steps of the same sums: for each adapter among a
-// tile's rows ceil(R / 32) of them, in which x stands for the rows' v, high parts then
-// low parts (rows of other adapters lie past the buffer's end: zeros), and W for the adapter's
-// B, twice.  So a tile of one adapter of rank 32 costs one super-step more.
+// tile's rows ceil(3 R / 64) of them, in which x stands for the rows' v, part after
+// part (rows of other adapters lie past the buffer's end: zeros), and W for the adapter's
+// B, three times.  So a tile of one adapter of rank 16 costs one super-step more.
 // Bound by issuing MFMAs and by L2: 8192^3, rank 16 850 us (1290 TFLOP/s; MFMAs in 75 % of a working
 // CU's cycles, 11 TB/s out of L2).  Where rows start inside a 128-byte line (K not a
 // multiple of 64) each copy touches two: 2047 x 3001 x 4104 75 us, 1.26 GB out of L2 (17 TB/s).
@@ -746,7 +749,7 @@ __global__ void __launch_bounds__(256, SX * FM + SW * FN <= 10 ? 2 : 1) lora_til
       *q1 = min(*q0 + p->slice_steps, KS);
     } else {
       *q0 = 0;
-      *q1 = KS + __builtin_amdgcn_readfirstlane(p->tiles[*tm].count) * ((p->R + 31) >> 5);
+      *q1 = KS + __builtin_amdgcn_readfirstlane(p->tiles[*tm].count) * lora_steps(p->R);
     }
   };
   // offsets of super-step q: of K, the ragged last one's chunks past K out of range
@@ -765,35 +768,43 @@ __global__ void __launch_bounds__(256, SX * FM + SW * FN <= 10 ? 2 : 1) lora_til
 #pragma unroll
     for (int c = 0; c < CW; ++c) vw[c] = base(wq, row_w(c, l.row), l.chunk[c & 1], K);
   };
-  // or of an adapter: piece e of its 2 R values
+  // or of an adapter: piece e of its 3 R values
   auto extra_x = [&]() __attribute__((always_inline)) {
     const auto* p = args();
     const Place l = place();
-    const int ES = (p->R + 31) >> 5, a = (xq - KS) / ES, e = (xq - KS) - a * ES;
-    const uint32_t R4 = 4u * (uint32_t)p->R;
+    const int ES = lora_steps(p->R), a = (xq - KS) / ES, e = (xq - KS) - a * ES;
+    const uint32_t R6 = 6u * (uint32_t)p->R;
+    if (e > 0) {  // the same rows, a piece further
+#pragma unroll
+      for (int c = 0; c < CX; ++c)
+        vx[c] = vx[c] < 0x80000000u && 128u * (uint32_t)e + l.chunk[c & 1] < R6 ? vx[c] + 128u : 0x80000000u;
+      return;
+    }
     int tm, tn, q0, q1;
     unit(min(xi, my_units - 1), &tm, &tn, &q0, &q1);
-    rx = tile_rows(p->v, (int64_t)tm * BM, p->M, BM, R4);
+    rx = tile_rows(p->v, (int64_t)tm * BM, p->M, BM, R6);
     const uint64_t rows = p->tiles[tm].rows[a][(8 * wave * CX) >> 6] >> ((8 * wave * CX) & 63);
 #pragma unroll
     for (int c = 0; c < CX; ++c) {
-      const uint32_t at = 128u * (uint32_t)e + l.chunk[c & 1];
-      vx[c] = at < R4 && ((rows >> (8 * c + l.row)) & 1) ? row_x(c, l.row) * R4 + at : 0x80000000u;
+      const uint32_t at = l.chunk[c & 1];
+      vx[c] = at < R6 && ((rows >> (8 * c + l.row)) & 1) ? row_x(c, l.row) * R6 + at : 0x80000000u;
     }
   };
   auto extra_w = [&]() __attribute__((always_inline)) {
     const auto* p = args();
     const Place l = place();
-    const int ES = (p->R + 31) >> 5, a = (wq - KS) / ES, e = (wq - KS) - a * ES;
+    const int ES = lora_steps(p->R), a = (wq - KS) / ES, e = (wq - KS) - a * ES;
     const uint32_t R2 = 2u * (uint32_t)p->R;
-    int tm, tn, q0, q1;
-    unit(min(wi, my_units - 1), &tm, &tn, &q0, &q1);
-    const int64_t first = (int64_t)__builtin_amdgcn_readfirstlane(p->tiles[tm].adapter[a]) * p->N;
-    rw = tile_rows(p->B, first + (int64_t)tn * BN, first + p->N, BN, R2);
+    if (e == 0) {  // (later pieces: the same rows)
+      int tm, tn, q0, q1;
+      unit(min(wi, my_units - 1), &tm, &tn, &q0, &q1);
+      const int64_t first = (int64_t)__builtin_amdgcn_readfirstlane(p->tiles[tm].adapter[a]) * p->N;
+      rw = tile_rows(p->B, first + (int64_t)tn * BN, first + p->N, BN, R2);
+    }
 #pragma unroll
     for (int c = 0; c < CW; ++c) {
       const uint32_t at = 128u * (uint32_t)e + l.chunk[c & 1];
-      vw[c] = at < 2 * R2 ? row_w(c, l.row) * R2 + (at >= R2 ? at - R2 : at) : 0x80000000u;
+      vw[c] = at < 3 * R2 ? row_w(c, l.row) * R2 + (at < R2 ? at : at < 2 * R2 ? at - R2 : at - 2 * R2) : 0x80000000u;
     }
   };
   // (past the last unit that one again, never read)

@@ -417,7 +417,7 @@ mm_status lora_plan(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, LoraP
   p->low_k = std::max<int64_t>(512, cdiv(cdiv(K, want), 64) * 64);
   p->low_slices = cdiv(K, p->low_k);
   p->low = round256(p->low_slices * M * R * 4);
-  p->v = round256(M * 2 * R * 2);
+  p->v = round256(M * 3 * R * 2);
   if (M <= kLoraRows) {
     p->mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
     const int64_t steps = cdiv(K, 64), most = 8 / p->mb;

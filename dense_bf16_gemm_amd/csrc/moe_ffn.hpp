@@ -214,19 +214,6 @@ __device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// A float as two bf16: the high part cut, the low part rounded (2^-16 of the
-// value together).  What is not finite stays in the high part.
-__device__ __forceinline__ void split_bf16(float v, uint16_t* hi, uint16_t* lo) {
-  const uint32_t b = __builtin_bit_cast(uint32_t, v);
-  if ((b & 0x7f800000u) == 0x7f800000u) {
-    *hi = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
-    *lo = 0;
-    return;
-  }
-  *hi = (uint16_t)(b >> 16);
-  *lo = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v - __builtin_bit_cast(float, b & 0xffff0000u)));
-}
-
 // A float as the sum of three bf16: 8 bits of the significand each, cut, so that the sum is exact
 // (to 2^-133, the last bit of a bf16).  put(i, part i); what is not finite stays in part 0.
 template <typename F>

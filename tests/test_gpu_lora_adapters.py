@@ -1,0 +1,59 @@
+"""The adapters' term of the linear layer with an adapter per row, on the GPU: what it
+keeps between its two products, and what a row's bits depend on.
+"""
+import pytest
+import torch
+
+import dense_bf16_gemm_amd as mm
+import layer_ref as ref
+from test_gpu_decoder import dev, gen  # noqa: F401 (dev is a fixture)
+from test_gpu_linear_lora import choices, inputs, on
+
+pytestmark = pytest.mark.gpu
+
+# rows in one launch with K whole (one and two blocks of 16) and with K in slices, up to 64, tiles with K
+# whole and in slices; ranks whose parts end inside a step of 32 or 64
+SHAPES = [(1, 70, 136, 8, 2), (9, 130, 1032, 24, 3), (16, 513, 4104, 16, 16), (30, 257, 2056, 72, 5), (32, 64, 4096, 256, 4),
+          (5, 333, 8264, 40, 3), (32, 70, 4104, 16, 9), (64, 257, 1024, 32, 30), (50, 130, 2056, 136, 4), (65, 70, 200, 16, 3),
+          (130, 515, 4104, 24, 3), (200, 517, 1032, 8, 12), (300, 300, 72, 72, 6), (513, 1030, 392, 64, 7), (2100, 2100, 328, 40, 8),
+          (700, 3000, 1032, 16, 5), (260, 140, 136, 256, 3)]
+
+
+@pytest.mark.parametrize("M,N,K,R,L", SHAPES)
+@pytest.mark.parametrize("how", ["mixed", "runs"])
+def test_linear_lora_keeps_all_bits_between_the_products(dev, M, N, K, R, L, how):  # noqa: F811
+    """Values s A x of 18 to 21 bits, neighbours of which differ by less than 2^10: B takes such
+    differences, so that one held with fewer bits is off by whole numbers.  Everything is a
+    whole number below 2^24, so outputs have to match bit for bit."""
+    g = gen(M + N + K + R)
+
+    def sparse(shape, top):
+        """Whole numbers up to top, four or so of them along the last axis, the first and last two of it among them."""
+        v = torch.randint(-top, top + 1, shape, generator=g)
+        keep = torch.randint(0, max(1, shape[-1] // 2), shape, generator=g) == 0
+        keep[..., 0] = keep[..., -1] = keep[..., -2] = True
+        return (v * keep).float()
+
+    x = torch.randint(-127, 128, (M, K), generator=g).float()
+    x[:, :24] = torch.randint(64, 128, (M, 24), generator=g).float()
+    W = sparse((N, K), 1)
+    A = sparse((L, R, K), 255)
+    A[:, :, :24] = 255.0  # (24 * 64 * 255 is 2^18.6)
+    A[:, 1::2] = A[:, ::2]
+    A[:, 1::2, -1] = torch.randint(-3, 4, (L, R // 2), generator=g) + A[:, 1::2, -1].clamp(-252, 252)
+    A[:, ::2, -1] = A[:, ::2, -1].clamp(-252, 252)
+    B = torch.zeros((L, N, R))
+    pair = torch.randint(0, R // 2, (L, N, 1), generator=g)
+    B.scatter_(2, 2 * pair, 1.0)
+    B.scatter_(2, 2 * pair + 1, -1.0)
+    scale = 2.0 ** torch.randint(0, 2, (L,), generator=g).float()
+    bf = [t.bfloat16() for t in (x, W, A, B)]
+    assert all(torch.equal(b.float(), t) for b, t in zip(bf, (x, W, A, B)))
+    index = choices(M, L, how, g)
+    index[0].clamp_(min=0)
+    low = x.double() @ A.double().reshape(L * R, K).t()
+    size = x.double().abs() @ A.double().abs().reshape(L * R, K).t()
+    assert float(size.max()) * 2 < 2 ** 22 and float(low.abs().min()) > 2 ** 17 and bool((low.long() % 2 == 1).any())
+    got = mm.linear_lora(*on(dev, *bf, index, scale)).cpu()
+    want = ref.lora(*bf, index, scale)
+    assert torch.equal(got, want.float().bfloat16())
