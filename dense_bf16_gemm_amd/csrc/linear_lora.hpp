@@ -265,8 +265,9 @@ __global__ void __launch_bounds__(256) lora_fold(LoraParams p, LoraTileRows* til
 // step's loads are issued one step ahead, across blocks.  The waves' sums of a block meet
 // in LDS (two sets in turn: one barrier per block) and are added in wave order, by
 // another wave for each block.
-// FINISH (K in one slice): v comes into LDS first, the adapters' terms join the sums
-// here, each adapter on a wave, and the output is written.  Else lora_join_few does both,
+// FINISH (K in one slice): v comes into LDS first, each adapter's terms are made by a
+// wave and added to the rows' sums after those of W x (so that no row's rounding depends on which wave that is,
+// and with it on other rows' adapters), and the output is written.  Else lora_join_few does both,
 // and v is left in memory for it.
 // Bound by reading W: 16 x 28672 x 8192 95 us (5.0 TB/s), 1 x 8192 x 8192 25 (5.4), 64 x 14336 x
 // 4096 26 (4.5, and 7 MB of parts).  With x read from L2 for every block the first took 150; with x
@@ -277,6 +278,7 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
   __shared__ f32x4 red[2][kLoraWaves][MB][64];
   __shared__ f32x4 turn[kLoraWaves][128];
   __shared__ u32x4 v[FINISH ? 16 * MB : 1][3][kLoraMaxRank / 8];
+  __shared__ f32x4 term[2][FINISH ? MB : 1][64];  // B v of rows with an adapter, in the order of red
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lx = lane & 15, lg = lane >> 4;
@@ -317,7 +319,7 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
   }
   // this wave's adapters (of at most 16 MB) and their rows
   int mine[MB];
-  uint64_t same[MB];
+  uint64_t same[MB], adapted = 0;  // (adapted: all rows with an adapter)
 #pragma unroll
   for (int q = 0; q < MB; ++q) {
     mine[q] = -1;
@@ -326,6 +328,7 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
   if constexpr (FINISH) {
     int nth = 0;
     each_adapter(lora_adapter(p, lane), [&](int a, uint64_t s) {
+      adapted |= s;
 #pragma unroll
       for (int q = 0; q < MB; ++q) {
         if (nth == kLoraWaves * q + wave) {
@@ -368,6 +371,9 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
     for (int q = 0; q < MB; ++q) {
       if (!FINISH || mine[q] < 0) continue;
       const uint16_t* bw = p.B + ((int64_t)mine[q] * p.N + min(n0 + lx, p.N - 1)) * p.R;
+      f32x4 d[MB];
+#pragma unroll
+      for (int b = 0; b < MB; ++b) d[b] = f32x4{0.f, 0.f, 0.f, 0.f};
       for (int r0 = 0; r0 < p.R; r0 += 32) {
         const int r = r0 + 8 * lg;
         u32x4 wf = {0u, 0u, 0u, 0u};
@@ -375,19 +381,22 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
 #pragma unroll
         for (int b = 0; b < MB; ++b) {
           if (!((same[q] >> (16 * b)) & 0xffff)) continue;
-          const bool mine = r < p.R && ((same[q] >> (16 * b + lx)) & 1);
-          f32x4 d = {0.f, 0.f, 0.f, 0.f};
+          const bool have = r < p.R && ((same[q] >> (16 * b + lx)) & 1);
 #pragma unroll
           for (int h = 0; h < 3; ++h) {
             u32x4 part = {0u, 0u, 0u, 0u};
-            if (mine) part = v[16 * b + lx][h][r >> 3];
-            d = mfma_bf16(part, wf, d);
+            if (have) part = v[16 * b + lx][h][r >> 3];
+            d[b] = mfma_bf16(part, wf, d[b]);
           }
-          // (0 times what is not finite: other rows' sums are left alone)
-#pragma unroll
-          for (int f = 0; f < 4; ++f)
-            if ((same[q] >> (16 * b + 4 * lg + f)) & 1) acc[b][f] += d[f];
         }
+      }
+      // (its rows only: 0 times what is not finite leaves other rows alone)
+#pragma unroll
+      for (int b = 0; b < MB; ++b) {
+        float* to = reinterpret_cast<float*>(&term[round & 1][b][lane]);
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+          if ((same[q] >> (16 * b + 4 * lg + f)) & 1) to[f] = d[b][f];
       }
     }
     f32x4(*set)[MB][64] = red[round & 1];
@@ -405,6 +414,11 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
     }
     const int n = n0 + lx;
     if (n >= p.N) continue;
+    if constexpr (FINISH) {
+      const f32x4 d = term[round & 1][b][lane];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) s[f] += (adapted >> (16 * b + 4 * lg + f)) & 1 ? d[f] : 0.f;
+    }
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
       const int m = 16 * b + 4 * lg + f;

@@ -348,7 +348,8 @@ mm_status mm_layer_norm_backward(const void* dy, const void* h, const void* weig
  *           N at most 2^27 - 16;  M at most 2^21 - 32
  * Sums and scale * (A x) are fp32 (the latter enters the second product in three bf16 parts: of an
  * infinity in B the sum may be NaN).  What an adapter
- * holds reaches the rows that name it and no others.  rank == 0, adapters == 0 or K == 0 is mm_linear.
+ * holds reaches the rows that name it and no others, and a row's bits do not depend on the other rows' adapters.
+ * rank == 0, adapters == 0 or K == 0 is mm_linear.
  * The workspace (size from the function below, a device query; 256-byte aligned, any
  * contents) is needed by every other call of M > 0 and N > 0; two calls in flight at
  * once must not share it.  Other arguments, the epilogue and errors as for mm_linear. */

@@ -57,3 +57,33 @@ def test_linear_lora_keeps_all_bits_between_the_products(dev, M, N, K, R, L, how
     got = mm.linear_lora(*on(dev, *bf, index, scale)).cpu()
     want = ref.lora(*bf, index, scale)
     assert torch.equal(got, want.float().bfloat16())
+
+
+# rows in one launch, in slices of K, up to 64, tiles with K whole (256 columns to a tile: many) and in slices
+@pytest.mark.parametrize("M,N,K,R", [(5, 4096, 4096, 16), (16, 4096, 4096, 16), (16, 2048, 8192, 64), (30, 4096, 2056, 24),
+                                     (32, 4096, 4096, 16), (12, 4096, 8264, 16), (32, 2048, 4104, 40), (40, 4096, 2056, 16),
+                                     (64, 4096, 4096, 16), (90, 4096, 1032, 24), (300, 2100, 1032, 16), (600, 4096, 520, 40)])
+def test_linear_lora_row_does_not_depend_on_other_rows_adapters(dev, M, N, K, R):  # noqa: F811
+    """The bits of a row stay when other rows take other adapters, more, fewer or none.
+
+    All rows are one, and the bias takes off what a sum is to 8 bits: of what is left, a sum in
+    another order changes bits that the output has."""
+    L = min(M, 40)
+    g = gen(M + K)
+    x = torch.randn((1, K), generator=g).bfloat16().expand(M, K).contiguous()
+    W = (torch.randn((N, K), generator=g) * K ** -0.5).bfloat16()
+    A = (torch.randn((L, R, K), generator=g) * K ** -0.5).bfloat16()
+    B = (torch.randn((L, N, R), generator=g) * R ** -0.5).bfloat16()
+    A[1:], B[1:] = A[:1].clone(), B[:1].clone()  # (the same in all, so that one bias does for all)
+    index = torch.arange(M, dtype=torch.int32) % L
+    scale = torch.full((L,), 1.25)
+    d = on(dev, x, W, A, B, index, scale)
+    bias = -mm.linear_lora(*d)[0]
+    want = mm.linear_lora(*d, bias, "bias")
+    assert float((want != 0).float().mean()) > 0.9
+    rows = torch.arange(M)
+    for kept in (rows % 2 == 1, rows % 3 == 2, rows >= M - 2, rows >= M // 2):
+        for others in (torch.full_like(index, -1), index.flip(0), (index * 7 + 3) % L, torch.zeros_like(index)):
+            other = torch.where(kept, index, others).int().to(dev)
+            got = mm.linear_lora(*d[:4], other, scale.to(dev), bias, "bias")
+            assert torch.equal(got[kept.to(dev)], want[kept.to(dev)])
