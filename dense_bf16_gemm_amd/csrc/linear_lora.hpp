@@ -61,6 +61,21 @@ __device__ __forceinline__ int lora_adapter(const LoraParams& p, int row) {
   return (unsigned)a < (unsigned)p.L ? a : -1;
 }
 
+// B v of row m and column n, term by term, for sums that came out NaN: of the three parts of a v, 8 bits
+// or less leave some 0, and 0 times an infinity of B is NaN where v times it is infinite.  v: the
+// row's parts [3][stride].
+__device__ __forceinline__ float lora_term(const LoraParams& p, int m, int n, const uint16_t* v, int stride) {
+  const uint16_t* b = p.B + ((int64_t)lora_adapter(p, m) * p.N + n) * p.R;
+  float sum = 0.f;
+#pragma unroll 1
+  for (int r = 0; r < p.R; ++r)
+    sum = __builtin_fmaf(bf16_float(v[r]) + bf16_float(v[stride + r]) + bf16_float(v[2 * stride + r]), bf16_float(b[r]), sum);
+  return sum;
+}
+__device__ __forceinline__ float lora_term(const LoraParams& p, int m, int n) {
+  return lora_term(p, m, n, p.v + (int64_t)m * 3 * p.R, p.R);
+}
+
 // Calls f(adapter, its lanes) for every different adapter >= 0 among a wave's lanes, in
 // the order of their first lanes.
 template <typename F>
@@ -415,9 +430,22 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
     const int n = n0 + lx;
     if (n >= p.N) continue;
     if constexpr (FINISH) {
-      const f32x4 d = term[round & 1][b][lane];
+      f32x4 d = term[round & 1][b][lane];
+      bool again = false;
 #pragma unroll
-      for (int f = 0; f < 4; ++f) s[f] += (adapted >> (16 * b + 4 * lg + f)) & 1 ? d[f] : 0.f;
+      for (int f = 0; f < 4; ++f) {
+        if (!((adapted >> (16 * b + 4 * lg + f)) & 1)) d[f] = 0.f;
+        again |= d[f] != d[f] && s[f] == s[f];
+      }
+      if (again) {
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          const int m = 16 * b + 4 * lg + f;
+          if (d[f] != d[f]) d[f] = lora_term(p, m, n, reinterpret_cast<const uint16_t*>(v[m]), kLoraMaxRank);
+        }
+      }
+#pragma unroll
+      for (int f = 0; f < 4; ++f) s[f] += d[f];
     }
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
@@ -442,12 +470,12 @@ __global__ void __launch_bounds__(256) lora_join(LoraParams p) {
   const int m0 = blockIdx.y * 64 + 16 * wave, n0 = blockIdx.x * 64;
   if (m0 >= p.M) return;
   const int m = m0 + lx;
-  f32x4 acc[2][2];
+  f32x4 acc[2][2], term[2][2];
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const int n = n0 + 32 * c + 8 * lg;
     const float* at = p.acc + (int64_t)min(m, p.M - 1) * p.N;
-    acc[c][0] = acc[c][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    acc[c][0] = acc[c][1] = term[c][0] = term[c][1] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (int s = 0; s < p.slices; ++s, at += (int64_t)p.M * p.N) {
       f32x4 u[2];
       if (n + 8 <= p.N) {
@@ -489,12 +517,18 @@ __global__ void __launch_bounds__(256) lora_join(LoraParams p) {
           for (int i = 0; i < 3; ++i) d = mfma_bf16(wf[c][h], part[i], d);
           // (0 times what is not finite: other rows' sums are left alone)
 #pragma unroll
-          for (int f = 0; f < 4; ++f) acc[c][h][f] += mine ? d[f] : 0.f;
+          for (int f = 0; f < 4; ++f) term[c][h][f] += mine ? d[f] : 0.f;
         }
       }
     }
   });
   if (m >= p.M) return;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int c = i >> 3, h = (i >> 2) & 1, f = i & 3, n = n0 + 32 * c + 8 * lg + 4 * h + f;
+    if (term[c][h][f] != term[c][h][f] && acc[c][h][f] == acc[c][h][f] && n < p.N) term[c][h][f] = lora_term(p, m, n);
+    acc[c][h][f] += term[c][h][f];
+  }
   const bool has_bias = p.epi == EPI_BIAS || p.epi == EPI_BIAS_GELU;
   const bool gelu = p.epi == EPI_GELU || p.epi == EPI_BIAS_GELU;
 #pragma unroll
@@ -588,11 +622,17 @@ __global__ void __launch_bounds__(512) lora_join_few(LoraParams p) {
 #pragma unroll
       for (int f = 0; f < 4; ++f) sum[f] += u[f];
     }
+    f32x4 term = red[0][i][lane];
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
+    for (int w = 1; w < 8; ++w) {
       const f32x4 u = red[w][i][lane];
 #pragma unroll
-      for (int f = 0; f < 4; ++f) sum[f] += u[f];
+      for (int f = 0; f < 4; ++f) term[f] += u[f];
+    }
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      if (term[f] != term[f] && sum[f] == sum[f] && n + f < p.N) term[f] = lora_term(p, m, n + f);
+      sum[f] += term[f];
     }
     uint16_t o[4];
 #pragma unroll
@@ -668,22 +708,30 @@ __device__ __forceinline__ void lora_block(const LoraParams& p, float (&v)[16], 
   }
 }
 
-// NaN into those outputs of a wave's 32 x 32 block at (mb, nb) whose row of B, of the output
-// row's adapter, is not finite.
-__device__ __forceinline__ void lora_mark(const LoraParams& p, int mb, int nb, int lane) {
+// Those outputs of a wave's 32 x 32 block at (mb, nb) whose row of B, of the output row's adapter, is
+// not finite: the output has the class of the sum of those terms and of what is there (which the
+// other terms and the epilogue gave).
+__device__ __forceinline__ void lora_mark(const LoraParams& p, int mb, int nb, int lane, bool gelu) {
   const int m = mb + (lane & 31), a = lora_adapter(p, m);
   if (a < 0) return;
 #pragma unroll 1
   for (int n = nb + 16 * (lane >> 5); n < min(nb + 16 * (lane >> 5) + 16, p.N); ++n) {
     const uint16_t* b = p.B + ((int64_t)a * p.N + n) * p.R;
+    const uint16_t* v = p.v + (int64_t)m * 3 * p.R;
     bool odd = false;
+    float sum = 0.f;
 #pragma unroll 1
-    for (int r = 0; r < p.R; r += 8) {
-      const u32x4 u = *reinterpret_cast<const u32x4*>(b + r);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) odd |= (((u[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0;
+    for (int r = 0; r < p.R; ++r) {
+      if ((b[r] & 0x7f80) != 0x7f80) continue;
+      odd = true;
+      sum += (bf16_float(v[r]) + bf16_float(v[p.R + r]) + bf16_float(v[2 * p.R + r])) * bf16_float(b[r]);
     }
-    if (odd) p.out[(int64_t)m * p.N + n] = 0x7fc0;
+    if (!odd) continue;
+    uint16_t* o = p.out + (int64_t)m * p.N + n;
+    const float was = bf16_float(*o);
+    if (!__builtin_isfinite(was)) sum += was;
+    if (gelu) sum = gelu_tanh(sum);
+    *o = __builtin_bit_cast(uint16_t, static_cast<__bf16>(sum));
   }
 }
 
@@ -698,8 +746,9 @@ __device__ __forceinline__ void lora_mark(const LoraParams& p, int mb, int nb, i
 // Bound by issuing MFMAs and by L2: 8192^3, rank 16 850 us (1290 TFLOP/s; MFMAs in 75 % of a working
 // CU's cycles, 11 TB/s out of L2).  Where rows start inside a 128-byte line (K not a
 // multiple of 64) each copy touches two: 2047 x 3001 x 4104 75 us, 1.26 GB out of L2 (17 TB/s).
-// (A zero times an infinity or a NaN of B would be NaN in the other rows: zeros are taken
-// for them, and the adapter's rows get NaN in their columns at the end.)
+// (A zero times an infinity or a NaN of B would be NaN in the other rows: 1 with their sign is taken
+// for them, whose product has the class of theirs where v is not finite, and the outputs of the adapter's rows in
+// those columns get their class at the end.)
 // SPLIT: the instance for a K cut into slices; those leave their sums of W x for lora_join.
 template <int FM, int FN, int SX, int SW, bool SPLIT>
 __global__ void __launch_bounds__(256, SX * FM + SW * FN <= 10 ? 2 : 1) lora_tile(LoraParams p) {
@@ -946,7 +995,8 @@ __global__ void __launch_bounds__(256, SX * FM + SW * FN <= 10 ? 2 : 1) lora_til
         for (int i = 0; i < 8; ++i) {
           // (an exponent of ones carries into the sign's place)
           const uint32_t u = w[s][b].j[i >> 2][i & 3], odd = ((u & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-          w[s][b].j[i >> 2][i & 3] = u & ~((odd >> 15) * 0xffffu);
+          const uint32_t value = (odd >> 15) * 0x7fffu;  // (all but the sign)
+          w[s][b].j[i >> 2][i & 3] = (u & ~value) | (0x3f803f80u & value);
           any |= odd;
         }
       }
@@ -1074,7 +1124,7 @@ __global__ void __launch_bounds__(256, SX * FM + SW * FN <= 10 ? 2 : 1) lora_til
       __builtin_amdgcn_s_waitcnt(0);  // (after the stores above, some of the same places)
       order();
 #pragma unroll 1
-      for (int i = 0; i < FM * FN; ++i) lora_mark(p, m0 + 32 * (i / FN), n0 + 32 * (i % FN), el);
+      for (int i = 0; i < FM * FN; ++i) lora_mark(p, m0 + 32 * (i / FN), n0 + 32 * (i % FN), el, gelu);
     }
   }
   __builtin_amdgcn_s_waitcnt(0);  // (the copies past the last unit land before the workgroup ends)

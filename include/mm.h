@@ -346,8 +346,8 @@ mm_status mm_layer_norm_backward(const void* dy, const void* h, const void* weig
  *   scale   [adapters] fp32
  *   rank    a multiple of 8, at most 256;  K a multiple of 8, below 2^22;
  *           N at most 2^27 - 16;  M at most 2^21 - 32
- * Sums and scale * (A x) are fp32 (the latter enters the second product in three bf16 parts: of an
- * infinity in B the sum may be NaN).  What an adapter
+ * Sums and scale * (A x) are fp32, and an output that is not finite has the class of the
+ * definition's sum.  What an adapter
  * holds reaches the rows that name it and no others, and a row's bits do not depend on the other rows' adapters.
  * rank == 0, adapters == 0 or K == 0 is mm_linear.
  * The workspace (size from the function below, a device query; 256-byte aligned, any

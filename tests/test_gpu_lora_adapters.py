@@ -6,7 +6,7 @@ import torch
 
 import dense_bf16_gemm_amd as mm
 import layer_ref as ref
-from test_gpu_decoder import dev, gen  # noqa: F401 (dev is a fixture)
+from test_gpu_decoder import dev, gen, same_class  # noqa: F401 (dev is a fixture)
 from test_gpu_linear_lora import choices, inputs, on
 
 pytestmark = pytest.mark.gpu
@@ -87,3 +87,37 @@ def test_linear_lora_row_does_not_depend_on_other_rows_adapters(dev, M, N, K, R)
             other = torch.where(kept, index, others).int().to(dev)
             got = mm.linear_lora(*d[:4], other, scale.to(dev), bias, "bias")
             assert torch.equal(got[kept.to(dev)], want[kept.to(dev)])
+
+
+@pytest.mark.parametrize("M,N,K,R", [(1, 70, 64, 8), (9, 130, 1032, 24), (30, 70, 392, 40), (12, 130, 8264, 16), (32, 70, 4104, 8),
+                                     (50, 200, 520, 40), (90, 130, 1032, 16), (150, 130, 520, 16), (300, 2100, 264, 72),
+                                     (700, 3000, 1032, 16), (2100, 2100, 328, 8)])
+@pytest.mark.parametrize("epi", ["none", "gelu_tanh"])
+def test_linear_lora_infinities_of_B(dev, M, N, K, R, epi):  # noqa: F811
+    """An infinity in B gives its rows the infinity or NaN of the definition's sum, also where
+    values of A x are whole numbers (whose further parts are 0) or exactly 0."""
+    L = 4
+    (x, W, A, B, index, scale), _ = inputs(M, N, K, R, L, "mixed", M + N, exact=True)
+    index[0] = 1
+    A[1, 0], A[1, 1] = 0, 0                             # exactly 0: 0 times an infinity is NaN
+    A[2, 2] = 0
+    A[2, 2, :4] = torch.tensor([1.0, 0.5, 0.25, 2.0])
+    inf = float("inf")
+    for a, n, r, v in ((1, 3, 0, inf), (1, 4, 3, inf), (1, 5, 3, -inf), (2, 6, 2, inf), (2, 7, 2, -inf), (0, N - 1, R - 1, inf),
+                       (0, 8, 4, inf), (0, 8, 5, -inf), (3, 9, 1, inf), (3, 9, 6, inf), (3, 64, 7, -inf), (1, 64, 2, float("nan"))):
+        B[a, n, r] = v
+    if M > 8:
+        # s A x itself infinite or NaN, by finite and infinite values of B
+        index[3:6] = torch.tensor([3, 3, 0])
+        x[3, 5], x[4, 6] = inf, -inf
+        A[3, 1, 5], A[3, 6, 5], A[3, 1, 6] = 1.0, 1.0, 2.0
+        A[0, 5, 7], W[11, 5] = inf, 0.0
+    got = mm.linear_lora(*on(dev, x, W, A, B, index, scale), epilogue=epi).float().cpu()
+    want = ref.lora(x, W, A, B, index, scale).float()
+    assert want.isinf().any() and want.isnan().any()
+    if epi == "gelu_tanh":  # t times 0 is NaN for minus infinity, here as in linear
+        want = torch.where(want == -inf, float("nan"), want)
+    same_class(got, want)
+    if epi == "none":
+        fine = want.isfinite()
+        assert torch.equal(got[fine], want.bfloat16().float()[fine])
