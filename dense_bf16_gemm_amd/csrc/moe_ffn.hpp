@@ -294,6 +294,7 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_gate_up(MoeParams p) {
           p.tab->rows[i] = own.rows[i];
         }
         p.tab->tok[i] = own.tok[i];
+        p.tab->row[i] = own.row[i];
       }
     }
   }
@@ -366,6 +367,47 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_gate_up(MoeParams p) {
       }
       moe_leave(p, s + m, c0 + c, pick([&](auto& t) { return t.wt[s + m]; }) * swiglu(g, u));
     }
+  }
+}
+
+// Outputs (t, n) of a wave's lanes that came out NaN, from the definition: of the three parts of a value,
+// 8 bits or less leave some 0, and 0 times an infinity of W_down is NaN where the value times it is
+// infinite.  One output after another, by the whole wave, but those of tokens whose values are NaN, which
+// the first of them nearly always tells.
+__device__ __forceinline__ void moe_again(const MoeParams& p, int t, int n, float& v, int lane) {
+  bool odd = v != v;
+  for (int j = 0; odd && j < p.k; ++j) {
+    const int row = p.tab->row[t * p.k + j];
+    if (row < 0) break;
+    const float first = bf16_float(p.mid[(int64_t)row * 3 * p.I]);
+    odd = first == first;
+  }
+  for (uint64_t left = __ballot(odd); left; left &= left - 1) {
+    const int l = __builtin_ctzll(left);
+    const int lt = __builtin_amdgcn_readlane(t, l), ln = __builtin_amdgcn_readlane(n, l);
+    float sum = 0.f;
+    for (int j = 0; j < p.k; ++j) {
+      const int e = p.experts[lt * p.k + j];
+      if (e < 0) break;
+      const uint16_t* w = p.wd + ((int64_t)e * p.H + ln) * p.I;
+      const uint16_t* x = p.mid + (int64_t)p.tab->row[lt * p.k + j] * 3 * p.I;
+#pragma unroll 1
+      for (int i = lane; i < p.I && !__any(sum != sum); i += 64)
+        sum = __builtin_fmaf(bf16_float(x[i]) + bf16_float(x[p.I + i]) + bf16_float(x[2 * p.I + i]), bf16_float(w[i]), sum);
+    }
+    sum = wave_sum(sum);
+    if (lane == l) v = sum;
+  }
+}
+
+// The same of four columns from n on.
+__device__ __forceinline__ void moe_again(const MoeParams& p, int t, int n, f32x4& v, int lane) {
+  if (__ballot(v[0] + v[1] + v[2] + v[3] != v[0] + v[1] + v[2] + v[3]) == 0) return;
+#pragma unroll
+  for (int f = 0; f < 4; ++f) {
+    float u = v[f];
+    moe_again(p, t, n + f, u, lane);
+    v[f] = u;
   }
 }
 
@@ -505,35 +547,37 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_down(MoeParams p) {
   }
   __syncthreads();
   const int splits = gridDim.y;
-  auto place = [&](int i, int s) __attribute__((always_inline)) {
-    return ((int64_t)s * p.T + (i >> 4)) * p.H + n0 + (i & 15);
-  };
-  auto put = [&](int i, float v) __attribute__((always_inline)) {
-    p.out[place(i, 0)] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
-  };
-  for (int i = threadIdx.x; i < p.T * 16; i += kMoeWaves * 64) {
-    if (n0 + (i & 15) >= p.H) continue;
+  for (int first = wave * 64; first < p.T * 16; first += kMoeWaves * 64) {
+    const int i = first + lane, t = i >> 4, n = n0 + (i & 15);
+    const bool there = t < p.T && n < p.H;
     float v = 0.f;
+    if (there) {
 #pragma unroll
-    for (int w = 0; w < kMoeWaves; ++w) v += sums[w][i >> 4][i & 15];
-    if (splits == 1)
-      put(i, v);
-    else
-      p.part[place(i, blockIdx.y)] = v;
+      for (int w = 0; w < kMoeWaves; ++w) v += sums[w][t][i & 15];
+    }
+    if (splits == 1) {
+      moe_again(p, t, n, v, lane);
+      if (there) p.out[(int64_t)t * p.H + n] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+    } else if (there) {
+      p.part[((int64_t)blockIdx.y * p.T + t) * p.H + n] = v;
+    }
   }
 }
 
 // The output from the parts of several workgroups, added in order: four columns per thread.
 __global__ void __launch_bounds__(256) moe_join(MoeParams p) {
   const int64_t n = (int64_t)p.T * p.H, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (i >= n) return;
+  const int splits = i < n ? p.splits : 0;
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-  for (int s = 0; s < p.splits; ++s) {
+  for (int s = 0; s < splits; ++s) {
     const f32x4 u = *reinterpret_cast<const f32x4*>(p.part + s * n + i);
 #pragma unroll
     for (int f = 0; f < 4; ++f) v[f] += u[f];
   }
+  const int t = (int)(i / p.H), c = (int)(i - (int64_t)t * p.H);  // (H is a multiple of 8)
+  moe_again(p, t, c, v, threadIdx.x & 63);
+  if (i >= n) return;
   uint16_t* o = p.out + i;
   const uint32_t pk[2] = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
   __builtin_memcpy(o, pk, 8);
@@ -834,9 +878,8 @@ __global__ void __launch_bounds__(kMoeManyWaves * 64) moe_down_many(MoeParams p)
 // thread.
 __global__ void __launch_bounds__(256) moe_combine(MoeParams p) {
   const int t = blockIdx.y, n = (blockIdx.x * 256 + threadIdx.x) * 4;
-  if (n >= p.H) return;
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  for (int j = 0; j < p.k; ++j) {
+  for (int j = 0; j < (n < p.H ? p.k : 0); ++j) {
     const int row = p.tab->row[t * p.k + j];
     if (row < 0) break;
     for (int s = 0; s < p.slices; ++s) {
@@ -845,6 +888,8 @@ __global__ void __launch_bounds__(256) moe_combine(MoeParams p) {
       for (int f = 0; f < 4; ++f) v[f] += u[f];
     }
   }
+  moe_again(p, t, n, v, threadIdx.x & 63);
+  if (n >= p.H) return;
   const uint32_t pk[2] = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
   __builtin_memcpy(p.out + (int64_t)t * p.H + n, pk, 8);
 }
