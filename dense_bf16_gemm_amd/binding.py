@@ -152,7 +152,7 @@ def layer_norm_backward_workspace_size(rows: int, hidden: int) -> int:
 
 
 def linear_lora_workspace_size(M: int, N: int, K: int, rank: int, adapters: int) -> int:
-    """Bytes of workspace mm_linear_lora needs for this shape on the current device."""
+    """Bytes of workspace mm_linear_lora needs for this shape."""
     n = ctypes.c_int64(0)
     check(load().mm_linear_lora_workspace_size(M, N, K, rank, adapters, ctypes.byref(n)),
           "mm_linear_lora_workspace_size")

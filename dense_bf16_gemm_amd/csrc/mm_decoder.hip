@@ -403,35 +403,36 @@ struct LoraPlan {
 // these equal.
 Q8Plan lora_tile_plan(int64_t M, int64_t N, int64_t K) { return q8_plan(M, N, 2 * K, kQ8MaxChunks); }
 
-mm_status lora_plan(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, LoraPlan* p) {
+LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
+  LoraPlan p;
   // A x: enough workgroups to draw on every CU, K in slices of 512 or more.  Decode rows
   // may each have an adapter of their own; of prompts a block of rows has one or two.
   // Measured (us, prompts, blocks of 32 rows in 4 slices / of 64 in 256 workgroups): 2047 x 4104,
   // rank 32 10.8 / 13.0, 8192 x 8192, rank 16 42 / 44.
-  p->low_mb = M <= 16 ? 1 : M <= 32 || M > 64 ? 2 : 4;
-  p->low_rb = M > 64 && R > 16 ? 2 : 1;
-  p->turns = M <= 64 ? (int)std::min(M, L) : (int)std::min<int64_t>(2, L);
-  const int64_t at_once = cdiv(M, 16 * p->low_mb) * cdiv(R, 16 * p->low_rb) * (M <= 64 ? p->turns : 1);
+  p.low_mb = M <= 16 ? 1 : M <= 32 || M > 64 ? 2 : 4;
+  p.low_rb = M > 64 && R > 16 ? 2 : 1;
+  p.turns = M <= 64 ? (int)std::min(M, L) : (int)std::min<int64_t>(2, L);
+  const int64_t at_once = cdiv(M, 16 * p.low_mb) * cdiv(R, 16 * p.low_rb) * (M <= 64 ? p.turns : 1);
   const int64_t want = M <= 64 ? std::min<int64_t>(16, cdiv(512, at_once))
                                : std::max<int64_t>({1, std::min<int64_t>(4, 1024 / at_once), std::min<int64_t>(16, 256 / at_once)});
-  p->low_k = std::max<int64_t>(512, cdiv(cdiv(K, want), 64) * 64);
-  p->low_slices = cdiv(K, p->low_k);
-  p->low = round256(p->low_slices * M * R * 4);
-  p->v = round256(M * 3 * R * 2);
+  p.low_k = std::max<int64_t>(512, cdiv(cdiv(K, want), 64) * 64);
+  p.low_slices = cdiv(K, p.low_k);
+  p.low = round256(p.low_slices * M * R * 4);
+  p.v = round256(M * 3 * R * 2);
   if (M <= kLoraRows) {
-    p->mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-    const int64_t steps = cdiv(K, 64), most = 8 / p->mb;
-    p->slices = cdiv(steps, mmk::kLoraWaves * most);
-    p->spw = 2;
-    while (mmk::kLoraWaves * p->spw * p->slices < steps) p->spw *= 2;
-    p->finish = p->slices == 1 && p->mb < 4;
-    if (!p->finish) p->acc = round256(p->slices * M * N * 4);
-    return MM_OK;
+    p.mb = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+    const int64_t steps = cdiv(K, 64), most = 8 / p.mb;
+    p.slices = cdiv(steps, mmk::kLoraWaves * most);
+    p.spw = 2;
+    while (mmk::kLoraWaves * p.spw * p.slices < steps) p.spw *= 2;
+    p.finish = p.slices == 1 && p.mb < 4;
+    if (!p.finish) p.acc = round256(p.slices * M * N * 4);
+    return p;
   }
-  p->tiles = lora_tile_plan(M, N, K);
-  p->tile_rows = p->tiles.chunks == 1 ? round256(p->tiles.tiles_m * (int64_t)sizeof(mmk::LoraTileRows)) : 0;
-  if (p->tiles.chunks > 1) p->acc = round256(p->tiles.chunks * M * N * 4);
-  return MM_OK;
+  p.tiles = lora_tile_plan(M, N, K);
+  p.tile_rows = p.tiles.chunks == 1 ? round256(p.tiles.tiles_m * (int64_t)sizeof(mmk::LoraTileRows)) : 0;
+  if (p.tiles.chunks > 1) p.acc = round256(p.tiles.chunks * M * N * 4);
+  return p;
 }
 
 template <int FM, int FN, int SX, int SW>
@@ -465,6 +466,8 @@ mm_status check_lora(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
   if (K % 8 != 0) return fail(MM_ERR_MISALIGNED, "K must be a multiple of 8 elements");
   if (K >= (int64_t(1) << 22)) return fail(MM_ERR_UNSUPPORTED, "K must be below 2^22");
   if (N > (int64_t(1) << 27) - 16) return fail(MM_ERR_UNSUPPORTED, "N must be at most 2^27 - 16");
+  // (blocks of 32 rows of A x along a grid's y; without adapters' terms there is none)
+  if (M > 32 * kMaxGridY && K > 0 && R > 0 && L > 0) return fail(MM_ERR_UNSUPPORTED, "M must be at most 2^21 - 32");
   const int64_t room = int64_t(1) << 60;
   if (M > 0 && (N > room / M || K > room / M)) return fail(MM_ERR_UNSUPPORTED, "an operand spans 2^60 elements or more");
   if (L * R > 0 && (N > room / (L * R) || K > room / (L * R)))
@@ -981,9 +984,7 @@ mm_status mm_linear_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t
   *bytes = 0;
   mm_status s = check_lora(M, N, K, rank, adapters);
   if (s != MM_OK || M == 0 || N == 0 || K == 0 || rank == 0 || adapters == 0) return s;
-  LoraPlan plan;
-  if ((s = lora_plan(M, N, K, rank, adapters, &plan)) != MM_OK) return s;
-  *bytes = plan.bytes();
+  *bytes = lora_plan(M, N, K, rank, adapters).bytes();
   return MM_OK;
 }
 
@@ -1006,8 +1007,7 @@ mm_status mm_linear_lora(const void* x, const void* W, const void* A, const void
                      {index, M * 4},        {scale, adapters * 4}, {bias, bias ? N * 2 : 0}};
   const Span outs[] = {{out, M * N * 2}, {workspace, workspace_bytes}};
   if (any_overlap(in, outs)) return fail(MM_ERR_INVALID_VALUE, "out or the workspace overlaps an operand or each other");
-  LoraPlan plan;
-  if ((s = lora_plan(M, N, K, rank, adapters, &plan)) != MM_OK) return s;
+  const LoraPlan plan = lora_plan(M, N, K, rank, adapters);
   if (!workspace || workspace_bytes < plan.bytes())
     return fail(MM_ERR_INVALID_VALUE, "workspace smaller than mm_linear_lora_workspace_size reports");
   if (!aligned(workspace, 256)) return fail(MM_ERR_MISALIGNED, "workspace must be 256-byte aligned");
@@ -1035,8 +1035,8 @@ mm_status mm_linear_lora(const void* x, const void* W, const void* A, const void
   p.low_k = (int)plan.low_k;
   void* args[] = {&p};
   const int64_t row_blocks = cdiv(M, 16 * plan.low_mb);
-  if (row_blocks > kMaxGridY) return fail(MM_ERR_UNSUPPORTED, "M must be at most 2^21 - 32");
-  void* shrink_args[] = {&p, &plan.turns};
+  int turns = plan.turns;
+  void* shrink_args[] = {&p, &turns};
   s = launch(plan.low_mb == 1   ? fn(&mmk::lora_shrink<1, 1, false>)
              : plan.low_mb == 4 ? fn(&mmk::lora_shrink<4, 1, false>)
              : M <= 64          ? fn(&mmk::lora_shrink<2, 1, false>)

@@ -350,7 +350,7 @@ mm_status mm_layer_norm_backward(const void* dy, const void* h, const void* weig
  * definition's sum.  What an adapter
  * holds reaches the rows that name it and no others, and a row's bits do not depend on the other rows' adapters.
  * rank == 0, adapters == 0 or K == 0 is mm_linear.
- * The workspace (size from the function below, a device query; 256-byte aligned, any
+ * The workspace (size from the function below, host arithmetic only; 256-byte aligned, any
  * contents) is needed by every other call of M > 0 and N > 0; two calls in flight at
  * once must not share it.  Other arguments, the epilogue and errors as for mm_linear. */
 mm_status mm_linear_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t adapters,
