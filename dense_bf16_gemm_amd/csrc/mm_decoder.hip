@@ -449,12 +449,16 @@ const void* lora_tile_kernel(int kind, bool split) {
   return lora_tile_kernel<2, 1, 6, 6>(split);
 }
 
-template <bool FINISH>
-const void* lora_rows_kernel(int mb, int spw) {
-  if (mb == 2) return spw == 2 ? fn(&mmk::lora_rows<2, 2, FINISH>) : fn(&mmk::lora_rows<2, 4, FINISH>);
-  return spw == 2   ? fn(&mmk::lora_rows<1, 2, FINISH>)
-         : spw == 4 ? fn(&mmk::lora_rows<1, 4, FINISH>)
-                    : fn(&mmk::lora_rows<1, 8, FINISH>);
+const void* lora_rows_kernel(int mb, int spw, bool finish) {
+  // (K in slices: as many steps as the registers hold)
+  if (!finish)
+    return mb == 1   ? fn(&mmk::lora_rows<1, 8, false>)
+           : mb == 2 ? fn(&mmk::lora_rows<2, 4, false>)
+                     : fn(&mmk::lora_rows<4, 2, false>);
+  if (mb == 2) return spw == 2 ? fn(&mmk::lora_rows<2, 2, true>) : fn(&mmk::lora_rows<2, 4, true>);
+  return spw == 2   ? fn(&mmk::lora_rows<1, 2, true>)
+         : spw == 4 ? fn(&mmk::lora_rows<1, 4, true>)
+                    : fn(&mmk::lora_rows<1, 8, true>);
 }
 
 mm_status check_lora(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
@@ -1049,11 +1053,9 @@ mm_status mm_linear_lora(const void* x, const void* W, const void* A, const void
     int cus = 0;
     if ((s = device_cus(&cus)) != MM_OK) return s;
     const int64_t blocks = cdiv(N, 16), each = cdiv(blocks * plan.slices, cus);
-    const void* k = plan.mb == 4   ? fn(&mmk::lora_rows<4, 2, false>)
-                    : plan.finish ? lora_rows_kernel<true>(plan.mb, plan.spw)
-                                  : lora_rows_kernel<false>(plan.mb, plan.spw);
-    s = launch(k, dim3((unsigned)cdiv(blocks, each), (unsigned)plan.slices),
-               mmk::kLoraWaves * 64, args, stream, "linear_lora rows");
+    s = launch(lora_rows_kernel(plan.mb, plan.spw, plan.finish),
+               dim3((unsigned)cdiv(blocks, each), (unsigned)plan.slices), mmk::kLoraWaves * 64, args, stream,
+               "linear_lora rows");
     if (s != MM_OK || plan.finish) return s;
   } else {
     const Q8Plan& t = plan.tiles;
