@@ -509,10 +509,12 @@ const void* moe_gate_up_kernel(int64_t E) {
                     : fn(&mmk::moe_gate_up<8>);
 }
 
-// Blocks of 16 tokens to a group there: two where an expert has 12 on the average and the
-// registers hold two.  Measured (us a call, one / two): 64 tokens, 2 of 8 experts of 4096 x 4096
-// 204 / 167, 64, 6 of 32 of 4096 x 2048 327 / 311, but 64, 1 of 8 of 4096 x 4096 154 / 160.
-int moe_group_blocks(int64_t T, int64_t E, int64_t H, int64_t k) { return T * k >= 12 * E && H <= 4096 ? 2 : 1; }
+// Blocks of 16 tokens to a group there: two where an expert has 14 on the average and the
+// registers hold two.  Measured (us a call, one / two; tokens, choices of experts, H x I): 16 to an expert, 64, 2 of 8,
+// 4096 x 4096 203 / 178 and 64, 4 of 16, 2048 x 1024 80 / 66; 14.2, 64, 2 of 9, 4096 x 4096 220 / 198; 14, 64, 7 of 32, 2048 x 2048
+// 209 / 195; but 13.3, 40, 1 of 3, 4096 x 4096 75 / 79; 12, 64, 6 of 32, 2568 x 1544 202 / 215 (of 4096 x 2048 341 / 330); 8, 64,
+// 1 of 8, 4096 x 4096 160 / 171.
+int moe_group_blocks(int64_t T, int64_t E, int64_t H, int64_t k) { return T * k >= 14 * E && H <= 4096 ? 2 : 1; }
 
 // Workgroups that share 16 columns of the second layer: the number that spreads the
 // columns' workgroups most evenly over the CUs, a further one for a twentieth (256 CUs: 516 workgroups
@@ -528,13 +530,18 @@ int64_t moe_splits(int64_t H) {
   return best;
 }
 
-// Whether experts of several tokens go to the kernels that hold the tokens' rows: they cost a
-// launch's worth of rows per expert, which wide experts, or many tokens to one, are worth, and lose less
-// where rows start inside a line.  Measured (us a call, without / with): wide, 16 tokens, 2 of 8
-// experts of 4104 x 14344 616 / 550, 48, 4 of 32 of 4096 x 2048 313 / 295, but 64, 6 of 64 of
-// 4096 x 1536 446 / 467; many tokens, 64, 2 of 8 of 4096 x 4096 225 / 167, 64, 4 of 16 of 1024 x 2048
-// 76 / 71, but 48, 8 of 64 of 2048 x 1408 229 / 240; ragged, 61, 4 of 60 of 2056 x 1416
-// 263 / 248, but 64, 8 of 128 of 4104 x 776 548 / 576, and 64, 2 of 48 of 2056 x 1416 197 / 199.
+// Whether experts of several tokens go to the kernels that hold the tokens' rows.  These read the rows once per
+// run of columns, not for every 8 or 16 of them, but take H and I in pieces of 1024 or 2048 and a launch more.
+// Measured (us a call, without / with; tokens, choices of experts, H x I), at 4 tokens to an expert and more:
+//   wide: 16, 2 of 8, 4096 x 14336 505 / 456; 48, 4 of 32, 4096 x 2048 331 / 305; 64, 4 of 32, 8192 x 2048 621 / 592; but of
+//     8192 x 1024 322 / 349
+//   12 to an expert: 64, 6 of 32, 2048 x 2048 223 / 189; 64, 4 of 16, 4096 x 768 104 / 88; but 3 of 16 88 / 96
+//   rows that start inside a line: 61, 4 of 60, 2056 x 1416 273 / 251; 64, 4 of 32 186 / 152; 33, 4 of 16 103 / 85; 17, 4 of 16
+//     88 / 82; 64, 4 of 40, 2600 x 1800 322 / 265; 64, 6 of 64, 4104 x 1544 627 / 523; 64, 4 of 64, 4104 x 1032 392 / 370 and
+//     1416 x 2056 311 / 306; 20, 4 of 12, 2056 x 1032 64 / 60; but with I below 1024 64, 8 of 128, 4104 x 776 578 / 592
+//   others, about even: 61, 4 of 60, 2048 x 1408 221 / 219; 64, 4 of 40, 2560 x 1792 250 / 243; 32, 4 of 32, 2048 x 1408 124 / 130;
+//     64, 4 of 64, 4096 x 1024 325 / 337 and 4096 x 768 252 / 280
+// and below 4 to an expert: 64, 3 of 64, 2056 x 2056 365 / 382; 64, 3 of 64, 4096 x 2048 545 / 542; 32, 2 of 32, 4096 x 4096 491 / 513.
 bool moe_many(int64_t T, int64_t E, int64_t H, int64_t I, int64_t k) {
   if (T <= mmk::kMoeFew || H > 8192 || T * k < 4 * E) return false;
   if (H * I >= (int64_t(1) << 23)) return true;
