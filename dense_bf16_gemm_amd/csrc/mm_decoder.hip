@@ -408,7 +408,10 @@ LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
   // A x: enough workgroups to draw on every CU, K in slices of 512 or more.  Decode rows
   // may each have an adapter of their own; of prompts a block of rows has one or two.
   // Measured (us, prompts, blocks of 32 rows in 4 slices / of 64 in 256 workgroups): 2047 x 4104,
-  // rank 32 10.8 / 13.0, 8192 x 8192, rank 16 42 / 44.
+  // rank 32 10.8 / 13.0, 8192 x 8192, rank 16 42 / 44.  Slices of K (us a call of 256 columns, in 1 / 2 / 4 / 8, the rule's
+  // number): 300 x 4096, rank 16 24.9 / 23.2 / 22.4 / 22.5, 8; 700 x 12288 40.0 / 34.1 / 31.0 / 31.6, 11; 1500 x 4096 28.7 / 27.4 / 28.3 /
+  // 29.6, 5; 1500 x 8192, rank 128 64.7 / 52.8 / 55.3 / 61.2, 4; 6000 x 2048, rank 128 72.7 / 79.3 / 104 / 126, 1; 16000 x 4096, rank 16
+  // 74.5 / 72.8 / 81.2 / 89.1, 2; farthest from the best 1500 x 2048, rank 64 27.2 / 29.1 / 32.7 / 35.2, 4.
   p.low_mb = M <= 16 ? 1 : M <= 32 || M > 64 ? 2 : 4;
   p.low_rb = M > 64 && R > 16 ? 2 : 1;
   p.turns = M <= 64 ? (int)std::min(M, L) : (int)std::min<int64_t>(2, L);
