@@ -6,7 +6,8 @@ import torch
 
 import dense_bf16_gemm_amd as mm
 import layer_ref as ref
-from test_gpu_decoder import dev, gen, same_class  # noqa: F401 (dev is a fixture)
+from dense_bf16_gemm_amd import binding
+from test_gpu_decoder import dev, gen, guarded, same_class  # noqa: F401 (dev is a fixture)
 from test_gpu_linear_lora import choices, inputs, on
 
 pytestmark = pytest.mark.gpu
@@ -121,3 +122,43 @@ def test_linear_lora_infinities_of_B(dev, M, N, K, R, epi):  # noqa: F811
     if epi == "none":
         fine = want.isfinite()
         assert torch.equal(got[fine], want.bfloat16().float()[fine])
+
+
+TILE_ROWS = 9224  # bytes of a tile's table: a count, 256 adapters, 256 masks of 256 rows
+
+
+def up256(n):
+    return -(-n // 256) * 256
+
+
+# the last region of the workspace: sums of W x of slices of K (12 rows: two; 50, in one and in two; 90: tiles in five), or
+# the tables of tiles with K whole (of 128 rows by 128 columns, and by 64)
+@pytest.mark.parametrize("M,N,K,R,L,region", [(12, 300, 8264, 24, 4, 2 * 12 * 300 * 4), (50, 300, 2056, 24, 30, 2 * 50 * 300 * 4),
+                                              (33, 130, 520, 8, 3, 33 * 130 * 4), (90, 300, 1032, 24, 4, 5 * 90 * 300 * 4),
+                                              (200, 14336, 4096, 40, 150, "128"), (300, 2100, 264, 8, 300, "128")])
+def test_linear_lora_stays_inside_its_workspace(dev, M, N, K, R, L, region):  # noqa: F811
+    """The bytes behind the reported workspace stay as they were, its last region is written, and a
+    workspace full of NaN serves as well as any."""
+    args, _ = inputs(M, N, K, R, L, "mixed", 5)
+    d = on(dev, *args)
+    want = mm.linear_lora(*d)
+    nbytes = binding.linear_lora_workspace_size(M, N, K, R, L)
+    ws = torch.full((nbytes + 4096,), 0xFF, dtype=torch.uint8, device=dev)
+    out, intact = guarded((M, N), torch.bfloat16, dev)
+    binding.check(binding.load().mm_linear_lora(*(t.data_ptr() for t in d), None, out.data_ptr(), M, N, K, R, L, 0,
+                                                ws.data_ptr(), nbytes, torch.cuda.current_stream().cuda_stream),
+                  "mm_linear_lora")
+    assert torch.equal(out, want) and bool((ws[nbytes:] == 0xFF).all())
+    intact()
+    if region == "128":
+        tiles = -(-M // 128)
+        table = ws[nbytes - up256(tiles * TILE_ROWS):][:tiles * TILE_ROWS].reshape(tiles, TILE_ROWS)
+        for t in range(tiles):
+            mine = args[4][128 * t:128 * (t + 1)]
+            first = list(dict.fromkeys(a for a in mine.tolist() if a >= 0))  # in the order of their first rows
+            got = table[t].cpu()
+            assert int(got[:4].view(torch.int32)) == len(first)
+            assert got[4:4 + 4 * len(first)].view(torch.int32).tolist() == first
+    else:
+        sums = ws[nbytes - up256(region):nbytes][:region].view(torch.float32)
+        assert bool(sums.isfinite().all())
