@@ -61,19 +61,43 @@ __device__ __forceinline__ int lora_adapter(const LoraParams& p, int row) {
   return (unsigned)a < (unsigned)p.L ? a : -1;
 }
 
+// Bit h of a 16-bit half (of two in a word) set where the half is an infinity or a NaN: its exponent of ones
+// carries into the sign's place.
+__device__ __forceinline__ uint32_t odd_halves(uint32_t u) { return ((u & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
+// The terms of chunk c (8 ranks) of B v added to `sum`; v: the row's parts [3][stride].  ODD: those only whose
+// value of B is not finite.
+template <bool ODD>
+__device__ __forceinline__ float lora_terms(float sum, u32x4 w, const uint16_t* v, int stride, int c) {
+  u32x4 part[3];
+#pragma unroll
+  for (int h = 0; h < 3; ++h) part[h] = *reinterpret_cast<const u32x4*>(v + h * stride + 8 * c);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    auto at = [&](const u32x4& u) { return bf16_float((uint16_t)(u[j >> 1] >> (16 * (j & 1)))); };
+    if (ODD && !(odd_halves(w[j >> 1]) >> (16 * (j & 1)) & 0x8000u)) continue;
+    sum = __builtin_fmaf(at(part[0]) + at(part[1]) + at(part[2]), at(w), sum);
+  }
+  return sum;
+}
+
 // B v of row m and column n, term by term, for sums that came out NaN: of the three parts of a v, 8 bits
-// or less leave some 0, and 0 times an infinity of B is NaN where v times it is infinite.  v: the
-// row's parts [3][stride].
+// or less leave some 0, and 0 times an infinity of B is NaN where v times it is infinite.  CHUNKS: 8 ranks at a
+// time (lora_rows has no registers for them).
+template <bool CHUNKS>
 __device__ __forceinline__ float lora_term(const LoraParams& p, int m, int n, const uint16_t* v, int stride) {
   const uint16_t* b = p.B + ((int64_t)lora_adapter(p, m) * p.N + n) * p.R;
   float sum = 0.f;
+  if constexpr (CHUNKS) {
 #pragma unroll 1
-  for (int r = 0; r < p.R; ++r)
-    sum = __builtin_fmaf(bf16_float(v[r]) + bf16_float(v[stride + r]) + bf16_float(v[2 * stride + r]), bf16_float(b[r]), sum);
+    for (int c = 0; c < p.R >> 3 && sum == sum; ++c)
+      sum = lora_terms<false>(sum, *reinterpret_cast<const u32x4*>(b + 8 * c), v, stride, c);
+  } else {
+#pragma unroll 1
+    for (int r = 0; r < p.R && sum == sum; ++r)
+      sum = __builtin_fmaf(bf16_float(v[r]) + bf16_float(v[stride + r]) + bf16_float(v[2 * stride + r]), bf16_float(b[r]), sum);
+  }
   return sum;
-}
-__device__ __forceinline__ float lora_term(const LoraParams& p, int m, int n) {
-  return lora_term(p, m, n, p.v + (int64_t)m * 3 * p.R, p.R);
 }
 
 // Calls f(adapter, its lanes) for every different adapter >= 0 among a wave's lanes, in
@@ -441,7 +465,7 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_rows(LoraParams p) {
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
           const int m = 16 * b + 4 * lg + f;
-          if (d[f] != d[f]) d[f] = lora_term(p, m, n, reinterpret_cast<const uint16_t*>(v[m]), kLoraMaxRank);
+          if (d[f] != d[f]) d[f] = lora_term<false>(p, m, n, reinterpret_cast<const uint16_t*>(v[m]), kLoraMaxRank);
         }
       }
 #pragma unroll
@@ -526,7 +550,8 @@ __global__ void __launch_bounds__(256) lora_join(LoraParams p) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const int c = i >> 3, h = (i >> 2) & 1, f = i & 3, n = n0 + 32 * c + 8 * lg + 4 * h + f;
-    if (term[c][h][f] != term[c][h][f] && acc[c][h][f] == acc[c][h][f] && n < p.N) term[c][h][f] = lora_term(p, m, n);
+    if (term[c][h][f] != term[c][h][f] && acc[c][h][f] == acc[c][h][f] && n < p.N)
+      term[c][h][f] = lora_term<true>(p, m, n, p.v + (int64_t)m * 3 * p.R, p.R);
     acc[c][h][f] += term[c][h][f];
   }
   const bool has_bias = p.epi == EPI_BIAS || p.epi == EPI_BIAS_GELU;
@@ -631,7 +656,8 @@ __global__ void __launch_bounds__(512) lora_join_few(LoraParams p) {
     }
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
-      if (term[f] != term[f] && sum[f] == sum[f] && n + f < p.N) term[f] = lora_term(p, m, n + f);
+      if (term[f] != term[f] && sum[f] == sum[f] && n + f < p.N)
+        term[f] = lora_term<true>(p, m, n + f, p.v + (int64_t)m * 3 * p.R, p.R);
       sum[f] += term[f];
     }
     uint16_t o[4];
@@ -721,10 +747,11 @@ __device__ __forceinline__ void lora_mark(const LoraParams& p, int mb, int nb, i
     bool odd = false;
     float sum = 0.f;
 #pragma unroll 1
-    for (int r = 0; r < p.R; ++r) {
-      if ((b[r] & 0x7f80) != 0x7f80) continue;
+    for (int c = 0; c < p.R >> 3; ++c) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(b + 8 * c);
+      if (!(odd_halves(w[0]) | odd_halves(w[1]) | odd_halves(w[2]) | odd_halves(w[3]))) continue;
       odd = true;
-      sum += (bf16_float(v[r]) + bf16_float(v[p.R + r]) + bf16_float(v[2 * p.R + r])) * bf16_float(b[r]);
+      sum = lora_terms<true>(sum, w, v, p.R, c);
     }
     if (!odd) continue;
     uint16_t* o = p.out + (int64_t)m * p.N + n;
@@ -993,8 +1020,7 @@ __global__ void __launch_bounds__(256, SX * FM + SW * FN <= 10 ? 2 : 1) lora_til
       for (int b = 0; b < FN; ++b) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          // (an exponent of ones carries into the sign's place)
-          const uint32_t u = w[s][b].j[i >> 2][i & 3], odd = ((u & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+          const uint32_t u = w[s][b].j[i >> 2][i & 3], odd = odd_halves(u);
           const uint32_t value = (odd >> 15) * 0x7fffu;  // (all but the sign)
           w[s][b].j[i >> 2][i & 3] = (u & ~value) | (0x3f803f80u & value);
           any |= odd;

@@ -370,33 +370,52 @@ __global__ void __launch_bounds__(kMoeWaves * 64) moe_gate_up(MoeParams p) {
   }
 }
 
+// f(i, e, row) for the chunks i of 8 values of I that a lane has of every choice of token t.
+template <typename F>
+__device__ __forceinline__ void moe_chunks(const MoeParams& p, int t, int lane, F f) {
+  for (int j = 0; j < p.k; ++j) {
+    const int e = p.experts[t * p.k + j];
+    if (e < 0) break;
+    const int64_t row = (int64_t)p.tab->row[t * p.k + j] * 3 * p.I;
+#pragma unroll 1
+    for (int i = 8 * lane; i < p.I; i += 512) f(i, e, p.mid + row + i);
+  }
+}
+
 // Outputs (t, n) of a wave's lanes that came out NaN, from the definition: of the three parts of a value,
 // 8 bits or less leave some 0, and 0 times an infinity of W_down is NaN where the value times it is
-// infinite.  One output after another, by the whole wave, but those of tokens whose values are NaN, which
-// the first of them nearly always tells.
+// infinite.  Token after token by the whole wave, first whether a value is NaN (then the outputs are), else
+// one output after another.
 __device__ __forceinline__ void moe_again(const MoeParams& p, int t, int n, float& v, int lane) {
-  bool odd = v != v;
-  for (int j = 0; odd && j < p.k; ++j) {
-    const int row = p.tab->row[t * p.k + j];
-    if (row < 0) break;
-    const float first = bf16_float(p.mid[(int64_t)row * 3 * p.I]);
-    odd = first == first;
-  }
-  for (uint64_t left = __ballot(odd); left; left &= left - 1) {
-    const int l = __builtin_ctzll(left);
-    const int lt = __builtin_amdgcn_readlane(t, l), ln = __builtin_amdgcn_readlane(n, l);
-    float sum = 0.f;
-    for (int j = 0; j < p.k; ++j) {
-      const int e = p.experts[lt * p.k + j];
-      if (e < 0) break;
-      const uint16_t* w = p.wd + ((int64_t)e * p.H + ln) * p.I;
-      const uint16_t* x = p.mid + (int64_t)p.tab->row[lt * p.k + j] * 3 * p.I;
-#pragma unroll 1
-      for (int i = lane; i < p.I && !__any(sum != sum); i += 64)
-        sum = __builtin_fmaf(bf16_float(x[i]) + bf16_float(x[p.I + i]) + bf16_float(x[2 * p.I + i]), bf16_float(w[i]), sum);
+  uint64_t left = __ballot(v != v);
+  while (left) {
+    const int lt = __builtin_amdgcn_readlane(t, __builtin_ctzll(left));
+    uint64_t mine = left & __ballot(t == lt);
+    left &= ~mine;
+    bool nan = false;
+    moe_chunks(p, lt, lane, [&](int, int, const uint16_t* x) {
+      const u32x4 u = *reinterpret_cast<const u32x4*>(x);
+#pragma unroll
+      for (int f = 0; f < 8; ++f) nan |= (u[f >> 1] >> (16 * (f & 1)) & 0x7fffu) > 0x7f80u;
+    });
+    if (__any(nan)) continue;
+    for (; mine; mine &= mine - 1) {
+      const int l = __builtin_ctzll(mine), ln = __builtin_amdgcn_readlane(n, l);
+      float sum = 0.f;
+      moe_chunks(p, lt, lane, [&](int i, int e, const uint16_t* x) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(p.wd + ((int64_t)e * p.H + ln) * p.I + i);
+        u32x4 part[3];
+#pragma unroll
+        for (int h = 0; h < 3; ++h) part[h] = *reinterpret_cast<const u32x4*>(x + (int64_t)h * p.I);
+#pragma unroll
+        for (int f = 0; f < 8; ++f) {
+          auto at = [&](const u32x4& u) { return bf16_float((uint16_t)(u[f >> 1] >> (16 * (f & 1)))); };
+          sum = __builtin_fmaf(at(part[0]) + at(part[1]) + at(part[2]), at(w), sum);
+        }
+      });
+      sum = wave_sum(sum);
+      if (lane == l) v = sum;
     }
-    sum = wave_sum(sum);
-    if (lane == l) v = sum;
   }
 }
 
