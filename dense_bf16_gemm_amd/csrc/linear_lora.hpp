@@ -61,8 +61,8 @@ __device__ __forceinline__ int lora_adapter(const LoraParams& p, int row) {
   return (unsigned)a < (unsigned)p.L ? a : -1;
 }
 
-// Bit h of a 16-bit half (of two in a word) set where the half is an infinity or a NaN: its exponent of ones
-// carries into the sign's place.
+// The signs' places of a word's two bf16 set where the value is an infinity or a NaN: its exponent of ones
+// carries into that place.
 __device__ __forceinline__ uint32_t odd_halves(uint32_t u) { return ((u & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
 // The terms of chunk c (8 ranks) of B v added to `sum`; v: the row's parts [3][stride].  ODD: those only whose

@@ -215,7 +215,7 @@ __device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
 }
 
 // A float as the sum of three bf16: 8 bits of the significand each, cut, so that the sum is exact
-// (to 2^-133, the last bit of a bf16).  put(i, part i); what is not finite stays in part 0.
+// (but for what lies below 2^-126, where bf16 has fewer bits).  put(i, part i); what is not finite stays in part 0.
 template <typename F>
 __device__ __forceinline__ void split_bf16(float v, F put) {
   uint32_t b = __builtin_bit_cast(uint32_t, v);
