@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(256) lora_fold(LoraParams p, LoraTileRows* til
 // wave and added to the rows' sums after those of W x (so that no row's rounding depends on which wave that is,
 // and with it on other rows' adapters), and the output is written.  Else lora_join_few does both,
 // and v is left in memory for it.
-// Bound by reading W: 16 x 28672 x 8192 95 us (5.0 TB/s), 1 x 8192 x 8192 25 (5.4), 64 x 14336 x
+// Bound by reading W: 16 x 28672 x 8192 96 us (4.9 TB/s), 1 x 8192 x 8192 25 (5.4), 64 x 14336 x
 // 4096 26 (4.5, and 7 MB of parts).  With x read from L2 for every block the first took 150; with x
 // and W loaded in the MFMA's order (see to_fragments) 99, 25 and 32.
 template <int MB, int SPW, bool FINISH>
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(256) lora_join(LoraParams p) {
 }
 
 // The same for 16 MB rows by 64 columns, which may have as many adapters as there are rows: the eight waves share these, and meet in LDS, where each finishes some
-// blocks of 16 by 16.  64 x 14336, rank 64, 8 adapters 10.5 us, 24 MB (2.3 TB/s): one chain of
+// blocks of 16 by 16.  64 x 14336, rank 64, 8 adapters 11.5 us, 24 MB (2.1 TB/s): one chain of
 // index, v and B, sums and parts per workgroup.
 template <int MB>
 __global__ void __launch_bounds__(512) lora_join_few(LoraParams p) {
@@ -770,9 +770,9 @@ __device__ __forceinline__ void lora_mark(const LoraParams& p, int mb, int nb, i
 // tile's rows ceil(3 R / 64) of them, in which x stands for the rows' v, part after
 // part (rows of other adapters lie past the buffer's end: zeros), and W for the adapter's
 // B, three times.  So a tile of one adapter of rank 16 costs one super-step more.
-// Bound by issuing MFMAs and by L2: 8192^3, rank 16 850 us (1290 TFLOP/s; MFMAs in 75 % of a working
-// CU's cycles, 11 TB/s out of L2).  Where rows start inside a 128-byte line (K not a
-// multiple of 64) each copy touches two: 2047 x 3001 x 4104 75 us, 1.26 GB out of L2 (17 TB/s).
+// Bound by issuing MFMAs and by L2: 8192^3, rank 16 870 us (864 to 921 in 60 calls; 1270 TFLOP/s; MFMAs in 75 % of a
+// working CU's cycles, 10 TB/s out of L2).  Where rows start inside a 128-byte line (K not a
+// multiple of 64) each copy touches two: 2047 x 3001 x 4104, rank 32 82 us, 1.27 GB out of L2 (16 TB/s).
 // (A zero times an infinity or a NaN of B would be NaN in the other rows: 1 with their sign is taken
 // for them, whose product has the class of theirs where v is not finite, and the outputs of the adapter's rows in
 // those columns get their class at the end.)

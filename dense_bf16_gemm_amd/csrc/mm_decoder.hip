@@ -381,8 +381,8 @@ bool layer_norm_few(int64_t rows, int64_t hidden) { return rows <= kFewRows || h
 // Linear layer with an adapter per row
 // ----------------------------------------------------------------------------
 // At most this many rows take the rows' kernel (us a call, so / as tiles: 64 x 14336 x 4096, rank 64
-// 45.6 / 56.3, 33 x 3001 x 1032 16.2 / 20.2, 64 x 8192 x 8192 with as many adapters 53.8 / 56.5; the kernel's
-// registers hold no more).
+// 46.1 / 56.3, 64 x 4096 x 4096 21.4 / 27.6, 64 x 1024 x 14336 23.4 / 29.3, 33 x 3001 x 1032 17.8 / 21.8, 48 x 28672 x 8192 with as
+// many adapters 129 / 137, 64 x 8192 x 8192 54.4 / 56.9; the kernel's registers hold no more).
 constexpr int64_t kLoraRows = 64;
 
 int64_t round256(int64_t n) { return cdiv(n, 256) * 256; }
@@ -1090,17 +1090,17 @@ mm_status mm_linear_lora(const void* x, const void* W, const void* A, const void
                "linear_lora tiles");
     if (s != MM_OK || !split) return s;
   }
-  // Few rows: all to a workgroup where the columns' workgroups are enough, which reads B once
-  // (64 x 14336, rank 64, 8 adapters 10.4 us, 12.8 in blocks of 16 rows; but 49 x 1473 9.1, 4.6).
-  // More: 64 by 64 where that makes a workgroup for every CU (us, so / in blocks of 16 rows:
-  // 1000 x 1024 6.9 / 8.0, 512 x 4096 6.2 / 9.8; but 300 x 2000 11.1 / 8.2, 100 x 4096 10.4 / 6.2).
+  // 33 to 64 rows: all to a workgroup, which reads B once, where B is much of what is read and the columns make
+  // workgroups enough; else, and for fewer rows, blocks of 16 (us a call of 64 x N x 4096 with 8 adapters, so / in blocks of
+  // 16: rank 64, N 14336 46.6 / 49.2, 28672 78.8 / 81.2, 11008 40.6 / 41.5, 8192 32.4 / 30.6; rank 128, N 11008 49.4 / 54.4, 8192
+  // 42.2 / 39.2; rank 16, N 14336 42.2 / 42.3, 28672 72.0 / 69.8, and with 64 adapters 87.4 / 80.3).
+  // More rows: 64 by 64 where that makes a workgroup for every CU (us a call of K 4096, so / in blocks of 16 rows:
+  // 1000 x 1024 34.7 / 35.4, 512 x 4096 40.5 / 44.6; but 300 x 2000 37.5 / 34.9, 100 x 4096 34.8 / 30.8).
   const int64_t groups = cdiv(N, 64);
   if (!plan.mb && groups * cdiv(M, 64) >= 256)
     return launch(fn(&mmk::lora_join), dim3((unsigned)groups, (unsigned)cdiv(M, 64)), 256, args, stream, "linear_lora join");
-  const int jb = plan.mb && N >= 8192 ? plan.mb : 1;
-  return launch(jb == 1   ? fn(&mmk::lora_join_few<1>)
-                : jb == 2 ? fn(&mmk::lora_join_few<2>)
-                          : fn(&mmk::lora_join_few<4>),
+  const int jb = plan.mb == 4 && rank >= 64 && N >= 10240 ? 4 : 1;
+  return launch(jb == 1 ? fn(&mmk::lora_join_few<1>) : fn(&mmk::lora_join_few<4>),
                 dim3((unsigned)groups, (unsigned)cdiv(M, 16 * jb)), 512, args, stream, "linear_lora join");
 }
 

@@ -270,8 +270,8 @@ __device__ __forceinline__ void to_fragments(u32x4 (&v)[2], f32x4* slot, int lan
 // step's loads one step ahead, and meet in LDS, added in wave order.  Of an expert with
 // more tokens than a group of 16 takes the weights are read again for each group.
 // VPL > 0: up to eight tokens, each workgroup chooses their experts itself.
-// Bound by the weights: one token, 2 of 8 experts of 4096 x 14336, both layers 124 us (5.7 TB/s); 16
-// tokens, 8 of 128 of 4096 x 1536 551 (5.6).  With w and x loaded in the MFMA's order 134 and 601.
+// Bound by the weights: one token, 2 of 8 experts of 4096 x 14336, both layers 122 us (5.8 TB/s); 16
+// tokens, 8 of 128 of 4096 x 1536 540 (5.8).  With w and x loaded in the MFMA's order some 10 and 50 us more.
 template <int VPL>
 __global__ void __launch_bounds__(kMoeWaves * 64) moe_gate_up(MoeParams p) {
   constexpr bool kOwn = VPL > 0;
@@ -611,9 +611,9 @@ __global__ void __launch_bounds__(256) moe_join(MoeParams p) {
 // rows in registers until the group changes: the steps 16 i + w of 64 values, i < SPW.
 // Each step's weights are loaded one step ahead, across units; the waves' sums of a unit
 // meet in LDS (two sets in turn: one barrier per unit), and are added in wave order by
-// another wave for each unit.  61 tokens, 4 of 60 experts of 2056 x 1416: 248 us
-// in all (4.2 TB/s of rows that start inside a line); 64, 6 of 32 of 4096 x 2048 311 (5.2), 343 with x
-// out of L2.
+// another wave for each unit.  61 tokens, 4 of 60 experts of 2056 x 1416: 251 us
+// in all (4.1 TB/s of rows that start inside a line), 220 of 2048 x 1408 (4.7); 64, 6 of 32 of 4096 x 2048 331 (4.9), 398 with x
+// out of L2.  All SPW steps are run; those past the row's end multiply zeros (31 of 64 at 2056).
 
 constexpr int kMoeManyWaves = 16;
 

@@ -17,7 +17,7 @@ pytestmark = pytest.mark.gpu
 SHAPES = [(1, 70, 136, 8, 2), (9, 130, 1032, 24, 3), (16, 513, 4104, 16, 16), (30, 257, 2056, 72, 5), (32, 64, 4096, 256, 4),
           (5, 333, 8264, 40, 3), (32, 70, 4104, 16, 9), (64, 257, 1024, 32, 30), (50, 130, 2056, 136, 4), (65, 70, 200, 16, 3),
           (130, 515, 4104, 24, 3), (200, 517, 1032, 8, 12), (300, 300, 72, 72, 6), (513, 1030, 392, 64, 7), (2100, 2100, 328, 40, 8),
-          (700, 3000, 1032, 16, 5), (260, 140, 136, 256, 3)]
+          (700, 3000, 1032, 16, 5), (260, 140, 136, 256, 3), (64, 10248, 136, 72, 5), (40, 10241, 2056, 64, 30)]
 
 
 @pytest.mark.parametrize("M,N,K,R,L", SHAPES)
@@ -63,7 +63,7 @@ def test_linear_lora_keeps_all_bits_between_the_products(dev, M, N, K, R, L, how
 # rows in one launch, in slices of K, up to 64, tiles with K whole (256 columns to a tile: many) and in slices
 @pytest.mark.parametrize("M,N,K,R", [(5, 4096, 4096, 16), (16, 4096, 4096, 16), (16, 2048, 8192, 64), (30, 4096, 2056, 24),
                                      (32, 4096, 4096, 16), (12, 4096, 8264, 16), (32, 2048, 4104, 40), (40, 4096, 2056, 16),
-                                     (64, 4096, 4096, 16), (90, 4096, 1032, 24), (300, 2100, 1032, 16), (600, 4096, 520, 40)])
+                                     (64, 4096, 4096, 16), (90, 4096, 1032, 24), (300, 2100, 1032, 16), (600, 4096, 520, 40), (50, 10248, 520, 64)])
 def test_linear_lora_row_does_not_depend_on_other_rows_adapters(dev, M, N, K, R):  # noqa: F811
     """The bits of a row stay when other rows take other adapters, more, fewer or none.
 
@@ -92,7 +92,7 @@ def test_linear_lora_row_does_not_depend_on_other_rows_adapters(dev, M, N, K, R)
 
 @pytest.mark.parametrize("M,N,K,R", [(1, 70, 64, 8), (9, 130, 1032, 24), (30, 70, 392, 40), (12, 130, 8264, 16), (32, 70, 4104, 8),
                                      (50, 200, 520, 40), (90, 130, 1032, 16), (150, 130, 520, 16), (300, 2100, 264, 72),
-                                     (700, 3000, 1032, 16), (2100, 2100, 328, 8)])
+                                     (700, 3000, 1032, 16), (2100, 2100, 328, 8), (40, 10248, 264, 64)])
 @pytest.mark.parametrize("epi", ["none", "gelu_tanh"])
 def test_linear_lora_infinities_of_B(dev, M, N, K, R, epi):  # noqa: F811
     """An infinity in B gives its rows the infinity or NaN of the definition's sum, also where
