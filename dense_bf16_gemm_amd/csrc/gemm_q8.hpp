@@ -308,6 +308,7 @@ __device__ __forceinline__ void q8_block(const Q8Params& p, float (&v)[16], floa
 // 8 (i / 4 % 2) + 4 (i / 8 % 2) + i % 4, which makes those sums two runs of 8
 // columns, the runs of the two lanes of a row side by side.
 // SPLIT: the instance for a K cut into chunks.
+// (lora_tile has the same rings, waits and barriers: what is mended in one of them belongs into the other.)
 template <int FM, int FN, int SX, int SW, bool SPLIT>
 __global__ void __launch_bounds__(256, SX * FM + SW * FN <= 10 ? 2 : 1) gemm_q8_tile(Q8Params p) {
   constexpr int BM = 64 * FM, BN = 64 * FN, XS = BM * 128, WS = BN * 128;

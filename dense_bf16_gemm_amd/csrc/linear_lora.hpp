@@ -763,8 +763,8 @@ __device__ __forceinline__ void lora_mark(const LoraParams& p, int mb, int nb, i
 }
 
 // Tiles of 64 FM rows by 64 FN columns, in the manner of gemm_q8_tile (LDS rows of 128
-// bytes, here 64 k of bf16; the same rings, waits and layout; two v_mfma_f32_32x32x16_bf16 where that
-// has one instruction).
+// bytes, here 64 k of bf16; the same rings, waits and layout, and what is mended in one belongs into the other; two
+// v_mfma_f32_32x32x16_bf16 where that has one instruction).
 //
 // The adapters' terms are further super-steps of the same sums: for each adapter among a
 // tile's rows ceil(3 R / 64) of them, in which x stands for the rows' v, part after

@@ -374,7 +374,8 @@ mm_status mm_linear_lora(const void* x, const void* W, const void* A, const void
  * token's weights and output NaN.
  * tokens <= 64, n_experts <= 512, top_k <= 16 and <= n_experts; H and I multiples of 8, at
  * most 2^18.  Sums and what stands between the two layers are fp32, and an output that is not finite
- * has the class of the definition's sum.  tokens == 0 is a no-op.
+ * has the class of the definition's sum; the order of an output's sums, and with it its last bit, may depend
+ * on which experts the other tokens have.  tokens == 0 is a no-op.
  * The workspace (size from the function below, host arithmetic only; 256-byte
  * aligned, any contents) is needed by every other call; two calls in flight at once
  * must not share it. */
